@@ -40,10 +40,20 @@ class LoraStruct(ctypes.Structure):
                 ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
 
 
+class MuonTensorStruct(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("m_out", ctypes.c_void_p),
+                ("w", ctypes.c_void_p), ("w_out", ctypes.c_void_p), ("w16", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("E", ctypes.c_int), ("r", ctypes.c_int),
+                ("rank_major", ctypes.c_int), ("w_dtype", ctypes.c_int),
+                ("w16_dtype", ctypes.c_int), ("scale", ctypes.c_double)]
+
+
 _c_i64 = ctypes.c_int64
 _c_int = ctypes.c_int
 _c_vp = ctypes.c_void_p
 _c_size = ctypes.c_size_t
+_c_f32 = ctypes.c_float
+_c_f64 = ctypes.c_double
 
 _DGRAD_ARGS = [_c_vp, _c_int, _c_i64, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_i64,
                _c_i64, _c_i64, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_vp]
@@ -106,6 +116,24 @@ _SIGNATURES = {
     "moe_expert_forward_mxfp4": (_c_int, [_c_vp, _c_int, _c_vp, _c_i64, _c_int, _c_int, _c_int,
                                           _c_int, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
                                           _c_int, _c_vp, _c_size, _c_vp]),
+    "nbit_matvec": (_c_int, [_c_int, _c_vp, _c_int, _c_i64, _c_vp, _c_vp, _c_int, _c_vp, _c_int,
+                             _c_i64, _c_i64, _c_vp, _c_vp, _c_int, _c_vp]),
+    "block_norm_forward": (_c_int, [_c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp,
+                                    _c_int, _c_f32, _c_f32, _c_f32, _c_f32, _c_i64, _c_i64,
+                                    _c_vp, _c_vp, _c_int, _c_vp]),
+    "block_norm_backward_workspace": (_c_size, [_c_i64, _c_i64]),
+    "block_norm_backward": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_vp,
+                                     _c_int, _c_vp, _c_vp, _c_int, _c_f32, _c_f32, _c_f32,
+                                     _c_f32, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
+                                     _c_vp, _c_size, _c_vp]),
+    "lora_muon_step_workspace": (_c_size, [ctypes.POINTER(MuonTensorStruct), _c_int]),
+    "lora_muon_step": (_c_int, [ctypes.POINTER(MuonTensorStruct), _c_int, _c_f64, _c_f64, _c_int,
+                                _c_f64, _c_int, _c_f64, _c_f64, _c_f64, _c_f64, _c_vp, _c_size,
+                                _c_vp]),
+    "lora_orthogonalize_workspace": (_c_size, [_c_int, _c_int, _c_i64]),
+    "lora_orthogonalize": (_c_int, [_c_vp, _c_int, _c_int, _c_int, _c_i64, _c_int, _c_int, _c_f64,
+                                    _c_f64, _c_f64, _c_f64, _c_vp, _c_int, _c_vp, _c_size,
+                                    _c_vp]),
 }
 
 # storage modes of the nbit entry points (NF4MOE_QT_* in include/nf4moe.h)
@@ -502,3 +530,216 @@ def moe_forward_mxfp4(x, logits, k: int, gu_blocks, gu_scales, dn_blocks, dn_sca
         _ptr(gu_blocks), _ptr(gu_scales), _ptr(dn_blocks), _ptr(dn_scales), _ptr(y),
         _dtype_code(y.dtype), _ptr(workspace), workspace.numel(), _stream(x.device)))
     return y
+
+
+# ---- operators around the routed experts ------------------------------------
+
+MATVEC_TYPES = {"nf4": 0, "fp4": 1, "int4": 2, "mxfp4": 7}
+GATE_AXES = {"none": 0, "token": 1, "channel": 2}
+NS_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def _need(t, what: str, dev, shape=None, dtype=None):
+    """A contiguous GPU tensor on ``dev`` of the given shape and type: its pointer."""
+    if t.device != dev:
+        raise ValueError(f"{what} is on {t.device}, not on {dev}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    return _ptr(t)
+
+
+def _call(dev, fn, *args) -> None:
+    """One C call on the current stream of ``dev``, which is made the current
+    device for it if it is not."""
+    torch = _torch()
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        return
+    with torch.cuda.device(dev):
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def nbit_matvec(x, codes, scales, quant_type: str = "nf4", group: Optional[int] = None,
+                zeros=None, bias=None, out=None, out_dtype=None):
+    """A few rows times one 4-bit matrix: x [T, K] -> [T, N] (see nbit_matvec in
+    include/nf4moe.h).
+
+    ``codes`` is uint8 [N, K/2] and ``scales`` [N, K/group]: fp32 for ``"nf4"`` and
+    ``"fp4"`` (what ``quantize`` returns, one expert's slice of it), fp32 / bf16 /
+    fp16 for ``"int4"`` (``zeros`` uint8 [N, K/group], None: 8), e8m0 bytes for
+    ``"mxfp4"``.  ``bias`` is fp32 [N].  ``group`` defaults to 64 (32 for mxfp4).
+    """
+    torch = _torch()
+    if quant_type not in MATVEC_TYPES:
+        raise ValueError(f"unknown quant_type {quant_type!r} (one of {sorted(MATVEC_TYPES)})")
+    if x.dim() != 2 or codes.dim() != 2:
+        raise ValueError("x must be [T, K] and codes [N, K/2]")
+    dev = x.device
+    T, K = x.shape
+    N = codes.shape[0]
+    if group is None:
+        group = 32 if quant_type == "mxfp4" else 64
+    if group < 1 or K % group:
+        raise ValueError(f"K={K} is not a multiple of the group {group}")
+    groups = (N, K // group)
+    mx = quant_type == "mxfp4"
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype or x.dtype, device=dev)
+    _call(dev, load().nbit_matvec, MATVEC_TYPES[quant_type], _ptr(x), _dtype_code(x.dtype), T,
+          _need(codes, "codes", dev, (N, K // 2), torch.uint8),
+          _need(scales, "scales", dev, groups, torch.uint8 if mx else None),
+          F32 if mx else _dtype_code(scales.dtype),
+          None if zeros is None else _need(zeros, "zeros", dev, groups, torch.uint8), group, N, K,
+          None if bias is None else _need(bias, "bias", dev, (N,), torch.float32),
+          _need(out, "out", dev, (T, N)), _dtype_code(out.dtype))
+    return out
+
+
+def _norm_args(res, y, gate, gate_axis, w_pre, w_post, w_offset, alpha, beta, eps):
+    """The arguments both directions of block_norm share, checked; from y to H."""
+    torch = _torch()
+    if res.dim() != 2:
+        raise ValueError("the residual must be [T, H]")
+    dev = res.device
+    T, H = res.shape
+    axis = "none" if gate is None else gate_axis
+    if axis not in GATE_AXES:
+        raise ValueError(f"unknown gate_axis {gate_axis!r} (one of {sorted(GATE_AXES)})")
+    w = w_pre if w_pre is not None else w_post
+    wt = w.dtype if w is not None else torch.float32
+    return (None if y is None else _need(y, "y", dev, (T, H)),
+            F32 if y is None else _dtype_code(y.dtype),
+            None if gate is None else _need(gate, "gate", dev, (H if axis == "channel" else T,),
+                                            torch.float32),
+            GATE_AXES[axis],
+            None if w_pre is None else _need(w_pre, "w_pre", dev, (H,), wt),
+            None if w_post is None else _need(w_post, "w_post", dev, (H,), wt),
+            _dtype_code(wt), w_offset, alpha, beta, eps, T, H)
+
+
+def block_norm(residual, y=None, w_pre=None, w_post=None, gate=None, gate_axis: str = "token",
+               alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6, w_offset: float = 0.0,
+               r_out=None, h=None, h_dtype=None):
+    """The norms after and before a block with its gate and residual scale (see
+    block_norm_forward in include/nf4moe.h): returns ``(r, h)`` with
+    r = beta * residual + alpha * gate * norm(y; w_post), h = norm(r; w_pre).
+
+    Without ``y``, r is ``residual`` itself; without ``w_pre``, h is None; without
+    ``w_post``, y is added as it is.  ``gate`` is fp32 [T] (``gate_axis="token"``) or
+    [H] (``"channel"``).  ``r_out`` may be ``residual``.
+    """
+    torch = _torch()
+    dev = residual.device
+    args = _norm_args(residual, y, gate, gate_axis, w_pre, w_post, w_offset, alpha, beta, eps)
+    if y is not None and r_out is None:
+        r_out = torch.empty_like(residual)
+    if w_pre is not None and h is None:
+        h = torch.empty(residual.shape, dtype=h_dtype or residual.dtype, device=dev)
+    _call(dev, load().block_norm_forward, _ptr(residual), _dtype_code(residual.dtype), *args,
+          None if r_out is None else _need(r_out, "r_out", dev, residual.shape, residual.dtype),
+          None if h is None else _need(h, "h", dev, residual.shape),
+          F32 if h is None else _dtype_code(h.dtype))
+    return (residual if y is None else r_out), h
+
+
+def block_norm_backward(dh, d_r_out, r, y=None, w_pre=None, w_post=None, gate=None,
+                        gate_axis: str = "token", alpha: float = 1.0, beta: float = 1.0,
+                        eps: float = 1e-6, w_offset: float = 0.0, workspace=None):
+    """Gradients of ``block_norm`` (see block_norm_backward in include/nf4moe.h) from
+    those of h and r (either may be None where the other is given); ``r`` is what
+    the forward returned.
+
+    Returns a dict with ``dresidual`` and, where their inputs are given, ``dy``,
+    ``dgate``, ``dw_pre`` and ``dw_post`` (the last three fp32).
+    """
+    torch = _torch()
+    dev = r.device
+    args = _norm_args(r, y, gate, gate_axis, w_pre, w_post, w_offset, alpha, beta, eps)
+    T, H = r.shape
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = dict(dresidual=torch.empty_like(r))
+    if y is not None:
+        out["dy"] = torch.empty_like(y)
+    if gate is not None:
+        out["dgate"] = torch.empty(gate.shape, **f32)
+    if w_pre is not None:
+        out["dw_pre"] = torch.empty(H, **f32)
+    if w_post is not None:
+        out["dw_post"] = torch.empty(H, **f32)
+    if workspace is None:
+        workspace = torch.empty(max(load().block_norm_backward_workspace(T, H), 1),
+                                dtype=torch.uint8, device=dev)
+    ptr = lambda k: out[k].data_ptr() if k in out else None  # noqa: E731
+    _call(dev, load().block_norm_backward,
+          None if dh is None else _need(dh, "dh", dev, r.shape),
+          F32 if dh is None else _dtype_code(dh.dtype),
+          None if d_r_out is None else _need(d_r_out, "d_r_out", dev, r.shape, r.dtype),
+          _ptr(r), _dtype_code(r.dtype), *args, ptr("dresidual"), ptr("dy"), ptr("dgate"),
+          ptr("dw_pre"), ptr("dw_post"), _need(workspace, "workspace", dev), workspace.numel())
+    return out
+
+
+def lora_orthogonalize(u, rank_major: bool = True, steps: int = 5, coeffs=NS_COEFFS,
+                       eps: float = 1e-7, out=None, out_dtype=None, workspace=None):
+    """Newton-Schulz orthogonalisation of per-expert factors u [E, r, n] (or
+    [E, n, r] with ``rank_major=False``); see lora_orthogonalize in include/nf4moe.h."""
+    torch = _torch()
+    if u.dim() != 3:
+        raise ValueError("u must be [E, r, n] or [E, n, r]")
+    dev = u.device
+    E, r, n = u.shape if rank_major else (u.shape[0], u.shape[2], u.shape[1])
+    if out is None:
+        out = torch.empty(u.shape, dtype=out_dtype or u.dtype, device=dev)
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(max(lib.lora_orthogonalize_workspace(E, r, n), 1),
+                                dtype=torch.uint8, device=dev)
+    _call(dev, lib.lora_orthogonalize, _ptr(u), _dtype_code(u.dtype), E, r, n,
+          int(bool(rank_major)), steps, *coeffs, eps, _need(out, "out", dev, u.shape),
+          _dtype_code(out.dtype), _need(workspace, "workspace", dev), workspace.numel())
+    return out
+
+
+def lora_muon_step(tensors, lr: float, momentum: float = 0.95, nesterov: bool = True,
+                   weight_decay: float = 0.0, steps: int = 5, coeffs=NS_COEFFS,
+                   eps: float = 1e-7, workspace=None) -> None:
+    """One optimiser step of up to eight adapter tensors (see lora_muon_step in
+    include/nf4moe.h), in place unless other outputs are named.
+
+    Each of ``tensors`` is a dict with ``grad`` and ``momentum`` (fp32), ``w`` (fp32,
+    bf16 or fp16), all [E, r, n] (``rank_major=True``, the A factors) or [E, n, r]
+    (False, the B factors), and optionally ``scale`` (of the update, default 1),
+    ``momentum_out``, ``w_out`` and ``w16`` (a bf16 or fp16 copy of the new fp32 w).
+    """
+    torch = _torch()
+    if not 1 <= len(tensors) <= 8:
+        raise ValueError(f"1 to 8 tensors are taken, got {len(tensors)}")
+    arr = (MuonTensorStruct * len(tensors))()
+    dev = tensors[0]["grad"].device
+    for s, t in zip(arr, tensors):
+        g, w, rank_major = t["grad"], t["w"], bool(t["rank_major"])
+        if g.dim() != 3:
+            raise ValueError("grad must be [E, r, n] or [E, n, r]")
+        shape, m = g.shape, t["momentum"]
+        w16 = t.get("w16")
+        m_out, w_out = t.get("momentum_out"), t.get("w_out")
+        s.grad = _need(g, "grad", dev, shape, torch.float32)
+        s.m = _need(m, "momentum", dev, shape, torch.float32)
+        s.m_out = s.m if m_out is None else _need(m_out, "momentum_out", dev, shape, torch.float32)
+        s.w = _need(w, "w", dev, shape)
+        s.w_out = s.w if w_out is None else _need(w_out, "w_out", dev, shape, w.dtype)
+        s.w_dtype = _dtype_code(w.dtype)
+        if w16 is not None:
+            s.w16 = _need(w16, "w16", dev, shape)
+            s.w16_dtype = _dtype_code(w16.dtype)
+        s.E, s.r, s.n = shape if rank_major else (shape[0], shape[2], shape[1])
+        s.rank_major = int(rank_major)
+        s.scale = t.get("scale", 1.0)
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(max(lib.lora_muon_step_workspace(arr, len(arr)), 1),
+                                dtype=torch.uint8, device=dev)
+    _call(dev, lib.lora_muon_step, arr, len(arr), lr, momentum, int(bool(nesterov)), weight_decay,
+          steps, *coeffs, eps, _need(workspace, "workspace", dev), workspace.numel())

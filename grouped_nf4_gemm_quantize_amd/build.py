@@ -26,7 +26,7 @@ LIB = os.path.join(PKG, "libnf4moe.so")
 ARCH = "gfx950"
 
 SOURCES = ["quantize.hip", "route.hip", "gemm.hip", "gemm16.hip", "dgrad.hip", "lora.hip", "gemv.hip",
-           "noalloc.hip", "abi.cpp"]
+           "noalloc.hip", "matvec.hip", "blocknorm.hip", "muon.hip", "abi.cpp"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

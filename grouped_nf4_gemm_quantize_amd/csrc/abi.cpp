@@ -1203,4 +1203,370 @@ int moe_expert_forward_mxfp4(const void* x, int x_dtype, const float* router_log
                       workspace, ws_bytes, stream);
 }
 
+// ---- 4-bit matrix-vector products ----------------------------------------
+
+static bool is_float_dtype(int d) { return d == NF4MOE_F32 || d == NF4MOE_BF16 || d == NF4MOE_F16; }
+static size_t dtype_bytes(int d) { return d == NF4MOE_F32 ? 4 : 2; }
+
+int nbit_matvec(int quant_type, const void* x, int x_dtype, int64_t T, const uint8_t* codes,
+                const void* scales, int scale_dtype, const uint8_t* zeros, int group,
+                int64_t N, int64_t K, const float* bias, void* y, int y_dtype, void* stream) {
+  if (quant_type != kMvNF4 && quant_type != kMvFP4 && quant_type != kMvINT4 &&
+      quant_type != kMvMXFP4)
+    return fail(NF4MOE_EINVAL, "storage mode %d: the matrix-vector product takes nf4, fp4, int4 "
+                               "or mxfp4", quant_type);
+  if (x == nullptr || codes == nullptr || scales == nullptr || y == nullptr)
+    return fail(NF4MOE_EINVAL, "x, codes, scales and y must be non-null");
+  if (T < 1 || N < 1 || K < 1)
+    return fail(NF4MOE_EINVAL, "T, N, K must be positive (got %lld, %lld, %lld)", (long long)T,
+                (long long)N, (long long)K);
+  if (x_dtype != NF4MOE_F16 && x_dtype != NF4MOE_BF16)
+    return fail(NF4MOE_EDTYPE, "x_dtype=%d must be F16 or BF16", x_dtype);
+  if (!is_float_dtype(y_dtype)) return fail(NF4MOE_EDTYPE, "y_dtype=%d is unknown", y_dtype);
+  if (quant_type == kMvINT4) {
+    if (group != 32 && group != 64 && group != 128)
+      return fail(NF4MOE_EBLOCK, "int4: group=%d must be 32, 64 or 128", group);
+    if (!is_float_dtype(scale_dtype))
+      return fail(NF4MOE_EDTYPE, "scale_dtype=%d is unknown", scale_dtype);
+  } else {
+    const int want = quant_type == kMvMXFP4 ? 32 : NF4MOE_BLOCKSIZE;
+    if (group != want)
+      return fail(NF4MOE_EBLOCK, "group=%d: this storage mode has groups of %d", group, want);
+    if (zeros != nullptr) return fail(NF4MOE_EINVAL, "zeros are for int4 only");
+    if (quant_type != kMvMXFP4 && scale_dtype != NF4MOE_F32)
+      return fail(NF4MOE_EDTYPE, "scale_dtype=%d: nf4 and fp4 have F32 scales", scale_dtype);
+  }
+  if (K % group)
+    return fail(NF4MOE_ESHAPE, "K=%lld is not a multiple of the group %d", (long long)K, group);
+  if (T > NF4MOE_MATVEC_MAX_T || N > (int64_t)INT32_MAX - 64 || K > ((int64_t)1 << 30))
+    return fail(NF4MOE_EOVERFLOW, "T=%lld, N=%lld or K=%lld is too large", (long long)T,
+                (long long)N, (long long)K);
+  const size_t sb = quant_type == kMvMXFP4 ? 1 : dtype_bytes(scale_dtype);
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, sb) || !aligned(bias, 4) ||
+      !aligned(y, dtype_bytes(y_dtype)))
+    return fail(NF4MOE_EINVAL, "misaligned buffer (x and codes need 16 bytes; scales, bias and y "
+                               "their element)");
+  int cus = 0;
+  int st = cu_count(&cus);
+  if (st != NF4MOE_OK) return st;
+  MatvecArgs a{};
+  a.x = x;
+  a.codes = codes;
+  a.scales = scales;
+  a.zeros = zeros;
+  a.bias = bias;
+  a.y = y;
+  a.T = T;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.x_bf16 = x_dtype == NF4MOE_BF16;
+  a.scale_dtype = scale_dtype;
+  a.group = group;
+  a.qt = quant_type;
+  a.y_dtype = y_dtype;
+  hipError_t err = launch_matvec(a, cus, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "matrix-vector launch");
+  return ok();
+}
+
+// ---- norms around a block --------------------------------------------------
+
+static_assert(NF4MOE_MAX_NORM_H <= 2 * 8 * 1024, "two vectors of eight columns a thread");
+
+// What both directions share: sizes, types, and which inputs go together.
+static int block_norm_check(const void* y, int res_dtype, int y_dtype, int h_dtype,
+                            const float* gate, int gate_axis, const void* w_pre,
+                            const void* w_post, int w_dtype, float w_offset, float alpha,
+                            float beta, float eps, int64_t T, int64_t H) {
+  if (T < 1 || H < 1)
+    return fail(NF4MOE_EINVAL, "T=%lld and H=%lld must be positive", (long long)T, (long long)H);
+  if (H % 8 || H > NF4MOE_MAX_NORM_H)
+    return fail(NF4MOE_ESHAPE, "H=%lld must be a multiple of 8 and at most %d", (long long)H,
+                NF4MOE_MAX_NORM_H);
+  if (T > (int64_t)INT32_MAX)
+    return fail(NF4MOE_EOVERFLOW, "T=%lld rows are too many", (long long)T);
+  if (y == nullptr && w_pre == nullptr)
+    return fail(NF4MOE_EINVAL, "nothing to do: y and w_pre are both NULL");
+  if (y == nullptr && (w_post != nullptr || gate != nullptr || gate_axis != NF4MOE_GATE_NONE))
+    return fail(NF4MOE_EINVAL, "w_post and the gate act on y, which is NULL");
+  if (y == nullptr && beta != 1.0f)
+    return fail(NF4MOE_EINVAL, "without y the residual is not scaled: beta must be 1");
+  if (gate_axis != NF4MOE_GATE_NONE && gate_axis != NF4MOE_GATE_TOKEN &&
+      gate_axis != NF4MOE_GATE_CHANNEL)
+    return fail(NF4MOE_EINVAL, "gate_axis=%d is unknown", gate_axis);
+  if ((gate != nullptr) != (gate_axis != NF4MOE_GATE_NONE))
+    return fail(NF4MOE_EINVAL, "a gate needs its axis and an axis its gate");
+  if (!is_float_dtype(res_dtype) || (y != nullptr && !is_float_dtype(y_dtype)) ||
+      (w_pre != nullptr && !is_float_dtype(h_dtype)) ||
+      ((w_pre != nullptr || w_post != nullptr) && !is_float_dtype(w_dtype)))
+    return fail(NF4MOE_EDTYPE, "unknown dtype (residual %d, y %d, h %d, weights %d)", res_dtype,
+                y_dtype, h_dtype, w_dtype);
+  if (!std::isfinite(alpha) || !std::isfinite(beta) || !std::isfinite(w_offset) ||
+      !std::isfinite(eps) || eps < 0.0f)
+    return fail(NF4MOE_EINVAL, "alpha, beta and w_offset must be finite and eps finite and "
+                               "not negative");
+  return NF4MOE_OK;
+}
+
+int block_norm_forward(const void* residual, int res_dtype, const void* y, int y_dtype,
+                       const float* gate, int gate_axis, const void* w_pre, const void* w_post,
+                       int w_dtype, float w_offset, float alpha, float beta, float eps,
+                       int64_t T, int64_t H, void* r_out, void* h, int h_dtype, void* stream) {
+  if (residual == nullptr) return fail(NF4MOE_EINVAL, "residual must be non-null");
+  int st = block_norm_check(y, res_dtype, y_dtype, h_dtype, gate, gate_axis, w_pre, w_post,
+                            w_dtype, w_offset, alpha, beta, eps, T, H);
+  if (st != NF4MOE_OK) return st;
+  if ((y != nullptr) != (r_out != nullptr))
+    return fail(NF4MOE_EINVAL, "r_out is written exactly if y is given");
+  if ((w_pre != nullptr) != (h != nullptr))
+    return fail(NF4MOE_EINVAL, "h is written exactly if w_pre is given");
+  if (!aligned(residual, 16) || !aligned(y, 16) || !aligned(w_pre, 16) || !aligned(w_post, 16) ||
+      !aligned(r_out, 16) || !aligned(h, 16) || !aligned(gate, 4))
+    return fail(NF4MOE_EINVAL, "misaligned buffer (16 bytes; gate 4)");
+  int cus = 0;
+  st = cu_count(&cus);
+  if (st != NF4MOE_OK) return st;
+  BlockNormArgs a{};
+  a.residual = residual;
+  a.y = y;
+  a.gate = gate;
+  a.w_pre = w_pre;
+  a.w_post = w_post;
+  a.r_out = r_out;
+  a.h = h;
+  a.T = T;
+  a.H = (int)H;
+  a.res_dtype = res_dtype;
+  a.y_dtype = y_dtype;
+  a.h_dtype = h_dtype;
+  a.w_dtype = w_dtype;
+  a.gate_axis = gate_axis;
+  a.w_offset = w_offset;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.eps = eps;
+  hipError_t err = launch_block_norm(a, cus, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "block norm launch");
+  return ok();
+}
+
+size_t block_norm_backward_workspace(int64_t T, int64_t H) {
+  if (T < 1 || H < 1 || H % 8 || H > NF4MOE_MAX_NORM_H || T > (int64_t)INT32_MAX) return 0;
+  return align_up((size_t)3 * block_norm_groups(T, (int)H) * H * 4, 256);
+}
+
+int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const void* r,
+                        int res_dtype, const void* y, int y_dtype, const float* gate,
+                        int gate_axis, const void* w_pre, const void* w_post, int w_dtype,
+                        float w_offset, float alpha, float beta, float eps, int64_t T, int64_t H,
+                        void* dresidual, void* dy, float* dgate, float* dw_pre, float* dw_post,
+                        void* workspace, size_t ws_bytes, void* stream) {
+  if (r == nullptr || dresidual == nullptr)
+    return fail(NF4MOE_EINVAL, "r and dresidual must be non-null");
+  int st = block_norm_check(y, res_dtype, y_dtype, h_dtype, gate, gate_axis, w_pre, w_post,
+                            w_dtype, w_offset, alpha, beta, eps, T, H);
+  if (st != NF4MOE_OK) return st;
+  if (dh == nullptr && d_r_out == nullptr)
+    return fail(NF4MOE_EINVAL, "dh and d_r_out are both NULL: no gradient comes in");
+  if ((dh != nullptr) != (w_pre != nullptr))
+    return fail(NF4MOE_EINVAL, "dh is given exactly if w_pre is");
+  if ((y != nullptr) != (dy != nullptr) || (gate != nullptr) != (dgate != nullptr) ||
+      (w_pre != nullptr) != (dw_pre != nullptr) || (w_post != nullptr) != (dw_post != nullptr))
+    return fail(NF4MOE_EINVAL, "dy, dgate, dw_pre and dw_post are written exactly where y, gate, "
+                               "w_pre and w_post are given");
+  if (!aligned(dh, 16) || !aligned(d_r_out, 16) || !aligned(r, 16) || !aligned(y, 16) ||
+      !aligned(w_pre, 16) || !aligned(w_post, 16) || !aligned(dresidual, 16) || !aligned(dy, 16) ||
+      !aligned(gate, 4) || !aligned(dgate, 4) || !aligned(dw_pre, 4) || !aligned(dw_post, 4))
+    return fail(NF4MOE_EINVAL, "misaligned buffer (16 bytes; gate, dgate, dw_pre and dw_post 4)");
+  const size_t need = block_norm_backward_workspace(T, H);
+  if (workspace == nullptr || ws_bytes < need)
+    return fail(NF4MOE_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                workspace ? ws_bytes : (size_t)0);
+  if (!aligned(workspace, 256)) return fail(NF4MOE_EINVAL, "workspace must be 256-byte aligned");
+  BlockNormArgs a{};
+  a.residual = r;
+  a.y = y;
+  a.gate = gate;
+  a.w_pre = w_pre;
+  a.w_post = w_post;
+  a.dh = dh;
+  a.d_r_out = d_r_out;
+  a.r_out = dresidual;
+  a.h = dy;
+  a.dgate = dgate;
+  a.dw_pre = dw_pre;
+  a.dw_post = dw_post;
+  a.part = (float*)workspace;
+  a.T = T;
+  a.H = (int)H;
+  a.res_dtype = res_dtype;
+  a.y_dtype = y_dtype;
+  a.h_dtype = h_dtype;
+  a.w_dtype = w_dtype;
+  a.gate_axis = gate_axis;
+  a.w_offset = w_offset;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.eps = eps;
+  hipError_t err = launch_block_norm_bwd(a, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "block norm backward launch");
+  return ok();
+}
+
+// ---- adapter update ----------------------------------------------------------
+
+static_assert(kMuonMaxTensors == NF4MOE_MAX_MUON_TENSORS, "one call's tensors");
+
+static int muon_shape_check(int E, int r, int64_t n) {
+  if (E < 1 || n < 1)
+    return fail(NF4MOE_EINVAL, "E=%d and n=%lld must be positive", E, (long long)n);
+  if (r < 1 || r > NF4MOE_MAX_LORA_R)
+    return fail(NF4MOE_EINVAL, "rank r=%d outside [1, %d]", r, NF4MOE_MAX_LORA_R);
+  // each tensor below 2^40 elements; a call's threads fit the 32-bit grid
+  if (n > ((int64_t)1 << 40) / r / E || (int64_t)muon_chunks(n, r) * E > kMuonMaxBlocks)
+    return fail(NF4MOE_EOVERFLOW, "E=%d, r=%d, n=%lld is too large", E, r, (long long)n);
+  return NF4MOE_OK;
+}
+
+static int muon_scalar_check(int ns_steps, double a, double b, double c, double ns_eps) {
+  if (ns_steps < 1 || ns_steps > 16)
+    return fail(NF4MOE_EINVAL, "ns_steps=%d outside [1, 16]", ns_steps);
+  if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || !std::isfinite(ns_eps) ||
+      ns_eps < 0)
+    return fail(NF4MOE_EINVAL, "a, b and c must be finite and ns_eps finite and not negative");
+  return NF4MOE_OK;
+}
+
+static size_t muon_gram_bytes(int E, int r, int64_t n) {
+  return align_up((size_t)E * muon_chunks(n, r) * r * r * 8, 256);
+}
+
+// Places the tensors' workgroups and Gram parts, then launches.
+static int muon_run(MuonArgs& a, void* workspace, size_t ws_bytes, void* stream) {
+  size_t need = 0;
+  a.blocks = 0;
+  for (int i = 0; i < a.count; ++i) {
+    MuonTensor& t = a.t[i];
+    t.chunks = muon_chunks(t.n, t.r);
+    t.block0 = a.blocks;
+    t.gram = (double*)((char*)workspace + need);
+    a.blocks += t.E * t.chunks;
+    need += muon_gram_bytes(t.E, t.r, t.n);
+  }
+  if (workspace == nullptr || ws_bytes < need)
+    return fail(NF4MOE_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                workspace ? ws_bytes : (size_t)0);
+  if (!aligned(workspace, 256)) return fail(NF4MOE_EINVAL, "workspace must be 256-byte aligned");
+  hipError_t err = launch_muon(a, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "adapter update launch");
+  return ok();
+}
+
+size_t lora_muon_step_workspace(const nf4moe_muon_tensor* tensors, int count) {
+  if (tensors == nullptr || count < 1 || count > NF4MOE_MAX_MUON_TENSORS) return 0;
+  size_t need = 0;
+  for (int i = 0; i < count; ++i) {
+    if (muon_shape_check(tensors[i].E, tensors[i].r, tensors[i].n) != NF4MOE_OK) return 0;
+    need += muon_gram_bytes(tensors[i].E, tensors[i].r, tensors[i].n);
+  }
+  return need;
+}
+
+int lora_muon_step(const nf4moe_muon_tensor* tensors, int count, double lr, double mu,
+                   int nesterov, double weight_decay, int ns_steps, double a, double b, double c,
+                   double ns_eps, void* workspace, size_t ws_bytes, void* stream) {
+  if (tensors == nullptr || count < 1 || count > NF4MOE_MAX_MUON_TENSORS)
+    return fail(NF4MOE_EINVAL, "1 to %d tensors are taken, got %d", NF4MOE_MAX_MUON_TENSORS,
+                tensors ? count : 0);
+  int st = muon_scalar_check(ns_steps, a, b, c, ns_eps);
+  if (st != NF4MOE_OK) return st;
+  if (!std::isfinite(lr) || !std::isfinite(mu) || !std::isfinite(weight_decay))
+    return fail(NF4MOE_EINVAL, "lr, mu and weight_decay must be finite");
+  if (nesterov != 0 && nesterov != 1) return fail(NF4MOE_EINVAL, "nesterov must be 0 or 1");
+  MuonArgs m{};
+  m.count = count;
+  m.nesterov = nesterov;
+  m.steps = ns_steps;
+  m.mu = (float)mu;
+  m.lr = lr;
+  m.weight_decay = weight_decay;
+  m.a = a;
+  m.b = b;
+  m.c = c;
+  m.eps = ns_eps;
+  for (int i = 0; i < count; ++i) {
+    const nf4moe_muon_tensor& s = tensors[i];
+    st = muon_shape_check(s.E, s.r, s.n);
+    if (st != NF4MOE_OK) return st;
+    if (s.grad == nullptr || s.m == nullptr || s.m_out == nullptr || s.w == nullptr ||
+        s.w_out == nullptr)
+      return fail(NF4MOE_EINVAL, "tensor %d: grad, m, m_out, w and w_out must be non-null", i);
+    if (s.rank_major != 0 && s.rank_major != 1)
+      return fail(NF4MOE_EINVAL, "tensor %d: rank_major must be 0 or 1", i);
+    if (!is_float_dtype(s.w_dtype))
+      return fail(NF4MOE_EDTYPE, "tensor %d: w_dtype=%d is unknown", i, s.w_dtype);
+    if (s.w16 != nullptr && s.w16_dtype != NF4MOE_BF16 && s.w16_dtype != NF4MOE_F16)
+      return fail(NF4MOE_EDTYPE, "tensor %d: w16_dtype=%d must be BF16 or F16", i, s.w16_dtype);
+    if (!std::isfinite(s.scale))
+      return fail(NF4MOE_EINVAL, "tensor %d: scale is not finite", i);
+    const size_t wb = dtype_bytes(s.w_dtype);
+    if (!aligned(s.grad, 4) || !aligned(s.m, 4) || !aligned(s.m_out, 4) || !aligned(s.w, wb) ||
+        !aligned(s.w_out, wb) || !aligned(s.w16, 2))
+      return fail(NF4MOE_EINVAL, "tensor %d: misaligned buffer (each needs its element)", i);
+    MuonTensor& t = m.t[i];
+    t.g = s.grad;
+    t.m = s.m;
+    t.m_out = s.m_out;
+    t.w = s.w;
+    t.w_out = s.w_out;
+    t.w16 = s.w16;
+    t.n = s.n;
+    t.scale = s.scale;
+    t.E = s.E;
+    t.r = s.r;
+    t.rank_major = s.rank_major;
+    t.g_dtype = NF4MOE_F32;
+    t.w_dtype = s.w_dtype;
+    t.w16_dtype = s.w16_dtype;
+  }
+  return muon_run(m, workspace, ws_bytes, stream);
+}
+
+size_t lora_orthogonalize_workspace(int E, int r, int64_t n) {
+  if (muon_shape_check(E, r, n) != NF4MOE_OK) return 0;
+  return muon_gram_bytes(E, r, n);
+}
+
+int lora_orthogonalize(const void* u, int u_dtype, int E, int r, int64_t n, int rank_major,
+                       int ns_steps, double a, double b, double c, double ns_eps, void* out,
+                       int out_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (u == nullptr || out == nullptr) return fail(NF4MOE_EINVAL, "u and out must be non-null");
+  int st = muon_shape_check(E, r, n);
+  if (st == NF4MOE_OK) st = muon_scalar_check(ns_steps, a, b, c, ns_eps);
+  if (st != NF4MOE_OK) return st;
+  if (rank_major != 0 && rank_major != 1)
+    return fail(NF4MOE_EINVAL, "rank_major must be 0 or 1");
+  if (!is_float_dtype(u_dtype) || !is_float_dtype(out_dtype))
+    return fail(NF4MOE_EDTYPE, "unknown dtype (u %d, out %d)", u_dtype, out_dtype);
+  if (!aligned(u, dtype_bytes(u_dtype)) || !aligned(out, dtype_bytes(out_dtype)))
+    return fail(NF4MOE_EINVAL, "misaligned buffer (each needs its element)");
+  MuonArgs m{};
+  m.count = 1;
+  m.steps = ns_steps;
+  m.a = a;
+  m.b = b;
+  m.c = c;
+  m.eps = ns_eps;
+  MuonTensor& t = m.t[0];
+  t.g = u;
+  t.w_out = out;
+  t.n = n;
+  t.E = E;
+  t.r = r;
+  t.rank_major = rank_major;
+  t.g_dtype = u_dtype;
+  t.w_dtype = out_dtype;
+  return muon_run(m, workspace, ws_bytes, stream);
+}
+
 }  // extern "C"

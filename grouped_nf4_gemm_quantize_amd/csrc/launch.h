@@ -216,4 +216,79 @@ hipError_t launch_lora_to_f16(const void* src, int src_bf16, int transpose, int 
                               int r, _Float16* dst, int num_cus, hipStream_t s);
 hipError_t launch_lora_pass(const LoraPassArgs& a, int num_cus, hipStream_t s);
 
+// ---- 4-bit matrix-vector products (matvec.hip) ------------------------------
+enum MatvecType { kMvNF4 = 0, kMvFP4 = 1, kMvINT4 = 2, kMvMXFP4 = 7 };
+
+struct MatvecArgs {
+  const void* x;         // [T, K] fp16 or bf16
+  const uint8_t* codes;  // [N, K / 2]
+  const void* scales;    // [N, K / group]
+  const uint8_t* zeros;  // nullable (int4 only)
+  const float* bias;     // nullable
+  void* y;               // [T, N]
+  int64_t T;
+  int N, K;
+  int x_bf16;
+  int scale_dtype;
+  int group;
+  int qt;                // MatvecType
+  int y_dtype;
+};
+hipError_t launch_matvec(const MatvecArgs& a, int num_cus, hipStream_t s);
+
+// ---- norms around a block (blocknorm.hip) -----------------------------------
+struct BlockNormArgs {
+  const void* residual;  // forward: residual; backward: the stored r
+  const void* y;         // nullable
+  const float* gate;     // nullable
+  const void* w_pre;     // nullable
+  const void* w_post;    // nullable
+  const void* dh;        // backward
+  const void* d_r_out;   // backward, nullable
+  void* r_out;           // forward: r; backward: dresidual
+  void* h;               // forward: h; backward: dy
+  float* dgate;
+  float* dw_pre;
+  float* dw_post;
+  float* part;           // backward: [3, groups, H] partial sums over T
+  int64_t T;
+  int H;
+  int res_dtype, y_dtype, h_dtype, w_dtype, gate_axis;
+  float w_offset, alpha, beta, eps;
+};
+hipError_t launch_block_norm(const BlockNormArgs& a, int num_cus, hipStream_t s);
+hipError_t launch_block_norm_bwd(const BlockNormArgs& a, hipStream_t s);
+// Rows of partial sums that the backward of T rows writes per output.
+int block_norm_groups(int64_t T, int H);
+
+// ---- adapter update (muon.hip) ----------------------------------------------
+constexpr int kMuonMaxTensors = 8;
+constexpr int64_t kMuonMaxBlocks = 1 << 20;  // workgroups of one tensor
+struct MuonTensor {
+  const void* g;  // gradient, or u itself (m null)
+  const float* m;
+  float* m_out;
+  const void* w;
+  void* w_out;
+  void* w16;
+  double* gram;   // [E, chunks, r, r]
+  int64_t n;
+  double scale;
+  int E, r, rank_major;
+  int g_dtype, w_dtype, w16_dtype;
+  int chunks;     // workgroups of one factor
+  int block0;     // first workgroup of this tensor
+};
+struct MuonArgs {
+  MuonTensor t[kMuonMaxTensors];
+  int count;
+  int nesterov;
+  int steps;
+  int blocks;
+  float mu;
+  double lr, weight_decay, a, b, c, eps;
+};
+int muon_chunks(int64_t n, int r);
+hipError_t launch_muon(const MuonArgs& a, hipStream_t s);
+
 }  // namespace nf4moe

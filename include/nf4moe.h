@@ -497,6 +497,156 @@ int moe_expert_forward_routing(void* workspace, int64_t T, int H, int I,
                                float** topk_w, int32_t** sorted_pair,
                                int32_t** expert_offsets);
 
+/* ---- 4-bit matrix-vector products with group scales -------------------------
+ * The dense projections beside the routed experts (attention projections,
+ * shared projections, an output head) for the few rows of a decode step, on
+ * the same storage the expert stacks use:
+ *   y[t, n] = bias[n] + sum_g s[n, g] * sum_{k in g} (v(code[n, k]) - z[n, g]) * x[t, k]
+ * over the groups g of `group` consecutive k of row n.
+ *   quant_type  NF4MOE_QT_NF4 and _FP4: levels of nbit_codebook, group 64,
+ *               scales fp32 absmax (what nbit_quantize_experts writes; one
+ *               expert's [N, K] slice of a stack is a valid matrix);
+ *               NF4MOE_QT_INT4: v = code (0..15), group 32, 64 or 128,
+ *               scales F32, BF16 or F16, zeros uint8 [N, K/group] or NULL for 8
+ *               everywhere (symmetric);
+ *               NF4MOE_QT_MXFP4: e2m1 values, group 32, e8m0 scale bytes
+ *               (255 is NaN), element 2i in the LOW nibble;
+ *               element 2i is in the HIGH nibble for the other three;
+ *   x [T, K]    F16 or BF16; enters the multiplication as fp16 (the range
+ *               of the conventions above); T >= 1.  Products, sums and scales
+ *               are fp32: levels are held to 22 bits and more;
+ *   codes       [N, K/2]; K a multiple of `group` (ESHAPE), N >= 1, any;
+ *   scales      [N, K/group]; scale_dtype is for INT4 (must be F32 for NF4
+ *               and FP4, ignored for MXFP4);
+ *   bias        nullable fp32 [N];
+ *   y [T, N]    F32, BF16 or F16; must not overlap the inputs.
+ * 16 rows of x share one read of the matrix; more rows read it again (mostly from
+ * cache), so from about 128 rows on the grouped GEMM with E = 1 is the
+ * better call.  No workspace.  The order of the sums depends on the sizes only:
+ * results are the same from call to call.
+ * Alignment (else EINVAL): x and codes 16 bytes, scales, bias and y their
+ * element.  T beyond NF4MOE_MATVEC_MAX_T, N beyond 2^31 - 65 or K beyond 2^30 ->
+ * EOVERFLOW. */
+#define NF4MOE_QT_INT4 2  /* nbit_matvec only */
+#define NF4MOE_QT_MXFP4 7 /* nbit_matvec only */
+#define NF4MOE_MATVEC_MAX_T 262144
+int nbit_matvec(int quant_type, const void* x, int x_dtype, int64_t T,
+                const uint8_t* codes, const void* scales, int scale_dtype,
+                const uint8_t* zeros, int group, int64_t N, int64_t K,
+                const float* bias, void* y, int y_dtype, void* stream);
+
+/* ---- norms around a block, with its gate and residual scale -----------------
+ * Joins the output y of one block (moe_expert_forward's y, or any other) to
+ * the residual stream and normalises the sum for the next block, in one pass:
+ *   z = y * rsqrt(mean(y^2) + eps) * (w_post + w_offset)   (w_post NULL: z = y)
+ *   r = beta * residual + alpha * gate * z       (rounded once to r's type)
+ *   h = r * rsqrt(mean(r^2) + eps) * (w_pre + w_offset)    (from the stored r)
+ * with means over the H elements of a row.  y NULL: r is residual itself and
+ * only h is computed (the norm before a first block; beta must be 1, r_out,
+ * w_post and the gate absent).  w_pre and h NULL: only r is computed.
+ *   residual, r_out [T, H] of res_dtype; y [T, H] of y_dtype; h [T, H] of
+ *               h_dtype (each F32, BF16 or F16); r_out may be residual (in
+ *               place), h may be y if the types agree; no other overlap;
+ *   w_pre, w_post  [H] of w_dtype (F32, BF16 or F16);
+ *   gate        fp32: NF4MOE_GATE_TOKEN [T] or NF4MOE_GATE_CHANNEL [H];
+ *               NF4MOE_GATE_NONE with NULL: 1;
+ *   H           a multiple of 8, at most 16384 (ESHAPE); T >= 1;
+ *   eps >= 0, alpha, beta and w_offset finite (EINVAL).
+ * All matrices and weights 16-byte aligned, gate 4 (else EINVAL).  Means and
+ * sums are fp32.  One launch, no workspace. */
+#define NF4MOE_GATE_NONE 0
+#define NF4MOE_GATE_TOKEN 1
+#define NF4MOE_GATE_CHANNEL 2
+#define NF4MOE_MAX_NORM_H 16384
+int block_norm_forward(const void* residual, int res_dtype, const void* y, int y_dtype,
+                       const float* gate, int gate_axis, const void* w_pre,
+                       const void* w_post, int w_dtype, float w_offset, float alpha,
+                       float beta, float eps, int64_t T, int64_t H, void* r_out,
+                       void* h, int h_dtype, void* stream);
+
+/* The gradients of block_norm_forward.  With rms'(g; x, w) = rstd * g * w - x * rstd^3 *
+ * mean(g * w * x), w standing for w + w_offset:
+ *   dr        = d_r_out + rms'(dh; r, w_pre)
+ *   dresidual = beta * dr
+ *   dgate     = alpha * sum of dr * z over the other axis (H for a token
+ *               gate, T for a channel gate)
+ *   dz        = alpha * gate * dr;  dy = rms'(dz; y, w_post), or dz
+ *   dw_pre    = sum_t dh * r * rstd(r);   dw_post = sum_t dz * y * rstd(y)
+ *   r [T, H]    the forward's r_out (its residual when y was NULL), res_dtype;
+ *   dh          [T, H] of h_dtype, NULL exactly if w_pre is;
+ *   d_r_out     nullable [T, H] of res_dtype: the gradient that reaches r_out
+ *               directly (NULL: none; not both it and dh);
+ *   y, gate, weights and scalars as in the forward (beta must be 1 without y);
+ *   dresidual   [T, H] of res_dtype; dy [T, H] of y_dtype (with y);
+ *   dgate       fp32 like gate; dw_pre, dw_post fp32 [H]: required exactly where
+ *               their inputs are given.  dresidual may be d_r_out and dy
+ *               may be y or dh (types agreeing), each element is read before it
+ *               is written; no other overlap;
+ *   workspace   block_norm_backward_workspace(T, H) bytes, 256-byte aligned
+ *               (EWORKSPACE, EINVAL).
+ * Sums over T are taken per workgroup and then over the workgroups in a fixed
+ * order: results are the same from call to call.  Other arguments and errors as
+ * in the forward.  block_norm_backward_workspace returns 0 for invalid sizes. */
+size_t block_norm_backward_workspace(int64_t T, int64_t H);
+int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const void* r,
+                        int res_dtype, const void* y, int y_dtype, const float* gate,
+                        int gate_axis, const void* w_pre, const void* w_post, int w_dtype,
+                        float w_offset, float alpha, float beta, float eps, int64_t T,
+                        int64_t H, void* dresidual, void* dy, float* dgate, float* dw_pre,
+                        float* dw_post, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- adapter update orthogonalised by Newton-Schulz products ----------------
+ * The optimiser step of per-expert adapter factors with the gradients that
+ * moe_expert_backward returns.  Each expert's factor is one r x n matrix (its long axis
+ * n, its rank r); for each,
+ *   m' = mu * m + g;   u = nesterov ? g + mu * m' : m'
+ *   X  = u / (|u|_F + ns_eps), then ns_steps times
+ *   X <- a X + b (X X^T) X + c (X X^T)^2 X;            O = X
+ *   w' = w * (1 - lr * weight_decay) - lr * scale * O
+ * The Gram matrix, the r x r products and O are computed in 64 bits, m' and u in
+ * 32, and w' is rounded once to its type.  A factor whose u is zero has O = 0; one
+ * with a non-finite u gets NaN, and no other factor is touched by it.
+ *   grad, m, m_out  fp32 [E, r, n] (rank_major = 1: the A factors) or
+ *                   [E, n, r] (rank_major = 0: the B factors); m_out may be m;
+ *   w, w_out        the same layout, w_dtype F32, BF16 or F16; w_out may be w;
+ *   w16             nullable: a second copy of w_out rounded to w16_dtype (BF16
+ *                   or F16) once more, for fp32 w (the adapter the layer reads);
+ *   r               1 .. NF4MOE_MAX_LORA_R; E, n >= 1 (r > n is allowed);
+ *   tensors [host]  1 .. NF4MOE_MAX_MUON_TENSORS factors in one call, which
+ *                   must not share outputs;
+ *   ns_steps        1 .. 16; lr, mu, weight_decay, scale, a, b, c finite,
+ *                   ns_eps >= 0 (EINVAL);
+ *   workspace       lora_muon_step_workspace(tensors, count) bytes, 256-byte
+ *                   aligned; 0 for invalid arguments.
+ * Pointers are aligned to their element.  E * r * n at most 2^40 and E * ceil(n / 256) at
+ * most 2^20 (EOVERFLOW). */
+#define NF4MOE_MAX_MUON_TENSORS 8
+typedef struct {
+  const float* grad;
+  const float* m;
+  float* m_out;
+  const void* w;
+  void* w_out;
+  void* w16;
+  int64_t n;
+  int E, r, rank_major;
+  int w_dtype, w16_dtype;
+  double scale;
+} nf4moe_muon_tensor;
+size_t lora_muon_step_workspace(const nf4moe_muon_tensor* tensors, int count);
+int lora_muon_step(const nf4moe_muon_tensor* tensors, int count, double lr, double mu,
+                   int nesterov, double weight_decay, int ns_steps, double a, double b,
+                   double c, double ns_eps, void* workspace, size_t ws_bytes, void* stream);
+
+/* O alone: out = Newton-Schulz(u) for u [E, r, n] or [E, n, r] of u_dtype (F32, BF16 or F16),
+ * out of out_dtype in the same layout (out may be u if the types agree).
+ * workspace: lora_orthogonalize_workspace(E, r, n) bytes.  Other arguments and
+ * errors as above. */
+size_t lora_orthogonalize_workspace(int E, int r, int64_t n);
+int lora_orthogonalize(const void* u, int u_dtype, int E, int r, int64_t n, int rank_major,
+                       int ns_steps, double a, double b, double c, double ns_eps, void* out,
+                       int out_dtype, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

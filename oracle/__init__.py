@@ -94,3 +94,5 @@ from .nbit8 import (  # noqa: F401
     quantize_blockwise8,
     dequantize_blockwise8,
 )
+from .matvec import matvec, matvec_weight  # noqa: F401
+from . import blocknorm, muon  # noqa: F401
