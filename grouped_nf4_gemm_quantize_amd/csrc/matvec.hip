@@ -33,44 +33,76 @@ constexpr int kMvTile = 16;     // output rows of one matrix step
 constexpr int kMvTokens = 16;   // rows of x of one matrix step
 constexpr int kMvChunk = 128;   // k of one lane-wide read
 
-enum MvKind { kPlain = 0, kSplit = 1, kZeros = 2 };  // fp16 table; two tables; minus zeros
+// What a kernel is compiled for: how the table's values are held, and the groups.
+enum MvFormat {
+  kMvfNF4,      // two fp16 tables, fp32 scales of 64
+  kMvfFP4,      // fp32 scales of 64
+  kMvfMX,       // e8m0 scales of 32
+  kMvfInt32,    // codes minus zeros, scales of 32, 64 or 128 of any float type
+  kMvfInt64,
+  kMvfInt128
+};
+constexpr bool mv_split(int f) { return f == kMvfNF4; }
+constexpr bool mv_int(int f) { return f >= kMvfInt32; }
+// scale groups of a chunk
+constexpr int mv_groups(int f) { return f == kMvfMX || f == kMvfInt32 ? 4 : f == kMvfInt128 ? 1 : 2; }
 
+// Raw scales of a chunk's groups (their bits, widened), and zeros, a byte each.
+template <int kFmt>
 struct MvScales {
-  uint32_t s[4];  // raw scales of a chunk's groups
-  uint32_t z;     // raw zeros, one byte a group
+  uint32_t s[mv_groups(kFmt)];
+  uint32_t z;
 };
 
-// Raw scale i of the matrix (its bits, widened).
-__device__ __forceinline__ uint32_t mv_raw(const MatvecArgs& a, int64_t i) {
-  if (a.qt == kMvMXFP4) return reinterpret_cast<const uint8_t*>(a.scales)[i];
-  if (a.scale_dtype == kF32) return reinterpret_cast<const uint32_t*>(a.scales)[i];
-  return reinterpret_cast<const uint16_t*>(a.scales)[i];
-}
-
+template <int kFmt>
 __device__ __forceinline__ float mv_value(const MatvecArgs& a, uint32_t raw) {
-  if (a.qt == kMvMXFP4)  // 2^(raw - 127), 255 is NaN
-    return raw == 255u ? __builtin_nanf("") : ldexpf(1.0f, (int)raw - 127);
-  if (a.scale_dtype == kF32) return __uint_as_float(raw);
+  if constexpr (kFmt == kMvfMX)  // 2^(raw - 127), 255 is NaN
+    return __uint_as_float(raw == 0u ? 0x00400000u : raw == 255u ? 0x7fc00000u : raw << 23);
+  if (!mv_int(kFmt) || a.scale_dtype == kF32) return __uint_as_float(raw);
   return a.scale_dtype == kBF16 ? bf16_bits_to_f32(raw)
                                 : (float)__builtin_bit_cast(_Float16, (uint16_t)raw);
 }
 
-// The raw scales (and zeros) of chunk c of row n: `left` of its k exist.
-template <int kKind>
-__device__ __forceinline__ MvScales mv_load_scales(const MatvecArgs& a, int n, int c, int left) {
-  MvScales r;
-  const int per = kMvChunk / a.group;  // 1, 2 or 4
-  const int64_t i0 = (int64_t)n * (a.K / a.group) + c * per;
-  r.z = 0;
+// The raw scales (and zeros) of chunk c of row n, 0 for groups beyond the row. Rows of
+// whole chunks read a chunk's scales at once.
+template <int kFmt>
+__device__ __forceinline__ void mv_load_scales(const MatvecArgs& a, int n, int c, bool whole,
+                                               MvScales<kFmt>& r) {
+  constexpr int kPer = mv_groups(kFmt), kGroup = kMvChunk / kPer;
+  const int groups = a.K / kGroup;
+  const int64_t i0 = (int64_t)n * groups + c * kPer;
+  const bool wide = !mv_int(kFmt) || a.scale_dtype == kF32;
+  r.z = 0x08080808u;
+  if (whole) {
+    if constexpr (kFmt == kMvfMX) {
+      uint32_t v;
+      __builtin_memcpy(&v, reinterpret_cast<const uint8_t*>(a.scales) + i0, 4);
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    r.s[g] = 0;
-    if (g < per && g * a.group < left) {
-      r.s[g] = mv_raw(a, i0 + g);
-      if constexpr (kKind == kZeros) r.z |= (uint32_t)a.zeros[i0 + g] << (8 * g);
+      for (int g = 0; g < kPer; ++g) r.s[g] = (v >> (8 * g)) & 0xffu;
+    } else if (wide) {
+      __builtin_memcpy(r.s, reinterpret_cast<const uint32_t*>(a.scales) + i0, 4 * kPer);
+    } else {
+      uint16_t v[kPer];
+      __builtin_memcpy(v, reinterpret_cast<const uint16_t*>(a.scales) + i0, 2 * kPer);
+#pragma unroll
+      for (int g = 0; g < kPer; ++g) r.s[g] = v[g];
     }
+    if constexpr (mv_int(kFmt))
+      if (a.zeros) __builtin_memcpy(&r.z, a.zeros + i0, kPer);
+    return;
   }
-  return r;
+#pragma unroll
+  for (int g = 0; g < kPer; ++g) {
+    const bool in = c * kPer + g < groups;
+    const int64_t i = in ? i0 + g : i0;
+    uint32_t v;
+    if constexpr (kFmt == kMvfMX) v = reinterpret_cast<const uint8_t*>(a.scales)[i];
+    else if (wide) v = reinterpret_cast<const uint32_t*>(a.scales)[i];
+    else v = reinterpret_cast<const uint16_t*>(a.scales)[i];
+    r.s[g] = in ? v : 0u;
+    if constexpr (mv_int(kFmt))
+      if (a.zeros) r.z = (r.z & ~(0xffu << (8 * g))) | ((uint32_t)a.zeros[i] << (8 * g));
+  }
 }
 
 // Transposes 4 words x 4 lane rows of 16: lane row q, word s <-> lane row s, word q.
@@ -82,24 +114,24 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&d)[4]) {
   d[0] = u[0], d[1] = u[1], d[2] = v[0], d[3] = v[1];
 }
 
-// tot += the products of one chunk of one row tile.
-template <int kKind, int kRegs>
+// tot += the products of one chunk of one row tile. Steps beyond the end of the row
+// have x = 0 and a scale of 0.
+template <int kFmt, int kRegs>
 __device__ __forceinline__ void mv_chunk(const MatvecArgs& a, const char* lut, uint32_t lane_off,
-                                         u32x4 w, const MvScales& sc, const f16x8 (&x)[4],
-                                         int left, float (&tot)[kRegs]) {
+                                         u32x4 w, const MvScales<kFmt>& sc, const f16x8 (&x)[4],
+                                         float (&tot)[kRegs]) {
   uint32_t d[4] = {w.x, w.y, w.z, w.w};
   quad_transpose(d);
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    if (32 * s >= left) break;
-    const int g = a.group == 32 ? s : a.group == 64 ? s >> 1 : 0;
+    const int g = s * mv_groups(kFmt) / 4;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       // table address: byte j of the codes in bits 8..15, the lane's slot below
       const uint32_t at =
           __builtin_amdgcn_perm(d[s], lane_off, 0x0c0c0000u | ((4u + j) << 8));
-      if constexpr (kKind == kSplit) {
+      if constexpr (mv_split(kFmt)) {
         const u32x2 e = *reinterpret_cast<const u32x2*>(lut + at);
         hi[j] = e.x;
         lo[j] = e.y;
@@ -107,7 +139,7 @@ __device__ __forceinline__ void mv_chunk(const MatvecArgs& a, const char* lut, u
         hi[j] = *reinterpret_cast<const uint32_t*>(lut + at);
       }
     }
-    if constexpr (kKind == kZeros) {
+    if constexpr (mv_int(kFmt)) {
       const _Float16 z = (_Float16)(float)((sc.z >> (8 * g)) & 0xffu);
       const f16x2 z2 = {z, z};
 #pragma unroll
@@ -116,12 +148,12 @@ __device__ __forceinline__ void mv_chunk(const MatvecArgs& a, const char* lut, u
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     const u32x4 h4 = {hi[0], hi[1], hi[2], hi[3]};
     acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s], __builtin_bit_cast(f16x8, h4), acc, 0, 0, 0);
-    if constexpr (kKind == kSplit) {
+    if constexpr (mv_split(kFmt)) {
       const u32x4 l4 = {lo[0], lo[1], lo[2], lo[3]};
       acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s], __builtin_bit_cast(f16x8, l4), acc, 0, 0,
                                                    0);
     }
-    const float f = mv_value(a, sc.s[g]);
+    const float f = mv_value<kFmt>(a, sc.s[g]);
 #pragma unroll
     for (int i = 0; i < kRegs; ++i) tot[i] = fmaf(f, acc[i], tot[i]);
   }
@@ -131,8 +163,9 @@ __device__ __forceinline__ void mv_chunk(const MatvecArgs& a, const char* lut, u
 // (m / 4) kRegs + m % 4 where m % 4 < kRegs, so that the first kRegs result
 // registers of a lane hold all tokens.
 template <int kRegs>
-__device__ __forceinline__ void mv_load_x(const MatvecArgs& a, int64_t t0, int nt, int c, int left,
-                                          int lane, f16x8 (&x)[4]) {
+__device__ __forceinline__ void mv_load_x(const MatvecArgs& a, int64_t t0, int nt, int c, int lane,
+                                          f16x8 (&x)[4]) {
+  const int left = a.K - c * kMvChunk;
   const int m = lane & 15, q = lane >> 4;
   const int t = (m >> 2) * kRegs + (m & 3);
   const bool live = (m & 3) < kRegs && t < nt;
@@ -155,16 +188,13 @@ __device__ __forceinline__ void mv_load_x(const MatvecArgs& a, int64_t t0, int n
 }
 
 // The decode table: 256 byte values x 256 bytes, as 32 copies of two words
-// (kSplit) or 64 of one.  Ends with a barrier.
-template <int kKind>
-__device__ __forceinline__ void mv_fill(const MatvecArgs& a, u32x4* lut, uint32_t* stage, int tid) {
+// (nf4) or 64 of one.  Ends with a barrier.
+template <int kFmt>
+__device__ __forceinline__ void mv_fill(u32x4* lut, uint32_t* stage, int tid) {
   const float nf4[16] = NF4MOE_LEVELS_INIT;
   const float e2m1[16] = NF4MOE_E2M1_VALUES_INIT;
   if (tid < 16) {
-    const float v = kKind == kSplit       ? 256.0f * nf4[tid]
-                    : kKind == kZeros     ? (float)tid
-                    : a.qt == kMvINT4     ? (float)tid - 8.0f
-                                          : e2m1[tid];
+    const float v = mv_split(kFmt) ? 256.0f * nf4[tid] : mv_int(kFmt) ? (float)tid : e2m1[tid];
     const _Float16 hi = (_Float16)v, lo = (_Float16)(v - (float)hi);
     stage[tid] = pack_half2(hi, lo);
   }
@@ -172,11 +202,11 @@ __device__ __forceinline__ void mv_fill(const MatvecArgs& a, u32x4* lut, uint32_
 #pragma unroll
   for (int i = 0; i < 4096 / kMvThreads; ++i) {
     const int u = i * kMvThreads + tid, b = u >> 4;  // 16 16-byte units an entry
-    const uint32_t first = stage[a.qt == kMvMXFP4 ? b & 15 : b >> 4];
-    const uint32_t second = stage[a.qt == kMvMXFP4 ? b >> 4 : b & 15];
+    const uint32_t first = stage[kFmt == kMvfMX ? b & 15 : b >> 4];
+    const uint32_t second = stage[kFmt == kMvfMX ? b >> 4 : b & 15];
     const uint32_t h = (first & 0xffffu) | (second << 16);
     const uint32_t l = (first >> 16) | (second & 0xffff0000u);
-    lut[u] = kKind == kSplit ? u32x4{h, l, h, l} : u32x4{h, h, h, h};
+    lut[u] = mv_split(kFmt) ? u32x4{h, l, h, l} : u32x4{h, h, h, h};
   }
   __syncthreads();
 }
@@ -185,7 +215,7 @@ __device__ __forceinline__ void mv_fill(const MatvecArgs& a, u32x4* lut, uint32_
 
 // kCpw: chunks of a wave that stay in registers as x (0: x is read for every
 // tile, any K).
-template <int kKind, int kRegs, int kCpw>
+template <int kFmt, int kRegs, int kCpw>
 __global__ __launch_bounds__(kMvThreads) void matvec_kernel(MatvecArgs a) {
   constexpr int kX = kCpw ? kCpw : 1;
   __shared__ u32x4 lut[4096];
@@ -196,11 +226,11 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(MatvecArgs a) {
   const int64_t t0 = (int64_t)blockIdx.y * kMvTokens;
   const int nt = a.T - t0 < kMvTokens ? (int)(a.T - t0) : kMvTokens;
   const int chunks = (a.K + kMvChunk - 1) / kMvChunk;
+  const bool whole = a.K % kMvChunk == 0;
   const int tiles = (a.N + kMvTile - 1) / kMvTile;
   const int q = lane >> 4;
-  const uint32_t lane_off = kKind == kSplit ? (lane & 31) * 8 : lane * 4;
+  const uint32_t lane_off = mv_split(kFmt) ? (lane & 31) * 8 : lane * 4;
   const int64_t row_bytes = a.K / 2;
-  const auto left_of = [&](int c) { return a.K - c * kMvChunk; };
   const auto row_of = [&](int tile) {
     const int n = tile * kMvTile + (lane & 15);
     return n < a.N ? n : a.N - 1;
@@ -208,58 +238,53 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(MatvecArgs a) {
   // 16 packed bytes of chunk c: the lane's 32 codes, or the row's first where the
   // row has ended (x is zero there)
   const auto load_w = [&](int n, int c) {
-    const int64_t at = 32 * q < left_of(c) ? c * (kMvChunk / 2) + 16 * q : 0;
-    return *reinterpret_cast<const u32x4*>(a.codes + n * row_bytes + at);
+    const int at = c * (kMvChunk / 2) + 16 * q;
+    return *reinterpret_cast<const u32x4*>(a.codes + n * row_bytes + (at < row_bytes ? at : 0));
   };
 
   f16x8 x[kX][4];
-  u32x4 w[kX];
-  MvScales sc[kX];
+  u32x4 w[kX] = {};
+  MvScales<kFmt> sc[kX] = {};
   int tile = blockIdx.x;
-  if constexpr (kCpw > 0) {
-    const int n = row_of(tile);
+  const auto load_tile = [&](int tl) {
+    const int n = row_of(tl);
 #pragma unroll
     for (int j = 0; j < kX; ++j) {
       const int c = wave + j * kMvWaves;
-      if (c >= chunks) break;
+      if (c >= chunks) continue;
       w[j] = load_w(n, c);
-      sc[j] = mv_load_scales<kKind>(a, n, c, left_of(c));
-      mv_load_x<kRegs>(a, t0, nt, c, left_of(c), lane, x[j]);
+      mv_load_scales<kFmt>(a, n, c, whole, sc[j]);
     }
+  };
+  if constexpr (kCpw > 0) {
+    load_tile(tile);
+#pragma unroll
+    for (int j = 0; j < kX; ++j)
+      mv_load_x<kRegs>(a, t0, nt, wave + j * kMvWaves, lane, x[j]);
   }
-  mv_fill<kKind>(a, lut, stage, tid);
+  mv_fill<kFmt>(lut, stage, tid);
   const char* table = reinterpret_cast<const char*>(lut);
-  const float last = kKind == kSplit ? 1.0f / 256.0f : 1.0f;
+  const float last = mv_split(kFmt) ? 1.0f / 256.0f : kFmt == kMvfFP4 ? 1.0f / 6.0f : 1.0f;
 
   for (int buf = 0; tile < tiles; tile += gridDim.x, buf ^= 1) {
     float tot[kRegs] = {};
     if constexpr (kCpw > 0) {
-      const int next = tile + (int)gridDim.x;
-      const int n = row_of(next);
-      u32x4 w2[kX];
-      MvScales sc2[kX];
+      u32x4 w1[kX];
+      MvScales<kFmt> sc1[kX];
 #pragma unroll
-      for (int j = 0; j < kX; ++j) {
-        const int c = wave + j * kMvWaves;
-        if (c >= chunks || next >= tiles) break;
-        w2[j] = load_w(n, c);
-        sc2[j] = mv_load_scales<kKind>(a, n, c, left_of(c));
-      }
+      for (int j = 0; j < kX; ++j) w1[j] = w[j], sc1[j] = sc[j];
+      if (tile + (int)gridDim.x < tiles) load_tile(tile + gridDim.x);
 #pragma unroll
-      for (int j = 0; j < kX; ++j) {
-        const int c = wave + j * kMvWaves;
-        if (c >= chunks) break;
-        mv_chunk<kKind, kRegs>(a, table, lane_off, w[j], sc[j], x[j], left_of(c), tot);
-      }
-#pragma unroll
-      for (int j = 0; j < kX; ++j) w[j] = w2[j], sc[j] = sc2[j];
+      for (int j = 0; j < kX; ++j)
+        mv_chunk<kFmt, kRegs>(a, table, lane_off, w1[j], sc1[j], x[j], tot);
     } else {
       const int n = row_of(tile);
       for (int c = wave; c < chunks; c += kMvWaves) {
         const u32x4 wc = load_w(n, c);
-        const MvScales s = mv_load_scales<kKind>(a, n, c, left_of(c));
-        mv_load_x<kRegs>(a, t0, nt, c, left_of(c), lane, x[0]);
-        mv_chunk<kKind, kRegs>(a, table, lane_off, wc, s, x[0], left_of(c), tot);
+        MvScales<kFmt> s;
+        mv_load_scales<kFmt>(a, n, c, whole, s);
+        mv_load_x<kRegs>(a, t0, nt, c, lane, x[0]);
+        mv_chunk<kFmt, kRegs>(a, table, lane_off, wc, s, x[0], tot);
       }
     }
 #pragma unroll
@@ -271,7 +296,7 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(MatvecArgs a) {
       for (int u = 0; u < kMvWaves; ++u) v += red[buf][u][wave][lane];
       const int t = q * kRegs + wave, n = tile * kMvTile + (lane & 15);
       if (t < nt && n < a.N) {
-        v = (a.qt == kMvFP4 ? v * (1.0f / 6.0f) : v * last) + (a.bias ? a.bias[n] : 0.f);
+        v = v * last + (a.bias ? a.bias[n] : 0.f);
         const int64_t i = (t0 + t) * a.N + n;
         if (a.y_dtype == kF32) reinterpret_cast<float*>(a.y)[i] = v;
         else if (a.y_dtype == kBF16) reinterpret_cast<uint16_t*>(a.y)[i] = f32_to_bf16_bits(v);
@@ -283,24 +308,23 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(MatvecArgs a) {
 
 namespace {
 
-template <int kKind, int kRegs>
+template <int kFmt, int kRegs>
 void mv_launch(const MatvecArgs& a, dim3 grid, hipStream_t s) {
   const int per = (a.K + kMvChunk * kMvWaves - 1) / (kMvChunk * kMvWaves);
   if (per <= 1)
-    hipLaunchKernelGGL((matvec_kernel<kKind, kRegs, 1>), grid, dim3(kMvThreads), 0, s, a);
+    hipLaunchKernelGGL((matvec_kernel<kFmt, kRegs, 1>), grid, dim3(kMvThreads), 0, s, a);
   else if (per <= 2)
-    hipLaunchKernelGGL((matvec_kernel<kKind, kRegs, 2>), grid, dim3(kMvThreads), 0, s, a);
+    hipLaunchKernelGGL((matvec_kernel<kFmt, kRegs, 2>), grid, dim3(kMvThreads), 0, s, a);
   else if (per <= 4)
-    hipLaunchKernelGGL((matvec_kernel<kKind, kRegs, 4>), grid, dim3(kMvThreads), 0, s, a);
+    hipLaunchKernelGGL((matvec_kernel<kFmt, kRegs, 4>), grid, dim3(kMvThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((matvec_kernel<kKind, kRegs, 0>), grid, dim3(kMvThreads), 0, s, a);
+    hipLaunchKernelGGL((matvec_kernel<kFmt, kRegs, 0>), grid, dim3(kMvThreads), 0, s, a);
 }
 
-template <int kKind>
+template <int kFmt>
 void mv_launch_rows(const MatvecArgs& a, dim3 grid, hipStream_t s) {
-  if (a.T <= 4) mv_launch<kKind, 1>(a, grid, s);
-  else if (a.T <= 8) mv_launch<kKind, 2>(a, grid, s);
-  else mv_launch<kKind, 4>(a, grid, s);
+  if (a.T <= 4) mv_launch<kFmt, 1>(a, grid, s);
+  else mv_launch<kFmt, 4>(a, grid, s);
 }
 
 }  // namespace
@@ -314,9 +338,12 @@ hipError_t launch_matvec(const MatvecArgs& a, int num_cus, hipStream_t s) {
   if (nx < 8) nx = 8;
   if (nx > tiles) nx = tiles;
   const dim3 grid((unsigned)nx, ny);
-  if (a.qt == kMvNF4) mv_launch_rows<kSplit>(a, grid, s);
-  else if (a.zeros) mv_launch_rows<kZeros>(a, grid, s);
-  else mv_launch_rows<kPlain>(a, grid, s);
+  if (a.qt == kMvNF4) mv_launch_rows<kMvfNF4>(a, grid, s);
+  else if (a.qt == kMvFP4) mv_launch_rows<kMvfFP4>(a, grid, s);
+  else if (a.qt == kMvMXFP4) mv_launch_rows<kMvfMX>(a, grid, s);
+  else if (a.group == 32) mv_launch_rows<kMvfInt32>(a, grid, s);
+  else if (a.group == 64) mv_launch_rows<kMvfInt64>(a, grid, s);
+  else mv_launch_rows<kMvfInt128>(a, grid, s);
   return hipGetLastError();
 }
 
