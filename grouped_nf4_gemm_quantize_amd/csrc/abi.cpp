@@ -1238,7 +1238,7 @@ int nbit_matvec(int quant_type, const void* x, int x_dtype, int64_t T, const uin
   }
   if (K % group)
     return fail(NF4MOE_ESHAPE, "K=%lld is not a multiple of the group %d", (long long)K, group);
-  if (T > NF4MOE_MATVEC_MAX_T || N > (int64_t)INT32_MAX - 64 || K > ((int64_t)1 << 30))
+  if (T > NF4MOE_MATVEC_MAX_T || N > (int64_t)INT32_MAX - 64 || K > ((int64_t)1 << 24))
     return fail(NF4MOE_EOVERFLOW, "T=%lld, N=%lld or K=%lld is too large", (long long)T,
                 (long long)N, (long long)K);
   const size_t sb = quant_type == kMvMXFP4 ? 1 : dtype_bytes(scale_dtype);

@@ -27,7 +27,7 @@ namespace nf4moe {
 
 namespace {
 
-constexpr int kMvThreads = 512;
+constexpr int kMvThreads = 1024;
 constexpr int kMvWaves = kMvThreads / 64;
 constexpr int kMvTile = 16;     // output rows of one matrix step
 constexpr int kMvTokens = 16;   // rows of x of one matrix step
@@ -47,62 +47,96 @@ constexpr bool mv_int(int f) { return f >= kMvfInt32; }
 // scale groups of a chunk
 constexpr int mv_groups(int f) { return f == kMvfMX || f == kMvfInt32 ? 4 : f == kMvfInt128 ? 1 : 2; }
 
-// Raw scales of a chunk's groups (their bits, widened), and zeros, a byte each.
-template <int kFmt>
-struct MvScales {
-  uint32_t s[mv_groups(kFmt)];
-  uint32_t z;
-};
+typedef __amdgpu_buffer_rsrc_t Rsrc;
 
-template <int kFmt>
-__device__ __forceinline__ float mv_value(const MatvecArgs& a, uint32_t raw) {
-  if constexpr (kFmt == kMvfMX)  // 2^(raw - 127), 255 is NaN
-    return __uint_as_float(raw == 0u ? 0x00400000u : raw == 255u ? 0x7fc00000u : raw << 23);
-  if (!mv_int(kFmt) || a.scale_dtype == kF32) return __uint_as_float(raw);
-  return a.scale_dtype == kBF16 ? bf16_bits_to_f32(raw)
-                                : (float)__builtin_bit_cast(_Float16, (uint16_t)raw);
+// The rows of a tile as a buffer: reads beyond its end return 0 without
+// touching memory, which covers rows beyond N and tiles beyond the last.
+__device__ __forceinline__ Rsrc mv_rsrc(const void* p, int64_t offset, int64_t bytes) {
+  char* at = const_cast<char*>(reinterpret_cast<const char*>(p)) + offset;
+  return __builtin_amdgcn_make_buffer_rsrc(at, 0, bytes > 0 ? (int)bytes : 0, 0x00020000);
 }
 
-// The raw scales (and zeros) of chunk c of row n, 0 for groups beyond the row. Rows of
-// whole chunks read a chunk's scales at once.
-template <int kFmt>
-__device__ __forceinline__ void mv_load_scales(const MatvecArgs& a, int n, int c, bool whole,
-                                               MvScales<kFmt>& r) {
-  constexpr int kPer = mv_groups(kFmt), kGroup = kMvChunk / kPer;
-  const int groups = a.K / kGroup;
-  const int64_t i0 = (int64_t)n * groups + c * kPer;
-  const bool wide = !mv_int(kFmt) || a.scale_dtype == kF32;
-  r.z = 0x08080808u;
-  if (whole) {
+// Raw scales of a chunk's groups as they are read, and zeros, a byte each.  Nothing is
+// computed on them before they are used, so that a read can stay in flight.
+template <int kFmt, bool kWhole>
+struct MvScales {
+  static constexpr int kPer = mv_groups(kFmt);
+  uint32_t s[kPer];  // kWhole: packed as in memory
+  uint32_t z[kPer];  // kWhole: all in z[0]
+};
+
+// What a lane needs of a tile's scales: byte offsets of its row.
+struct MvScaleRow {
+  int size;  // bytes of a scale
+  int s, z;  // offset of the row's first scale, and first zero
+  int groups;
+};
+
+template <int kFmt, bool kWhole>
+__device__ __forceinline__ void mv_load_scales(Rsrc rs, Rsrc rz, const MvScaleRow& row, int c,
+                                               MvScales<kFmt, kWhole>& r) {
+  constexpr int kPer = mv_groups(kFmt);
+  if constexpr (kWhole) {
+    const int at = row.s + c * kPer * row.size;
     if constexpr (kFmt == kMvfMX) {
-      uint32_t v;
-      __builtin_memcpy(&v, reinterpret_cast<const uint8_t*>(a.scales) + i0, 4);
-#pragma unroll
-      for (int g = 0; g < kPer; ++g) r.s[g] = (v >> (8 * g)) & 0xffu;
-    } else if (wide) {
-      __builtin_memcpy(r.s, reinterpret_cast<const uint32_t*>(a.scales) + i0, 4 * kPer);
+      r.s[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
+    } else if constexpr (!mv_int(kFmt)) {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
+      r.s[0] = v[0], r.s[1] = v[1];
+    } else if (row.size == 4) {
+      if constexpr (kPer == 4) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
+        r.s[0] = v[0], r.s[1] = v[1], r.s[2] = v[2], r.s[3] = v[3];
+      } else if constexpr (kPer == 2) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
+        r.s[0] = v[0], r.s[1] = v[1];
+      } else {
+        r.s[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
+      }
     } else {
-      uint16_t v[kPer];
-      __builtin_memcpy(v, reinterpret_cast<const uint16_t*>(a.scales) + i0, 2 * kPer);
-#pragma unroll
-      for (int g = 0; g < kPer; ++g) r.s[g] = v[g];
+      if constexpr (kPer == 4) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
+        r.s[0] = v[0], r.s[1] = v[1];
+      } else if constexpr (kPer == 2) {
+        r.s[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
+      } else {
+        r.s[0] = __builtin_amdgcn_raw_buffer_load_b16(rs, at, 0, 0);
+      }
     }
-    if constexpr (mv_int(kFmt))
-      if (a.zeros) __builtin_memcpy(&r.z, a.zeros + i0, kPer);
-    return;
-  }
+    if constexpr (mv_int(kFmt)) {
+      const int zat = row.z + c * kPer;
+      if constexpr (kPer == 4) r.z[0] = __builtin_amdgcn_raw_buffer_load_b32(rz, zat, 0, 0);
+      else if constexpr (kPer == 2) r.z[0] = __builtin_amdgcn_raw_buffer_load_b16(rz, zat, 0, 0);
+      else r.z[0] = __builtin_amdgcn_raw_buffer_load_b8(rz, zat, 0, 0);
+    }
+  } else {
 #pragma unroll
-  for (int g = 0; g < kPer; ++g) {
-    const bool in = c * kPer + g < groups;
-    const int64_t i = in ? i0 + g : i0;
-    uint32_t v;
-    if constexpr (kFmt == kMvfMX) v = reinterpret_cast<const uint8_t*>(a.scales)[i];
-    else if (wide) v = reinterpret_cast<const uint32_t*>(a.scales)[i];
-    else v = reinterpret_cast<const uint16_t*>(a.scales)[i];
-    r.s[g] = in ? v : 0u;
-    if constexpr (mv_int(kFmt))
-      if (a.zeros) r.z = (r.z & ~(0xffu << (8 * g))) | ((uint32_t)a.zeros[i] << (8 * g));
+    for (int g = 0; g < kPer; ++g) {
+      // groups beyond the row (x is zero there) read its last one
+      const int i = c * kPer + g < row.groups ? c * kPer + g : row.groups - 1;
+      const int at = row.s + i * row.size;
+      if constexpr (kFmt == kMvfMX)
+        r.s[g] = __builtin_amdgcn_raw_buffer_load_b8(rs, at, 0, 0);
+      else if (!mv_int(kFmt) || row.size == 4)
+        r.s[g] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
+      else
+        r.s[g] = __builtin_amdgcn_raw_buffer_load_b16(rs, at, 0, 0);
+      if constexpr (mv_int(kFmt)) r.z[g] = __builtin_amdgcn_raw_buffer_load_b8(rz, row.z + i, 0, 0);
+    }
   }
+}
+
+// Scale g of a chunk as fp32.
+template <int kFmt, bool kWhole>
+__device__ __forceinline__ float mv_scale(const MvScales<kFmt, kWhole>& r, int g, int dtype) {
+  if constexpr (kFmt == kMvfMX) {  // 2^(raw - 127), 255 is NaN
+    const uint32_t raw = kWhole ? (r.s[0] >> (8 * g)) & 0xffu : r.s[g];
+    return __uint_as_float(raw == 0u ? 0x00400000u : raw == 255u ? 0x7fc00000u : raw << 23);
+  }
+  if (!mv_int(kFmt) || dtype == kF32) return __uint_as_float(r.s[g]);
+  const uint32_t raw = kWhole ? (r.s[g >> 1] >> (16 * (g & 1))) & 0xffffu : r.s[g];
+  return dtype == kBF16 ? bf16_bits_to_f32(raw)
+                        : (float)__builtin_bit_cast(_Float16, (uint16_t)raw);
 }
 
 // Transposes 4 words x 4 lane rows of 16: lane row q, word s <-> lane row s, word q.
@@ -114,46 +148,55 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&d)[4]) {
   d[0] = u[0], d[1] = u[1], d[2] = v[0], d[3] = v[1];
 }
 
-// tot += the products of one chunk of one row tile. Steps beyond the end of the row
-// have x = 0 and a scale of 0.
-template <int kFmt, int kRegs>
+// x of one matrix step: for nf4 each pair of values twice, against the two words of
+// a table entry as they are read.
+template <int kFmt>
+struct MvX {
+  f16x8 v[mv_split(kFmt) ? 2 : 1];
+};
+
+// tot += the products of one chunk of one row tile.  Steps beyond the end of the row
+// have x = 0.
+template <int kFmt, bool kWhole, int kRegs>
 __device__ __forceinline__ void mv_chunk(const MatvecArgs& a, const char* lut, uint32_t lane_off,
-                                         u32x4 w, const MvScales<kFmt>& sc, const f16x8 (&x)[4],
-                                         float (&tot)[kRegs]) {
+                                         u32x4 w, const MvScales<kFmt, kWhole>& sc,
+                                         const MvX<kFmt> (&x)[4], float* tot) {
   uint32_t d[4] = {w.x, w.y, w.z, w.w};
   quad_transpose(d);
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const int g = s * mv_groups(kFmt) / 4;
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // table address: byte j of the codes in bits 8..15, the lane's slot below
-      const uint32_t at =
-          __builtin_amdgcn_perm(d[s], lane_off, 0x0c0c0000u | ((4u + j) << 8));
-      if constexpr (mv_split(kFmt)) {
-        const u32x2 e = *reinterpret_cast<const u32x2*>(lut + at);
-        hi[j] = e.x;
-        lo[j] = e.y;
-      } else {
-        hi[j] = *reinterpret_cast<const uint32_t*>(lut + at);
-      }
-    }
-    if constexpr (mv_int(kFmt)) {
-      const _Float16 z = (_Float16)(float)((sc.z >> (8 * g)) & 0xffu);
-      const f16x2 z2 = {z, z};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) hi[j] = half2_as_u32(u32_as_half2(hi[j]) - z2);
-    }
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    const u32x4 h4 = {hi[0], hi[1], hi[2], hi[3]};
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s], __builtin_bit_cast(f16x8, h4), acc, 0, 0, 0);
+    uint32_t at[4];
+    // table address: byte j of the codes in bits 8..15, the lane's slot below
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      at[j] = __builtin_amdgcn_perm(d[s], lane_off, 0x0c0c0000u | ((4u + j) << 8));
     if constexpr (mv_split(kFmt)) {
-      const u32x4 l4 = {lo[0], lo[1], lo[2], lo[3]};
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s], __builtin_bit_cast(f16x8, l4), acc, 0, 0,
-                                                   0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x2 e = *reinterpret_cast<const u32x2*>(lut + at[2 * h]);
+        const u32x2 f = *reinterpret_cast<const u32x2*>(lut + at[2 * h + 1]);
+        const u32x4 b = {e.x, e.y, f.x, f.y};
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s].v[h], __builtin_bit_cast(f16x8, b), acc,
+                                                     0, 0, 0);
+      }
+    } else {
+      uint32_t b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const uint32_t*>(lut + at[j]);
+      if constexpr (mv_int(kFmt)) {
+        const uint32_t raw = kWhole ? (sc.z[0] >> (8 * g)) & 0xffu : sc.z[g];
+        const _Float16 z = (_Float16)(float)(a.zeros ? raw : 8u);
+        const f16x2 z2 = {z, z};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = half2_as_u32(u32_as_half2(b[j]) - z2);
+      }
+      const u32x4 b4 = {b[0], b[1], b[2], b[3]};
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s].v[0], __builtin_bit_cast(f16x8, b4), acc, 0,
+                                                   0, 0);
     }
-    const float f = mv_value<kFmt>(a, sc.s[g]);
+    const float f = mv_scale<kFmt, kWhole>(sc, g, a.scale_dtype);
 #pragma unroll
     for (int i = 0; i < kRegs; ++i) tot[i] = fmaf(f, acc[i], tot[i]);
   }
@@ -162,9 +205,9 @@ __device__ __forceinline__ void mv_chunk(const MatvecArgs& a, const char* lut, u
 // The matrix unit's x operand of step s of chunk c: row m of the 16 is token
 // (m / 4) kRegs + m % 4 where m % 4 < kRegs, so that the first kRegs result
 // registers of a lane hold all tokens.
-template <int kRegs>
+template <int kFmt, int kRegs>
 __device__ __forceinline__ void mv_load_x(const MatvecArgs& a, int64_t t0, int nt, int c, int lane,
-                                          f16x8 (&x)[4]) {
+                                          MvX<kFmt> (&x)[4]) {
   const int left = a.K - c * kMvChunk;
   const int m = lane & 15, q = lane >> 4;
   const int t = (m >> 2) * kRegs + (m & 3);
@@ -183,7 +226,12 @@ __device__ __forceinline__ void mv_load_x(const MatvecArgs& a, int64_t t0, int n
                           (_Float16)bf16_bits_to_f32(w[i] >> 16));
       v = u32x4{o[0], o[1], o[2], o[3]};
     }
-    x[s] = __builtin_bit_cast(f16x8, v);
+    if constexpr (mv_split(kFmt)) {
+      x[s].v[0] = __builtin_bit_cast(f16x8, (u32x4{v.x, v.x, v.y, v.y}));
+      x[s].v[1] = __builtin_bit_cast(f16x8, (u32x4{v.z, v.z, v.w, v.w}));
+    } else {
+      x[s].v[0] = __builtin_bit_cast(f16x8, v);
+    }
   }
 }
 
@@ -213,88 +261,102 @@ __device__ __forceinline__ void mv_fill(u32x4* lut, uint32_t* stage, int tid) {
 
 }  // namespace
 
-// kCpw: chunks of a wave that stay in registers as x (0: x is read for every
-// tile, any K).
-template <int kFmt, int kRegs, int kCpw>
+// kWhole: rows are whole chunks and a chunk's scales one aligned read.  kRegs:
+// result registers of a lane (1: up to 4 tokens, 4: up to 16).  kCpw: chunks of a wave
+// whose x stays in registers (0: x is read again for every kRows tiles, any K).
+// kRows: tiles between two barriers.
+template <int kFmt, bool kWhole, int kRegs, int kCpw, int kRows>
 __global__ __launch_bounds__(kMvThreads) void matvec_kernel(MatvecArgs a) {
   constexpr int kX = kCpw ? kCpw : 1;
+  constexpr int kOut = kRows * kRegs;  // result registers of a lane between barriers
   __shared__ u32x4 lut[4096];
-  __shared__ float red[2][kMvWaves][kRegs][64];
+  __shared__ float red[2][kMvWaves][kOut][64];
   __shared__ uint32_t stage[16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t t0 = (int64_t)blockIdx.y * kMvTokens;
   const int nt = a.T - t0 < kMvTokens ? (int)(a.T - t0) : kMvTokens;
   const int chunks = (a.K + kMvChunk - 1) / kMvChunk;
-  const bool whole = a.K % kMvChunk == 0;
   const int tiles = (a.N + kMvTile - 1) / kMvTile;
-  const int q = lane >> 4;
+  const int n_lane = lane & 15, q = lane >> 4;
   const uint32_t lane_off = mv_split(kFmt) ? (lane & 31) * 8 : lane * 4;
-  const int64_t row_bytes = a.K / 2;
-  const auto row_of = [&](int tile) {
-    const int n = tile * kMvTile + (lane & 15);
-    return n < a.N ? n : a.N - 1;
+  const int row_bytes = a.K / 2;
+  MvScaleRow sr;
+  sr.groups = a.K / (kMvChunk / mv_groups(kFmt));
+  sr.size = kFmt == kMvfMX ? 1 : !mv_int(kFmt) || a.scale_dtype == kF32 ? 4 : 2;
+  sr.s = n_lane * sr.groups * sr.size;
+  sr.z = n_lane * sr.groups;
+  const uint8_t* zeros = a.zeros ? a.zeros : a.codes;  // read but not used
+
+  MvX<kFmt> x[kX][4];
+  u32x4 w[kRows][kX];
+  MvScales<kFmt, kWhole> sc[kRows][kX];
+  const int lane_w = n_lane * row_bytes + 16 * q;
+
+  // reads chunk c of row tile `tile` (all zeros beyond the last tile)
+  const auto load = [&](int tile, int c, u32x4& wo, MvScales<kFmt, kWhole>& so) {
+    const int64_t n0 = (int64_t)tile * kMvTile;
+    const int64_t rows = a.N - n0 < kMvTile ? a.N - n0 : kMvTile;
+    const Rsrc rw = mv_rsrc(a.codes, n0 * row_bytes, rows * row_bytes);
+    const Rsrc rs = mv_rsrc(a.scales, n0 * sr.groups * sr.size, rows * sr.groups * sr.size);
+    const Rsrc rz = mv_rsrc(zeros, n0 * sr.groups, rows * sr.groups);
+    wo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                       rw, lane_w, c * (kMvChunk / 2), 0));
+    mv_load_scales<kFmt, kWhole>(rs, rz, sr, c, so);
   };
-  // 16 packed bytes of chunk c: the lane's 32 codes, or the row's first where the
-  // row has ended (x is zero there)
-  const auto load_w = [&](int n, int c) {
-    const int at = c * (kMvChunk / 2) + 16 * q;
-    return *reinterpret_cast<const u32x4*>(a.codes + n * row_bytes + (at < row_bytes ? at : 0));
+  const auto chunk_of = [&](int j) {
+    // a wave without a j-th chunk repeats the last one with x = 0
+    const int c = wave + j * kMvWaves;
+    return c < chunks ? c : chunks - 1;
   };
 
-  f16x8 x[kX][4];
-  u32x4 w[kX] = {};
-  MvScales<kFmt> sc[kX] = {};
-  int tile = blockIdx.x;
-  const auto load_tile = [&](int tl) {
-    const int n = row_of(tl);
-#pragma unroll
-    for (int j = 0; j < kX; ++j) {
-      const int c = wave + j * kMvWaves;
-      if (c >= chunks) continue;
-      w[j] = load_w(n, c);
-      mv_load_scales<kFmt>(a, n, c, whole, sc[j]);
-    }
-  };
+  int tile = blockIdx.x * kRows;
   if constexpr (kCpw > 0) {
-    load_tile(tile);
 #pragma unroll
     for (int j = 0; j < kX; ++j)
-      mv_load_x<kRegs>(a, t0, nt, wave + j * kMvWaves, lane, x[j]);
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) load(tile + u, chunk_of(j), w[u][j], sc[u][j]);
+#pragma unroll
+    for (int j = 0; j < kX; ++j)
+      mv_load_x<kFmt, kRegs>(a, t0, nt, wave + j * kMvWaves, lane, x[j]);
   }
   mv_fill<kFmt>(lut, stage, tid);
   const char* table = reinterpret_cast<const char*>(lut);
   const float last = mv_split(kFmt) ? 1.0f / 256.0f : kFmt == kMvfFP4 ? 1.0f / 6.0f : 1.0f;
+  const int step = gridDim.x * kRows;
 
-  for (int buf = 0; tile < tiles; tile += gridDim.x, buf ^= 1) {
-    float tot[kRegs] = {};
+  for (int buf = 0; tile < tiles; tile += step, buf ^= 1) {
+    float tot[kOut] = {};
     if constexpr (kCpw > 0) {
-      u32x4 w1[kX];
-      MvScales<kFmt> sc1[kX];
-#pragma unroll
-      for (int j = 0; j < kX; ++j) w1[j] = w[j], sc1[j] = sc[j];
-      if (tile + (int)gridDim.x < tiles) load_tile(tile + gridDim.x);
 #pragma unroll
       for (int j = 0; j < kX; ++j)
-        mv_chunk<kFmt, kRegs>(a, table, lane_off, w1[j], sc1[j], x[j], tot);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          const u32x4 w1 = w[u][j];
+          const MvScales<kFmt, kWhole> s1 = sc[u][j];
+          load(tile + step + u, chunk_of(j), w[u][j], sc[u][j]);
+          mv_chunk<kFmt, kWhole, kRegs>(a, table, lane_off, w1, s1, x[j], tot + u * kRegs);
+        }
     } else {
-      const int n = row_of(tile);
       for (int c = wave; c < chunks; c += kMvWaves) {
-        const u32x4 wc = load_w(n, c);
-        MvScales<kFmt> s;
-        mv_load_scales<kFmt>(a, n, c, whole, s);
-        mv_load_x<kRegs>(a, t0, nt, c, lane, x[0]);
-        mv_chunk<kFmt, kRegs>(a, table, lane_off, wc, s, x[0], tot);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) load(tile + u, c, w[u][0], sc[u][0]);
+        mv_load_x<kFmt, kRegs>(a, t0, nt, c, lane, x[0]);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+          mv_chunk<kFmt, kWhole, kRegs>(a, table, lane_off, w[u][0], sc[u][0], x[0],
+                                        tot + u * kRegs);
       }
     }
 #pragma unroll
-    for (int i = 0; i < kRegs; ++i) red[buf][wave][i][lane] = tot[i];
-    __syncthreads();  // red[buf] is written again two tiles on, after the next barrier
-    if (wave < kRegs) {
+    for (int i = 0; i < kOut; ++i) red[buf][wave][i][lane] = tot[i];
+    __syncthreads();  // red[buf] is written again two rounds on, after the next barrier
+    if (wave < kOut) {
       float v = 0.f;
 #pragma unroll
       for (int u = 0; u < kMvWaves; ++u) v += red[buf][u][wave][lane];
-      const int t = q * kRegs + wave, n = tile * kMvTile + (lane & 15);
+      const int t = q * kRegs + wave % kRegs;
+      const int64_t n = (int64_t)(tile + wave / kRegs) * kMvTile + n_lane;
       if (t < nt && n < a.N) {
         v = v * last + (a.bias ? a.bias[n] : 0.f);
         const int64_t i = (t0 + t) * a.N + n;
@@ -308,42 +370,54 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(MatvecArgs a) {
 
 namespace {
 
-template <int kFmt, int kRegs>
-void mv_launch(const MatvecArgs& a, dim3 grid, hipStream_t s) {
+template <int kFmt, bool kWhole, int kRegs, int kCpw, int kRows>
+void mv_go(const MatvecArgs& a, int nx, unsigned ny, hipStream_t s) {
+  hipLaunchKernelGGL((matvec_kernel<kFmt, kWhole, kRegs, kCpw, kRows>), dim3((unsigned)nx, ny),
+                     dim3(kMvThreads), 0, s, a);
+}
+
+template <int kFmt, bool kWhole, int kRegs>
+void mv_launch(const MatvecArgs& a, int cus, hipStream_t s) {
+  constexpr int kMany = kRegs == 1 ? 4 : 2;
+  const unsigned ny = (unsigned)((a.T + kMvTokens - 1) / kMvTokens);
+  const int tiles = (a.N + kMvTile - 1) / kMvTile;
+  // one workgroup per compute unit, shared by the token blocks; a multiple of 8, so
+  // that the blocks of one tile run on the same XCD and share its L2
+  int nx = cus / (int)ny / 8 * 8;
+  if (nx < 8) nx = 8;
+  const bool many = tiles >= 2 * kMany * nx;
+  const int rounds = many ? (tiles + kMany - 1) / kMany : tiles;
+  if (nx > rounds) nx = rounds;
   const int per = (a.K + kMvChunk * kMvWaves - 1) / (kMvChunk * kMvWaves);
-  if (per <= 1)
-    hipLaunchKernelGGL((matvec_kernel<kFmt, kRegs, 1>), grid, dim3(kMvThreads), 0, s, a);
-  else if (per <= 2)
-    hipLaunchKernelGGL((matvec_kernel<kFmt, kRegs, 2>), grid, dim3(kMvThreads), 0, s, a);
-  else if (per <= 4)
-    hipLaunchKernelGGL((matvec_kernel<kFmt, kRegs, 4>), grid, dim3(kMvThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((matvec_kernel<kFmt, kRegs, 0>), grid, dim3(kMvThreads), 0, s, a);
+  if (per <= 1 && many) mv_go<kFmt, kWhole, kRegs, 1, kMany>(a, nx, ny, s);
+  else if (per <= 1) mv_go<kFmt, kWhole, kRegs, 1, 1>(a, nx, ny, s);
+  else if (per <= 2) mv_go<kFmt, kWhole, kRegs, 2, 1>(a, nx, ny, s);
+  else if (many) mv_go<kFmt, kWhole, kRegs, 0, kMany>(a, nx, ny, s);
+  else mv_go<kFmt, kWhole, kRegs, 0, 1>(a, nx, ny, s);
 }
 
 template <int kFmt>
-void mv_launch_rows(const MatvecArgs& a, dim3 grid, hipStream_t s) {
-  if (a.T <= 4) mv_launch<kFmt, 1>(a, grid, s);
-  else mv_launch<kFmt, 4>(a, grid, s);
+void mv_launch_format(const MatvecArgs& a, int cus, hipStream_t s) {
+  constexpr int kPer = mv_groups(kFmt);
+  const int size = kFmt == kMvfMX ? 1 : !mv_int(kFmt) || a.scale_dtype == kF32 ? 4 : 2;
+  const int read = kPer * size < 4 ? kPer * size : 4;
+  const bool whole = a.K % kMvChunk == 0 && (uintptr_t)a.scales % read == 0 &&
+                     (uintptr_t)a.zeros % kPer == 0;
+  if (whole && a.T <= 4) mv_launch<kFmt, true, 1>(a, cus, s);
+  else if (whole) mv_launch<kFmt, true, 4>(a, cus, s);
+  else if (a.T <= 4) mv_launch<kFmt, false, 1>(a, cus, s);
+  else mv_launch<kFmt, false, 4>(a, cus, s);
 }
 
 }  // namespace
 
 hipError_t launch_matvec(const MatvecArgs& a, int num_cus, hipStream_t s) {
-  const unsigned ny = (unsigned)((a.T + kMvTokens - 1) / kMvTokens);
-  const int tiles = (a.N + kMvTile - 1) / kMvTile;
-  // one workgroup per compute unit, shared by the token blocks; a multiple of 8, so
-  // that the blocks of one tile run on the same XCD and share its L2
-  int nx = num_cus / (int)ny / 8 * 8;
-  if (nx < 8) nx = 8;
-  if (nx > tiles) nx = tiles;
-  const dim3 grid((unsigned)nx, ny);
-  if (a.qt == kMvNF4) mv_launch_rows<kMvfNF4>(a, grid, s);
-  else if (a.qt == kMvFP4) mv_launch_rows<kMvfFP4>(a, grid, s);
-  else if (a.qt == kMvMXFP4) mv_launch_rows<kMvfMX>(a, grid, s);
-  else if (a.group == 32) mv_launch_rows<kMvfInt32>(a, grid, s);
-  else if (a.group == 64) mv_launch_rows<kMvfInt64>(a, grid, s);
-  else mv_launch_rows<kMvfInt128>(a, grid, s);
+  if (a.qt == kMvNF4) mv_launch_format<kMvfNF4>(a, num_cus, s);
+  else if (a.qt == kMvFP4) mv_launch_format<kMvfFP4>(a, num_cus, s);
+  else if (a.qt == kMvMXFP4) mv_launch_format<kMvfMX>(a, num_cus, s);
+  else if (a.group == 32) mv_launch_format<kMvfInt32>(a, num_cus, s);
+  else if (a.group == 64) mv_launch_format<kMvfInt64>(a, num_cus, s);
+  else mv_launch_format<kMvfInt128>(a, num_cus, s);
   return hipGetLastError();
 }
 

@@ -525,7 +525,7 @@ int moe_expert_forward_routing(void* workspace, int64_t T, int H, int I,
  * better call.  No workspace.  The order of the sums depends on the sizes only:
  * results are the same from call to call.
  * Alignment (else EINVAL): x and codes 16 bytes, scales, bias and y their
- * element.  T beyond NF4MOE_MATVEC_MAX_T, N beyond 2^31 - 65 or K beyond 2^30 ->
+ * element.  T beyond NF4MOE_MATVEC_MAX_T, N beyond 2^31 - 65 or K beyond 2^24 ->
  * EOVERFLOW. */
 #define NF4MOE_QT_INT4 2  /* nbit_matvec only */
 #define NF4MOE_QT_MXFP4 7 /* nbit_matvec only */

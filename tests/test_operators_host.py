@@ -34,7 +34,7 @@ MATVEC = dict(qt=0, x=FAKE, xd=2, T=1, codes=FAKE, scales=FAKE, sd=0, zeros=None
     (-3, dict(qt=7)), (-1, dict(zeros=FAKE)), (-1, dict(qt=7, group=32, zeros=FAKE)),
     (-5, dict(sd=1)), (-5, dict(qt=2, sd=7)), (-2, dict(K=96)), (-2, dict(qt=7, group=32, K=48)),
     (-2, dict(qt=2, group=128, K=192)), (-7, dict(T=262145)), (-7, dict(N=1 << 31)),
-    (-7, dict(K=(1 << 30) + 64)), (-1, dict(x=FAKE + 8)), (-1, dict(codes=FAKE + 4)),
+    (-7, dict(K=(1 << 24) + 64)), (-1, dict(x=FAKE + 8)), (-1, dict(codes=FAKE + 4)),
     (-1, dict(scales=FAKE + 2)), (-1, dict(bias=FAKE + 2)), (-1, dict(y=FAKE + 1)),
     (-1, dict(qt=2, sd=2, scales=FAKE + 1))])
 def test_matvec_refuses(lib, status, changes):
