@@ -3,10 +3,17 @@
 //   z = y * rstd(y) * (w_post + off),  r = beta * residual + alpha * gate * z,
 //   h = r * rstd(r) * (w_pre + off),   rstd(v) = 1 / sqrt(mean(v^2) + eps).
 //
-// One workgroup holds one row: a thread has eight consecutive columns (or two
-// such vectors beyond 8192 columns) in fp32 registers, so every matrix is read
-// once and written once; the row sums go through the waves and LDS.  r is rounded
-// to its type before it is normalised, so h follows from what is stored.
+// Bound by memory: every matrix is read once and written once.  The waves of a
+// row hold it in registers, eight consecutive columns a lane (sixteen beyond 8192
+// columns): few registers, so that sixteen waves and their reads are in flight on a
+// compute unit.  All of a row's reads are issued together, before any of them is converted; they go through
+// buffer bounds, so that columns and rows beyond the end need no branch between
+// them.  r is rounded to its type before it is normalised, so h follows from what
+// is stored.
+//
+// The backward's sums over T stay in registers over a workgroup's rows, are added over
+// its waves in LDS and go to one partial row a workgroup; a second kernel adds
+// the partial rows.
 
 #include "common.h"
 #include "launch.h"
@@ -16,25 +23,54 @@ namespace nf4moe {
 namespace {
 
 constexpr int kNormGroups = 512;  // workgroups (and partial rows) of the backward
+constexpr int kNormWaves = 8;     // waves of a workgroup of several rows
+constexpr int kNormMaxWaves = 16;  // waves of a workgroup of one row
 
-// Eight consecutive elements from element idx (a multiple of 8; rows are
-// 16-byte aligned).
-__device__ __forceinline__ void load8(const void* p, int dtype, int64_t idx, float (&v)[8]) {
-  if (dtype == kF32) {
-    const f32x4* q = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p) + idx);
-    const f32x4 a = q[0], b = q[1];
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+
+// Eight consecutive elements as they are read; kBytes is an element's size.
+template <int kBytes>
+struct Raw8 {
+  u32x4 v[kBytes / 2];
+};
+
+// `bytes` bytes at p: reads beyond them return 0, writes are dropped.
+__device__ __forceinline__ Rsrc span_of(const void* p, int64_t offset, int bytes) {
+  char* at = const_cast<char*>(reinterpret_cast<const char*>(p)) + offset;
+  return __builtin_amdgcn_make_buffer_rsrc(at, 0, bytes, 0x00020000);
+}
+
+__device__ __forceinline__ u32x4 read16(Rsrc r, int offset) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
+}
+
+template <int kBytes>
+__device__ __forceinline__ void fetch8(Rsrc r, int col, Raw8<kBytes>& o) {
+  o.v[0] = read16(r, col * kBytes);
+  if constexpr (kBytes == 4) o.v[1] = read16(r, col * 4 + 16);
+}
+
+// Weights of either size: the second half of 16-bit ones is read beyond the end.
+__device__ __forceinline__ void fetch8_any(Rsrc r, int size, int col, Raw8<4>& o) {
+  o.v[0] = read16(r, col * size);
+  o.v[1] = read16(r, size == 4 ? col * 4 + 16 : 0x7ffffff0);
+}
+
+template <int kBytes>
+__device__ __forceinline__ void widen8(const Raw8<kBytes>& r, int dtype, float (&v)[8]) {
+  if (kBytes == 4 && dtype == kF32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-    return;
-  }
-  const u32x4 q = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(p) + idx);
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.v[kBytes / 2 * i / 8][i & 3]);
+  } else if (dtype == kBF16) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (dtype == kBF16) {
-      v[2 * i] = bf16_bits_to_f32(q[i] & 0xffffu);
-      v[2 * i + 1] = bf16_bits_to_f32(q[i] >> 16);
-    } else {
-      const f16x2 h = u32_as_half2(q[i]);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(r.v[0][i] << 16);
+      v[2 * i + 1] = __uint_as_float(r.v[0][i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f16x2 h = u32_as_half2(r.v[0][i]);
       v[2 * i] = (float)h.x;
       v[2 * i + 1] = (float)h.y;
     }
@@ -42,14 +78,17 @@ __device__ __forceinline__ void load8(const void* p, int dtype, int64_t idx, flo
 }
 
 // Rounds v to dtype, stores it and leaves the stored values in v.
-__device__ __forceinline__ void store8(void* p, int dtype, int64_t idx, float (&v)[8]) {
+__device__ __forceinline__ void write8(Rsrc r, int dtype, int col, float (&v)[8]) {
+  u32x4 q;
   if (dtype == kF32) {
-    f32x4* q = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + idx);
-    q[0] = f32x4{v[0], v[1], v[2], v[3]};
-    q[1] = f32x4{v[4], v[5], v[6], v[7]};
+    const u32x4 a = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                     __float_as_uint(v[3])};
+    const u32x4 b = {__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                     __float_as_uint(v[7])};
+    __builtin_amdgcn_raw_buffer_store_b128(a, r, col * 4, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(b, r, col * 4 + 16, 0, 0);
     return;
   }
-  u32x4 q;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (dtype == kBF16) {
@@ -64,26 +103,46 @@ __device__ __forceinline__ void store8(void* p, int dtype, int64_t idx, float (&
       v[2 * i + 1] = (float)b;
     }
   }
-  *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p) + idx) = q;
+  __builtin_amdgcn_raw_buffer_store_b128(q, r, col * 2, 0, 0);
 }
 
-// Sums of kN values over the workgroup, in every thread.  `red` holds kN * 16
-// floats; the caller alternates between two of them from call to call.
-template <int kN>
-__device__ __forceinline__ void block_sum(float (&v)[kN], float* red) {
-  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+// How the waves of a workgroup share rows: kRowWaves waves a row in workgroups of
+// kNormWaves, or (kRowWaves 0) all waves of a workgroup of any size.
+template <int kRowWaves>
+struct NormShape {
+  static constexpr int kRows = kRowWaves ? kNormWaves / kRowWaves : 1;
+  static constexpr int kWaves = kRowWaves ? kNormWaves : kNormMaxWaves;
+  int lane, sub, part, row_waves;  // sub: row of the workgroup; part: wave of the row
+  __device__ NormShape() {
+    lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    row_waves = kRowWaves ? kRowWaves : blockDim.x >> 6;
+    sub = kRowWaves ? wave / row_waves : 0;
+    part = wave - sub * row_waves;
+  }
+  __device__ int col(int u) const { return ((u * row_waves + part) * 64 + lane) * 8; }
+};
+
+// Sums of kN values over the waves of a row, in every lane.  A barrier has to come
+// between two uses of `red`.
+template <int kN, int kRowWaves>
+__device__ __forceinline__ void row_sum(float (&v)[kN],
+                                        float (&red)[3][NormShape<kRowWaves>::kWaves],
+                                        const NormShape<kRowWaves>& at) {
 #pragma unroll
   for (int i = 0; i < kN; ++i) v[i] = wave_sum(v[i]);
-  if (waves == 1) return;
-  if ((threadIdx.x & 63) == 0)
+  if constexpr (kRowWaves != 1) {
+    const int first = at.sub * at.row_waves;
+    if (at.lane == 0)
 #pragma unroll
-    for (int i = 0; i < kN; ++i) red[i * 16 + wave] = v[i];
-  __syncthreads();
+      for (int i = 0; i < kN; ++i) red[i][first + at.part] = v[i];
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    float s = 0.f;
-    for (int w = 0; w < waves; ++w) s += red[i * 16 + w];
-    v[i] = s;
+    for (int i = 0; i < kN; ++i) {
+      float s = 0.f;
+      for (int w = 0; w < at.row_waves; ++w) s += red[i][first + w];
+      v[i] = s;
+    }
   }
 }
 
@@ -94,220 +153,332 @@ __device__ __forceinline__ float rstd_of(float sum, int H, float eps) {
 
 }  // namespace
 
-template <int kVec>
-__global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs a) {
-  __shared__ float red[2][16];
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-  const int64_t row = t * a.H;
-  float r[kVec][8], z[kVec][8], wv[8];
+// kRes, kY: element sizes of the residual and of y (2 where there is none).
+template <int kRes, int kY, int kVec, int kRowWaves>
+__global__ __launch_bounds__(64 * NormShape<kRowWaves>::kWaves) void block_norm_kernel(BlockNormArgs a) {
+  const NormShape<kRowWaves> at;
+  __shared__ float red[2][3][at.kWaves];
+  constexpr int kRows = at.kRows;
+  const int ws = a.w_dtype == kF32 ? 4 : 2;
+  const Rsrc r_pre = span_of(a.w_pre, 0, a.w_pre ? a.H * ws : 0);
+  const Rsrc r_post = span_of(a.w_post, 0, a.w_post ? a.H * ws : 0);
+  const Rsrc r_gate = span_of(a.gate, 0, a.gate_axis == 2 ? a.H * 4 : 0);
+  const int hs = a.h_dtype == kF32 ? 4 : 2;
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.T;
+       first += (int64_t)gridDim.x * kRows) {
+    // the waves of a row beyond the last take part in the barriers only
+    const int64_t t = first + at.sub;
+    const bool live = t < a.T;
+    const int n = live ? a.H : 0;
+    const int64_t row = live ? t * a.H : 0;
+    const Rsrc r_res = span_of(a.residual, row * kRes, n * kRes);
+    const Rsrc r_y = span_of(a.y, row * kY, a.y ? n * kY : 0);
+    Raw8<kRes> r0[kVec];
+    Raw8<kY> y0[kVec];
+    Raw8<4> w0[kVec], w1[kVec], g0[kVec];
 #pragma unroll
-  for (int u = 0; u < kVec; ++u) {
-    const int c = (threadIdx.x + u * blockDim.x) * 8;
+    for (int u = 0; u < kVec; ++u) {
+      fetch8<kY>(r_y, at.col(u), y0[u]);
+      fetch8<kRes>(r_res, at.col(u), r0[u]);
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[u][i] = z[u][i] = 0.f;
-    if (c >= a.H) continue;
-    load8(a.residual, a.res_dtype, row + c, r[u]);
-    if (a.y) load8(a.y, a.y_dtype, row + c, z[u]);
-  }
-  if (a.y) {
-    float rstd = 1.f;
-    if (a.w_post) {
+    for (int u = 0; u < kVec; ++u) {
+      fetch8_any(r_post, ws, at.col(u), w0[u]);
+      fetch8_any(r_pre, ws, at.col(u), w1[u]);
+      if (a.gate_axis == 2) fetch8<4>(r_gate, at.col(u), g0[u]);
+    }
+    float gt = a.alpha;
+    if (a.gate_axis == 1 && live) gt *= a.gate[t];
+    float r[kVec][8], z[kVec][8], wv[8];
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+      widen8<kRes>(r0[u], a.res_dtype, r[u]);
+      widen8<kY>(y0[u], a.y_dtype, z[u]);
+    }
+    if (a.y) {
+      float rstd = 1.f;
+      if (a.w_post) {
+        float s[1] = {0.f};
+#pragma unroll
+        for (int u = 0; u < kVec; ++u)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[0] += z[u][i] * z[u][i];
+        row_sum<1, kRowWaves>(s, red[0], at);
+        rstd = rstd_of(s[0], a.H, a.eps);
+      }
+      const Rsrc r_out = span_of(a.r_out, row * kRes, n * kRes);
+#pragma unroll
+      for (int u = 0; u < kVec; ++u) {
+        if (a.w_post) {
+          widen8<4>(w0[u], a.w_dtype, wv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[u][i] *= rstd * (wv[i] + a.w_offset);
+        }
+        if (a.gate_axis == 2) {
+          widen8<4>(g0[u], kF32, wv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[u][i] *= wv[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[u][i] = a.beta * r[u][i] + gt * z[u][i];
+        write8(r_out, a.res_dtype, at.col(u), r[u]);
+      }
+    }
+    if (a.w_pre) {
       float s[1] = {0.f};
 #pragma unroll
       for (int u = 0; u < kVec; ++u)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] += z[u][i] * z[u][i];
-      block_sum(s, red[0]);
-      rstd = rstd_of(s[0], a.H, a.eps);
-    }
-    const float gt = a.gate_axis == 1 ? a.alpha * a.gate[t] : a.alpha;
+        for (int i = 0; i < 8; ++i) s[0] += r[u][i] * r[u][i];
+      row_sum<1, kRowWaves>(s, red[1], at);
+      const float rstd = rstd_of(s[0], a.H, a.eps);
+      const Rsrc r_h = span_of(a.h, row * hs, n * hs);
 #pragma unroll
-    for (int u = 0; u < kVec; ++u) {
-      const int c = (threadIdx.x + u * blockDim.x) * 8;
-      if (c >= a.H) continue;
-      if (a.w_post) {
-        load8(a.w_post, a.w_dtype, c, wv);
+      for (int u = 0; u < kVec; ++u) {
+        widen8<4>(w1[u], a.w_dtype, wv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[u][i] *= rstd * (wv[i] + a.w_offset);
+        for (int i = 0; i < 8; ++i) r[u][i] = r[u][i] * rstd * (wv[i] + a.w_offset);
+        write8(r_h, a.h_dtype, at.col(u), r[u]);
       }
-      if (a.gate_axis == 2) {
-        for (int i = 0; i < 8; ++i) z[u][i] *= a.gate[c + i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[u][i] = a.beta * r[u][i] + gt * z[u][i];
-      store8(a.r_out, a.res_dtype, row + c, r[u]);
     }
-  }
-  if (!a.w_pre) {
-    __syncthreads();  // the sums' LDS is written again for the next row
-    continue;
-  }
-  float s[1] = {0.f};
-#pragma unroll
-  for (int u = 0; u < kVec; ++u)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[0] += r[u][i] * r[u][i];
-  block_sum(s, red[1]);
-  const float rstd = rstd_of(s[0], a.H, a.eps);
-#pragma unroll
-  for (int u = 0; u < kVec; ++u) {
-    const int c = (threadIdx.x + u * blockDim.x) * 8;
-    if (c >= a.H) continue;
-    load8(a.w_pre, a.w_dtype, c, wv);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[u][i] = r[u][i] * rstd * (wv[i] + a.w_offset);
-    store8(a.h, a.h_dtype, row + c, r[u]);
-  }
-  __syncthreads();
+    if constexpr (kRowWaves != 1) __syncthreads();  // `red` is written again for the next row
   }
 }
 
-// A workgroup takes rows blockIdx.x, blockIdx.x + gridDim.x, ...; its sums over
-// them of the column gradients stay in registers and go to row blockIdx.x of the
-// partial sums (dw_pre, dw_post, dgate by channel).
-template <int kVec>
-__global__ __launch_bounds__(1024) void block_norm_bwd_kernel(BlockNormArgs a) {
-  __shared__ float red[2][3 * 16];
-  __shared__ float red_g[2 * 16];
+// A workgroup takes rows in turn with the others; its sums over them of the column
+// gradients go to row blockIdx.x of the partial sums (dw_pre, dw_post, dgate
+// by channel).  kDh: element size of dh (2 where there is none).
+template <int kRes, int kY, int kDh, int kVec, int kRowWaves>
+__global__ __launch_bounds__(64 * NormShape<kRowWaves>::kWaves, 4) void block_norm_bwd_kernel(BlockNormArgs a) {
+  const NormShape<kRowWaves> at;
+  constexpr int kRows = at.kRows, kCols = kVec * kRowWaves * 512;
+  __shared__ float red[2][3][at.kWaves];
+  // partial sums of the waves that share columns
+  __shared__ f32x4 all[kRows > 1 ? kRows / 2 : 1][kRows > 1 ? kCols / 4 : 1];
+  const int ws = a.w_dtype == kF32 ? 4 : 2;
+  const Rsrc r_pre = span_of(a.w_pre, 0, a.w_pre ? a.H * ws : 0);
+  const Rsrc r_post = span_of(a.w_post, 0, a.w_post ? a.H * ws : 0);
+  const Rsrc r_gate = span_of(a.gate, 0, a.gate_axis == 2 ? a.H * 4 : 0);
   float s_pre[kVec][8] = {}, s_post[kVec][8] = {}, s_gate[kVec][8] = {};
   const float inv_h = 1.0f / (float)a.H;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const int64_t row = t * a.H;
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.T;
+       first += (int64_t)gridDim.x * kRows) {
+    const int64_t t = first + at.sub;
+    const bool live = t < a.T;
+    const int n = live ? a.H : 0;
+    const int64_t row = live ? t * a.H : 0;
+    const Rsrc r_r = span_of(a.residual, row * kRes, a.w_pre ? n * kRes : 0);
+    const Rsrc r_dh = span_of(a.dh, row * kDh, a.dh ? n * kDh : 0);
+    const Rsrc r_d = span_of(a.d_r_out, row * kRes, a.d_r_out ? n * kRes : 0);
+    const Rsrc r_y = span_of(a.y, row * kY, a.y ? n * kY : 0);
+    Raw8<kRes> r0[kVec], d0[kVec];
+    Raw8<kY> y0[kVec];
+    Raw8<kDh> h0[kVec];
+    Raw8<4> w0[kVec], w1[kVec], g0[kVec];
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+      fetch8<kRes>(r_r, at.col(u), r0[u]);
+      fetch8<kDh>(r_dh, at.col(u), h0[u]);
+      fetch8<kY>(r_y, at.col(u), y0[u]);
+      fetch8<kRes>(r_d, at.col(u), d0[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+      fetch8_any(r_pre, ws, at.col(u), w1[u]);
+      fetch8_any(r_post, ws, at.col(u), w0[u]);
+      if (a.gate_axis == 2) fetch8<4>(r_gate, at.col(u), g0[u]);
+    }
+    float gt = a.alpha;
+    if (a.gate_axis == 1 && live) gt *= a.gate[t];
     float r[kVec][8], d[kVec][8], y[kVec][8], g[kVec][8], wv[8];
     float s[3] = {0.f, 0.f, 0.f};  // r^2, dh * w * r, y^2
 #pragma unroll
     for (int u = 0; u < kVec; ++u) {
-      const int c = (threadIdx.x + u * blockDim.x) * 8;
+      widen8<kRes>(r0[u], a.res_dtype, r[u]);
+      widen8<kDh>(h0[u], a.h_dtype, g[u]);
+      widen8<kY>(y0[u], a.y_dtype, y[u]);
+      widen8<4>(w1[u], a.w_dtype, wv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r[u][i] = d[u][i] = y[u][i] = g[u][i] = 0.f;
-      if (c >= a.H) continue;
-      if (a.w_pre) {
-        load8(a.residual, a.res_dtype, row + c, r[u]);
-        load8(a.dh, a.h_dtype, row + c, g[u]);
-        load8(a.w_pre, a.w_dtype, c, wv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s[0] += r[u][i] * r[u][i];
-          s[1] += g[u][i] * (wv[i] + a.w_offset) * r[u][i];
-        }
-      }
-      if (a.d_r_out) load8(a.d_r_out, a.res_dtype, row + c, d[u]);
-      if (a.y) {
-        load8(a.y, a.y_dtype, row + c, y[u]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[2] += y[u][i] * y[u][i];
+      for (int i = 0; i < 8; ++i) {
+        s[0] += r[u][i] * r[u][i];
+        s[1] += g[u][i] * (wv[i] + a.w_offset) * r[u][i];
+        s[2] += y[u][i] * y[u][i];
       }
     }
-    block_sum(s, red[0]);
-    const float rstd_r = rstd_of(s[0], a.H, a.eps);
+    row_sum<3, kRowWaves>(s, red[0], at);
+    // without w_pre (or a row) r and dh are zero here, and so is all they give
+    const float rstd_r = a.w_pre && live ? rstd_of(s[0], a.H, a.eps) : 0.f;
     const float k_r = rstd_r * rstd_r * rstd_r * (s[1] * inv_h);
-    const float rstd_y = a.w_post ? rstd_of(s[2], a.H, a.eps) : 1.f;
-    const float gt = a.gate_axis == 1 ? a.alpha * a.gate[t] : a.alpha;
+    const float rstd_y = !a.w_post ? 1.f : live ? rstd_of(s[2], a.H, a.eps) : 0.f;
     float s2[2] = {0.f, 0.f};  // dz * w * y, dr * z
+    const Rsrc r_out = span_of(a.r_out, row * kRes, n * kRes);
 #pragma unroll
     for (int u = 0; u < kVec; ++u) {
-      const int c = (threadIdx.x + u * blockDim.x) * 8;
-      if (c >= a.H) continue;
-      if (a.w_pre) {
-        load8(a.w_pre, a.w_dtype, c, wv);
+      widen8<kRes>(d0[u], a.res_dtype, d[u]);
+      widen8<4>(w1[u], a.w_dtype, wv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s_pre[u][i] += g[u][i] * r[u][i] * rstd_r;
-          d[u][i] += rstd_r * g[u][i] * (wv[i] + a.w_offset) - r[u][i] * k_r;
-        }
+      for (int i = 0; i < 8; ++i) {
+        s_pre[u][i] += g[u][i] * r[u][i] * rstd_r;
+        d[u][i] += rstd_r * g[u][i] * (wv[i] + a.w_offset) - r[u][i] * k_r;
+        // d is dr; r becomes dresidual
+        r[u][i] = a.beta * d[u][i];
       }
-      // d is dr; r becomes dresidual, g the gradient dz of z
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[u][i] = a.beta * d[u][i];
-      store8(a.r_out, a.res_dtype, row + c, r[u]);
+      write8(r_out, a.res_dtype, at.col(u), r[u]);
       if (!a.y) continue;
-      if (a.w_post) load8(a.w_post, a.w_dtype, c, wv);
+      widen8<4>(w0[u], a.w_dtype, wv);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float w = a.w_post ? wv[i] + a.w_offset : 1.f;
         const float z = y[u][i] * rstd_y * w;
-        g[u][i] = gt * d[u][i];
-        if (a.gate_axis == 2) {
-          s_gate[u][i] += a.alpha * d[u][i] * z;
-          g[u][i] *= a.gate[c + i];
-        }
-        s2[0] += g[u][i] * w * y[u][i];
         s2[1] += d[u][i] * z;
+        s_gate[u][i] += a.alpha * d[u][i] * z;
+        // g becomes the gradient dz of z
+        g[u][i] = gt * d[u][i];
+        if (a.gate_axis == 2) g[u][i] *= __uint_as_float(g0[u].v[i >> 2][i & 3]);
         s_post[u][i] += g[u][i] * y[u][i] * rstd_y;
         g[u][i] *= w;
+        s2[0] += g[u][i] * y[u][i];
       }
     }
     if (a.y) {
-      block_sum(s2, red_g);
-      if (a.gate_axis == 1 && threadIdx.x == 0) a.dgate[t] = a.alpha * s2[1];
+      row_sum<2, kRowWaves>(s2, red[1], at);
+      if (a.gate_axis == 1 && live && at.part == 0 && at.lane == 0) a.dgate[t] = a.alpha * s2[1];
       const float k_y = a.w_post ? rstd_y * rstd_y * rstd_y * (s2[0] * inv_h) : 0.f;
+      const Rsrc r_dy = span_of(a.h, row * kY, n * kY);
 #pragma unroll
       for (int u = 0; u < kVec; ++u) {
-        const int c = (threadIdx.x + u * blockDim.x) * 8;
-        if (c >= a.H) continue;
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[u][i] = rstd_y * g[u][i] - y[u][i] * k_y;
-        store8(a.h, a.y_dtype, row + c, g[u]);
+        write8(r_dy, a.y_dtype, at.col(u), g[u]);
       }
     }
-    __syncthreads();  // the sums' LDS is written again for the next row
+    if constexpr (kRowWaves != 1) __syncthreads();  // `red` is written again for the next row
   }
-  float* part = a.part + (int64_t)blockIdx.x * a.H;
-  const int64_t plane = (int64_t)gridDim.x * a.H;
+  // the sums of waves that share columns, in halves: the upper half hands over
+  const auto join = [&](float (&v)[kVec][8]) {
 #pragma unroll
-  for (int u = 0; u < kVec; ++u) {
-    const int c = (threadIdx.x + u * blockDim.x) * 8;
-    if (c >= a.H) continue;
-    if (a.w_pre) store8(part, kF32, c, s_pre[u]);
-    if (a.w_post) store8(part + plane, kF32, c, s_post[u]);
-    if (a.gate_axis == 2) store8(part + 2 * plane, kF32, c, s_gate[u]);
+    for (int half = kRows / 2; half > 0; half /= 2) {
+      __syncthreads();
+      if (at.sub >= half && at.sub < 2 * half)
+#pragma unroll
+        for (int u = 0; u < kVec; ++u) {
+          f32x4* o = &all[at.sub - half][at.col(u) / 4];
+          o[0] = f32x4{v[u][0], v[u][1], v[u][2], v[u][3]};
+          o[1] = f32x4{v[u][4], v[u][5], v[u][6], v[u][7]};
+        }
+      __syncthreads();
+      if (at.sub < half)
+#pragma unroll
+        for (int u = 0; u < kVec; ++u) {
+          const f32x4 *o = &all[at.sub][at.col(u) / 4], p = o[0], q = o[1];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u][i] += p[i], v[u][4 + i] += q[i];
+        }
+    }
+  };
+  const auto put = [&](float (&v)[kVec][8], int p) {
+    join(v);
+    const int64_t row = ((int64_t)p * gridDim.x + blockIdx.x) * a.H;
+    const Rsrc r_part = span_of(a.part, row * 4, at.sub == 0 ? a.H * 4 : 0);
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) write8(r_part, kF32, at.col(u), v[u]);
+  };
+  if (a.w_pre) put(s_pre, 0);
+  if (a.w_post) put(s_post, 1);
+  if (a.gate_axis == 2) put(s_gate, 2);
+}
+
+// out[c] = sum over the partial rows: 16 lanes of four columns, the 16 x 4 row
+// classes of a workgroup each in order, then joined in order.
+__global__ __launch_bounds__(1024) void block_norm_reduce_kernel(BlockNormArgs a, int groups) {
+  __shared__ f32x4 red[64][16];
+  const int plane = blockIdx.y;
+  float* out = plane == 0 ? a.dw_pre : plane == 1 ? a.dw_post : a.dgate;
+  if (plane == 0 ? !a.w_pre : plane == 1 ? !a.w_post : a.gate_axis != 2) return;
+  const int q = threadIdx.x & 15, k = threadIdx.x >> 4;
+  const int c = (blockIdx.x * 16 + q) * 4;
+  const float* p = a.part + (int64_t)plane * groups * a.H + c;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (c < a.H)
+    for (int i = k; i < groups; i += 64) s += *reinterpret_cast<const f32x4*>(p + (int64_t)i * a.H);
+  red[k][q] = s;
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    // thread (column lane, word) of the 64 columns
+    const int col = blockIdx.x * 64 + threadIdx.x;
+    float v = 0.f;
+    for (int i = 0; i < 64; ++i) v += red[i][threadIdx.x >> 2][threadIdx.x & 3];
+    if (col < a.H) out[col] = v;
   }
-}
-
-// out[c] = sum over the partial rows, one thread a column.
-__global__ __launch_bounds__(64) void block_norm_reduce_kernel(BlockNormArgs a, int groups) {
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  float* out = blockIdx.y == 0 ? a.dw_pre : blockIdx.y == 1 ? a.dw_post : a.dgate;
-  if (blockIdx.y == 0 && !a.w_pre) return;
-  if (blockIdx.y == 1 && !a.w_post) return;
-  if (blockIdx.y == 2 && a.gate_axis != 2) return;
-  if (c >= a.H) return;
-  const float* p = a.part + (int64_t)blockIdx.y * groups * a.H + c;
-  float s = 0.f;
-  for (int i = 0; i < groups; ++i) s += p[(int64_t)i * a.H];
-  out[c] = s;
-}
-
-int block_norm_groups(int64_t T, int H) {
-  (void)H;
-  return (int)(T < kNormGroups ? T : kNormGroups);
 }
 
 namespace {
-// threads of a workgroup that holds a row: eight columns each, two vectors
-// a thread where one would need more than 1024 threads
-int norm_threads(int H, int vec) { return (H / 8 + 64 * vec - 1) / (64 * vec) * 64; }
+
+// Waves of a row, eight columns a lane: 1, 2 and 4 in workgroups of kNormWaves, more in one of
+// their own; sixteen columns a lane where they would be more than sixteen.
+int norm_row_waves(int H) {
+  const int vec = H > 512 * kNormMaxWaves ? 2 : 1;
+  const int w = (H + 512 * vec - 1) / (512 * vec);
+  return w == 3 ? 4 : w;
+}
+
+template <int kRes, int kY, int kVec, int kRowWaves>
+void norm_go(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
+  const int row_waves = norm_row_waves(a.H);
+  const dim3 block(64 * (kRowWaves ? kNormWaves : row_waves));
+  constexpr int kRows = NormShape<kRowWaves>::kRows;
+  const int64_t rounds = (a.T + kRows - 1) / kRows;
+  if (!bwd_groups)
+    hipLaunchKernelGGL((block_norm_kernel<kRes, kY, kVec, kRowWaves>),
+                       dim3((unsigned)(rounds < (1 << 20) ? rounds : (1 << 20))), block, 0, s, a);
+  else if (a.dh && a.h_dtype == kF32)
+    hipLaunchKernelGGL((block_norm_bwd_kernel<kRes, kY, 4, kVec, kRowWaves>), dim3(bwd_groups),
+                       block, 0, s, a);
+  else
+    hipLaunchKernelGGL((block_norm_bwd_kernel<kRes, kY, 2, kVec, kRowWaves>), dim3(bwd_groups),
+                       block, 0, s, a);
+}
+
+template <int kRes, int kY>
+void norm_sizes(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
+  switch (norm_row_waves(a.H)) {
+    case 1: return norm_go<kRes, kY, 1, 1>(a, bwd_groups, s);
+    case 2: return norm_go<kRes, kY, 1, 2>(a, bwd_groups, s);
+    case 4: return norm_go<kRes, kY, 1, 4>(a, bwd_groups, s);
+  }
+  if (a.H <= 512 * kNormMaxWaves) norm_go<kRes, kY, 1, 0>(a, bwd_groups, s);
+  else norm_go<kRes, kY, 2, 0>(a, bwd_groups, s);
+}
+
+void norm_launch(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
+  const bool wide_y = a.y && a.y_dtype == kF32;
+  if (a.res_dtype == kF32 && wide_y) norm_sizes<4, 4>(a, bwd_groups, s);
+  else if (a.res_dtype == kF32) norm_sizes<4, 2>(a, bwd_groups, s);
+  else if (wide_y) norm_sizes<2, 4>(a, bwd_groups, s);
+  else norm_sizes<2, 2>(a, bwd_groups, s);
+}
+
 }  // namespace
+
+int block_norm_groups(int64_t T, int H) {
+  const int waves = norm_row_waves(H);
+  const int64_t rows = waves <= 4 ? kNormWaves / waves : 1;
+  const int64_t rounds = (T + rows - 1) / rows;
+  return (int)(rounds < kNormGroups ? rounds : kNormGroups);
+}
 
 hipError_t launch_block_norm(const BlockNormArgs& a, int num_cus, hipStream_t s) {
   (void)num_cus;
-  const dim3 grid((unsigned)(a.T < (1 << 20) ? a.T : (1 << 20)));
-  if (a.H <= 8192)
-    hipLaunchKernelGGL(block_norm_kernel<1>, grid, dim3(norm_threads(a.H, 1)), 0, s, a);
-  else
-    hipLaunchKernelGGL(block_norm_kernel<2>, grid, dim3(norm_threads(a.H, 2)), 0, s, a);
+  norm_launch(a, 0, s);
   return hipGetLastError();
 }
 
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, hipStream_t s) {
   const int groups = block_norm_groups(a.T, a.H);
-  if (a.H <= 8192)
-    hipLaunchKernelGGL(block_norm_bwd_kernel<1>, dim3(groups), dim3(norm_threads(a.H, 1)), 0, s, a);
-  else
-    hipLaunchKernelGGL(block_norm_bwd_kernel<2>, dim3(groups), dim3(norm_threads(a.H, 2)), 0, s, a);
+  norm_launch(a, groups, s);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || (!a.w_pre && !a.w_post && a.gate_axis != 2)) return err;
-  hipLaunchKernelGGL(block_norm_reduce_kernel, dim3((a.H + 63) / 64, 3), dim3(64), 0, s, a, groups);
+  hipLaunchKernelGGL(block_norm_reduce_kernel, dim3((a.H + 63) / 64, 3), dim3(1024), 0, s, a, groups);
   return hipGetLastError();
 }
 
