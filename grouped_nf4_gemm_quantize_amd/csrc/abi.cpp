@@ -1417,13 +1417,18 @@ int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const 
 
 static_assert(kMuonMaxTensors == NF4MOE_MAX_MUON_TENSORS, "one call's tensors");
 
+static int64_t muon_chunks(int E, int64_t n, int r) {
+  const int64_t cols = muon_chunk_cols(E, n, r);
+  return (n + cols - 1) / cols;
+}
+
 static int muon_shape_check(int E, int r, int64_t n) {
   if (E < 1 || n < 1)
     return fail(NF4MOE_EINVAL, "E=%d and n=%lld must be positive", E, (long long)n);
   if (r < 1 || r > NF4MOE_MAX_LORA_R)
     return fail(NF4MOE_EINVAL, "rank r=%d outside [1, %d]", r, NF4MOE_MAX_LORA_R);
   // each tensor below 2^40 elements; a call's threads fit the 32-bit grid
-  if (n > ((int64_t)1 << 40) / r / E || (int64_t)muon_chunks(n, r) * E > kMuonMaxBlocks)
+  if (n > ((int64_t)1 << 40) / r / E || muon_chunks(E, n, r) * E > kMuonMaxBlocks)
     return fail(NF4MOE_EOVERFLOW, "E=%d, r=%d, n=%lld is too large", E, r, (long long)n);
   return NF4MOE_OK;
 }
@@ -1438,7 +1443,7 @@ static int muon_scalar_check(int ns_steps, double a, double b, double c, double 
 }
 
 static size_t muon_gram_bytes(int E, int r, int64_t n) {
-  return align_up((size_t)E * muon_chunks(n, r) * r * r * 8, 256);
+  return align_up((size_t)E * muon_chunks(E, n, r) * r * r * 8, 256);
 }
 
 // Places the tensors' workgroups and Gram parts, then launches.
@@ -1447,7 +1452,12 @@ static int muon_run(MuonArgs& a, void* workspace, size_t ws_bytes, void* stream)
   a.blocks = 0;
   for (int i = 0; i < a.count; ++i) {
     MuonTensor& t = a.t[i];
-    t.chunks = muon_chunks(t.n, t.r);
+    t.chunk_cols = muon_chunk_cols(t.E, t.n, t.r);
+    t.chunks = (int)muon_chunks(t.E, t.n, t.r);
+    // A factors: rows of four; B factors: a group of whole rows
+    t.vec = (t.rank_major ? t.n : 16 / t.r * t.r) % 4 == 0 && (int64_t)t.r * t.n % 4 == 0 &&
+            aligned(t.g, t.g_dtype == NF4MOE_F32 ? 16 : 8) && aligned(t.m, 16) &&
+            aligned(t.m_out, 16) && aligned(t.w, 16) && aligned(t.w_out, 16) && aligned(t.w16, 8);
     t.block0 = a.blocks;
     t.gram = (double*)((char*)workspace + need);
     a.blocks += t.E * t.chunks;

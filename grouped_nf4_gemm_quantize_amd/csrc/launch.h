@@ -276,7 +276,8 @@ struct MuonTensor {
   double scale;
   int E, r, rank_major;
   int g_dtype, w_dtype, w16_dtype;
-  int chunks;     // workgroups of one factor
+  int chunk_cols, chunks;  // long-axis elements of a workgroup, workgroups of a factor
+  int vec;        // four elements along the memory order are one aligned access
   int block0;     // first workgroup of this tensor
 };
 struct MuonArgs {
@@ -288,7 +289,7 @@ struct MuonArgs {
   float mu;
   double lr, weight_decay, a, b, c, eps;
 };
-int muon_chunks(int64_t n, int r);
+int muon_chunk_cols(int E, int64_t n, int r);
 hipError_t launch_muon(const MuonArgs& a, hipStream_t s);
 
 }  // namespace nf4moe
