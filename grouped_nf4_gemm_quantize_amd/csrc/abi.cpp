@@ -1427,8 +1427,8 @@ static int muon_shape_check(int E, int r, int64_t n) {
     return fail(NF4MOE_EINVAL, "E=%d and n=%lld must be positive", E, (long long)n);
   if (r < 1 || r > NF4MOE_MAX_LORA_R)
     return fail(NF4MOE_EINVAL, "rank r=%d outside [1, %d]", r, NF4MOE_MAX_LORA_R);
-  // each tensor below 2^40 elements; a call's threads fit the 32-bit grid
-  if (n > ((int64_t)1 << 40) / r / E || muon_chunks(E, n, r) * E > kMuonMaxBlocks)
+  // 32-bit places in a factor; a call's threads fit the 32-bit grid
+  if (n > ((int64_t)1 << 29) / r || muon_chunks(E, n, r) * E > kMuonMaxBlocks)
     return fail(NF4MOE_EOVERFLOW, "E=%d, r=%d, n=%lld is too large", E, r, (long long)n);
   return NF4MOE_OK;
 }
@@ -1467,7 +1467,10 @@ static int muon_run(MuonArgs& a, void* workspace, size_t ws_bytes, void* stream)
     return fail(NF4MOE_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                 workspace ? ws_bytes : (size_t)0);
   if (!aligned(workspace, 256)) return fail(NF4MOE_EINVAL, "workspace must be 256-byte aligned");
-  hipError_t err = launch_muon(a, (hipStream_t)stream);
+  int cus = 0;
+  const int st = cu_count(&cus);
+  if (st != NF4MOE_OK) return st;
+  hipError_t err = launch_muon(a, cus, (hipStream_t)stream);
   if (err != hipSuccess) return hip_fail(err, "adapter update launch");
   return ok();
 }

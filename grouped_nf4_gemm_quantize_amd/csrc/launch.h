@@ -278,6 +278,8 @@ struct MuonTensor {
   int g_dtype, w_dtype, w16_dtype;
   int chunk_cols, chunks;  // long-axis elements of a workgroup, workgroups of a factor
   int vec;        // four elements along the memory order are one aligned access
+  int lds_row;    // whole factors in LDS: distance of an A factor's rows
+  uint32_t n_magic;  // and i / n = umulhi(i, n_magic)
   int block0;     // first workgroup of this tensor
 };
 struct MuonArgs {
@@ -290,6 +292,6 @@ struct MuonArgs {
   double lr, weight_decay, a, b, c, eps;
 };
 int muon_chunk_cols(int E, int64_t n, int r);
-hipError_t launch_muon(const MuonArgs& a, hipStream_t s);
+hipError_t launch_muon(MuonArgs& a, int num_cus, hipStream_t s);
 
 }  // namespace nf4moe

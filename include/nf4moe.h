@@ -618,7 +618,7 @@ int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const 
  *                   ns_eps >= 0 (EINVAL);
  *   workspace       lora_muon_step_workspace(tensors, count) bytes, 256-byte
  *                   aligned; 0 for invalid arguments.
- * Pointers are aligned to their element.  E * r * n at most 2^40 and, a workgroup taking
+ * Pointers are aligned to their element.  r * n at most 2^29 and, a workgroup taking
  * 8192 elements of a factor, at most 2^20 workgroups a tensor (EOVERFLOW). */
 #define NF4MOE_MAX_MUON_TENSORS 8
 typedef struct {

@@ -49,6 +49,20 @@ def test_orthogonalize(gpu_lib, E, r, n, rank_major):
     assert np.all(np.abs(host(o) - ref) <= half_spacing(ref, "f32") + 1e-9)
 
 
+@pytest.mark.parametrize("rank_major", [True, False])
+@pytest.mark.parametrize("r,n", [(1, 1), (1, 30), (2, 33), (3, 50), (4, 64), (5, 1), (6, 129),
+                                 (7, 2), (8, 2048), (9, 31), (10, 256), (12, 500), (16, 2048),
+                                 (16, 2109), (16, 9), (13, 1024), (4, 8444), (8, 4224)])
+def test_orthogonalize_many_factors(gpu_lib, r, n, rank_major):
+    """More factors than compute units, below and beyond what one workgroup holds."""
+    E = 300
+    u = np.concatenate([factor(4, r, n, rank_major, k) for k in range(3)] * 25)
+    o = host(gpu_lib.lora_orthogonalize(torch.from_numpy(u).to(DEV), rank_major=rank_major))
+    ref = ns(u[:12], rank_major)
+    for k in range(0, E, 12):
+        assert np.all(np.abs(o[k:k + 12] - ref) <= half_spacing(ref, "f32") + 1e-9), k
+
+
 @pytest.mark.parametrize("ut", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("ot", ["f32", "bf16", "f16"])
 def test_orthogonalize_types_in_place_and_steps(gpu_lib, ut, ot):
@@ -113,11 +127,14 @@ SHAPES = [(4, 8, 2048, True), (4, 8, 1024, False), (3, 5, 100, True), (2, 16, 77
           (1, 1, 9, True), (2, 3, 64, False), (6, 7, 256, True), (1, 16, 2048, True)]
 
 
+MANY = [(130, 8, 256, True), (130, 8, 256, False), (20, 5, 77, True), (30, 6, 51, False)]
+
+
 @pytest.mark.parametrize("wt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("nesterov", [True, False])
-@pytest.mark.parametrize("count", [1, 4, 8])
+@pytest.mark.parametrize("count", [1, 4, 8, "many"])
 def test_step(gpu_lib, wt, nesterov, count):
-    t = step_case(SHAPES[:count], wt)
+    t = step_case(MANY if count == "many" else SHAPES[:count], wt)
     before = [{k: v.clone() if torch.is_tensor(v) else v for k, v in d.items()} for d in t]
     gpu_lib.lora_muon_step(t, lr=0.02, momentum=0.9, nesterov=nesterov, weight_decay=0.1)
     check_step(before, t, wt, 0.02, 0.9, nesterov, 0.1)
@@ -125,8 +142,9 @@ def test_step(gpu_lib, wt, nesterov, count):
         assert torch.equal(b["grad"], a["grad"])
 
 
-def test_step_out_of_place_is_in_place_and_repeats(gpu_lib):
-    t = step_case(SHAPES[:4], "bf16")
+@pytest.mark.parametrize("shapes", [SHAPES[:4], MANY])
+def test_step_out_of_place_is_in_place_and_repeats(gpu_lib, shapes):
+    t = step_case(shapes, "bf16")
     out = [dict(d, momentum_out=torch.empty_like(d["momentum"]), w_out=torch.empty_like(d["w"]))
            for d in t]
     kept = [(d["momentum"].clone(), d["w"].clone()) for d in t]
