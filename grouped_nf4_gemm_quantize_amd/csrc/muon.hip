@@ -549,6 +549,8 @@ __device__ __forceinline__ void whole_factor(const MuonArgs& a, const MuonTensor
 
 }  // namespace
 
+// kVec: every tensor of the call has aligned reads of four.
+template <bool kVec>
 __global__ __launch_bounds__(kMuonThreads) void muon_gram_kernel(MuonArgs a) {
   __shared__ double part[kMuonWaves][16][17];
   const MuonBlock b = muon_block(a);
@@ -556,12 +558,9 @@ __global__ __launch_bounds__(kMuonThreads) void muon_gram_kernel(MuonArgs a) {
   const Shape h = chunk_shape(t, b);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  f64x4 acc;
-  if (t.rank_major)
-    acc = t.vec ? gram_chunk<true, true>(a, t, b, h, wave, lane)
-                : gram_chunk<true, false>(a, t, b, h, wave, lane);
-  else
-    acc = gram_chunk<false, false>(a, t, b, h, wave, lane);
+  const f64x4 acc =
+      t.rank_major ? gram_chunk<true, kVec>(a, t, b, h, wave, lane)
+                   : gram_chunk<false, kVec>(a, t, b, h, wave, lane);
 #pragma unroll
   for (int j = 0; j < 4; ++j) part[wave][4 * j + (lane >> 4)][lane & 15] = acc[j];
   __syncthreads();
@@ -570,20 +569,17 @@ __global__ __launch_bounds__(kMuonThreads) void muon_gram_kernel(MuonArgs a) {
         fold_gram(part, kMuonWaves, h, tid);
 }
 
+template <bool kVec>
 __global__ __launch_bounds__(kMuonThreads, 4) void muon_apply_kernel(MuonArgs a) {
   __shared__ double gm[16][17];
   __shared__ double pm[4][64];
   const MuonBlock b = muon_block(a);
   const MuonTensor& t = a.t[b.ti];
-  if (t.rank_major) {
-    if (t.vec) apply_factor<true, true>(a, t, b, gm, pm);
-    else apply_factor<true, false>(a, t, b, gm, pm);
-  } else {
-    if (t.vec) apply_factor<false, true>(a, t, b, gm, pm);
-    else apply_factor<false, false>(a, t, b, gm, pm);
-  }
+  if (t.rank_major) apply_factor<true, kVec>(a, t, b, gm, pm);
+  else apply_factor<false, kVec>(a, t, b, gm, pm);
 }
 
+template <bool kVec>
 __global__ __launch_bounds__(kFactorThreads) void muon_factor_kernel(MuonArgs a) {
   extern __shared__ float lds_u[];
   __shared__ double part[kFactorWaves / 2][16][17];
@@ -591,13 +587,8 @@ __global__ __launch_bounds__(kFactorThreads) void muon_factor_kernel(MuonArgs a)
   __shared__ double pm[4][64];
   const MuonBlock b = muon_block(a);
   const MuonTensor& t = a.t[b.ti];
-  if (t.rank_major) {
-    if (t.vec) whole_factor<true, true>(a, t, b, lds_u, part, gm, pm);
-    else whole_factor<true, false>(a, t, b, lds_u, part, gm, pm);
-  } else {
-    if (t.vec) whole_factor<false, true>(a, t, b, lds_u, part, gm, pm);
-    else whole_factor<false, false>(a, t, b, lds_u, part, gm, pm);
-  }
+  if (t.rank_major) whole_factor<true, kVec>(a, t, b, lds_u, part, gm, pm);
+  else whole_factor<false, kVec>(a, t, b, lds_u, part, gm, pm);
 }
 
 // Long-axis elements of a workgroup: 8192 elements of the factor and whole blocks of both
@@ -609,9 +600,30 @@ int muon_chunk_cols(int E, int64_t n, int r) {
   return (int)cols;
 }
 
+namespace {
+
+template <bool kVec>
+hipError_t muon_go(const MuonArgs& a, int lds, hipStream_t s) {
+  if (lds > 0) {
+    const void* k = reinterpret_cast<const void*>(muon_factor_kernel<kVec>);
+    hipError_t err = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL(muon_factor_kernel<kVec>, dim3(a.blocks), dim3(kFactorThreads), lds, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(muon_gram_kernel<kVec>, dim3(a.blocks), dim3(kMuonThreads), 0, s, a);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(muon_apply_kernel<kVec>, dim3(a.blocks), dim3(kMuonThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_muon(MuonArgs& a, int num_cus, hipStream_t s) {
   // one workgroup a factor where half the compute units or more get one and all fit
   int64_t factors = 0, floats = 0;
+  bool vec = true;
   for (int i = 0; i < a.count; ++i) {
     MuonTensor& t = a.t[i];
     if (t.n == 1) t.rank_major = 0;  // the same memory either way
@@ -619,29 +631,22 @@ hipError_t launch_muon(MuonArgs& a, int num_cus, hipStream_t s) {
     const int64_t need = t.rank_major ? (int64_t)t.r * t.lds_row : t.r * t.n + 16;
     floats = need > floats ? need : floats;
     factors += t.E;
+    vec = vec && t.vec;
   }
+  int lds = 0;
   if (2 * factors >= num_cus && floats <= kFactorFloats) {
-    int block0 = 0;
+    lds = (int)floats * 4;
+    a.blocks = 0;
     for (int i = 0; i < a.count; ++i) {
-      MuonTensor& t = a.t[i];
-      t.chunks = 1;
-      t.block0 = block0;
-      block0 += t.E;
+      a.t[i].chunks = 1;
+      a.t[i].block0 = a.blocks;
+      a.blocks += a.t[i].E;
       // i / n = umulhi(i, n_magic): exact, as i and n are below 2^16; A factors have n > 1
-      t.n_magic = t.rank_major ? (uint32_t)((((uint64_t)1 << 32) + t.n - 1) / t.n) : 0u;
+      a.t[i].n_magic =
+          a.t[i].rank_major ? (uint32_t)((((uint64_t)1 << 32) + a.t[i].n - 1) / a.t[i].n) : 0u;
     }
-    const int lds = (int)floats * 4;
-    hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(muon_factor_kernel),
-                                         hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(muon_factor_kernel, dim3(block0), dim3(kFactorThreads), lds, s, a);
-    return hipGetLastError();
   }
-  hipLaunchKernelGGL(muon_gram_kernel, dim3(a.blocks), dim3(kMuonThreads), 0, s, a);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(muon_apply_kernel, dim3(a.blocks), dim3(kMuonThreads), 0, s, a);
-  return hipGetLastError();
+  return vec ? muon_go<true>(a, lds, s) : muon_go<false>(a, lds, s);
 }
 
 }  // namespace nf4moe
