@@ -9,11 +9,17 @@
 // fp16 values with one copy per lane slot, so that random bytes never share a
 // bank.
 //
-// The eight waves of a workgroup share the K axis of 16 output rows (a tile) in
-// chunks of 128, chunk c of wave c % 8.  A lane reads 16 consecutive packed bytes
-// (32 codes) of one row; four lane swaps then give each of the chunk's four matrix
-// steps 32 consecutive k, all of one scale group, whose sum is scaled in fp32.
-// A wave's part of x stays in registers from tile to tile.  The waves' sums meet in LDS.
+// The waves of a workgroup (up to sixteen) share the K axis of 16 output rows (a
+// tile) in chunks of 128, chunk c going to wave c % waves.  A lane reads 16 consecutive
+// packed bytes (32 codes) of one row; four lane swaps then give each of the chunk's four
+// matrix steps 32 consecutive k, all of one scale group, whose sum is scaled in fp32.
+// A wave's part of x stays in registers from tile to tile, and the next tiles' codes
+// are in flight while a tile is computed.  The waves' sums meet in LDS.
+//
+// Scales and zeros go through LDS too: read by the wave that uses them, a chunk's few
+// bytes of 16 rows cost as many cache lines as its codes (28672 x 4096 int4, groups of 128,
+// one token: 28.7 us, without these reads 15.9 us).  The workgroup reads a round's
+// as consecutive elements instead, one round ahead.
 //
 // nf4's levels are no fp16 values: each is held as a sum of two (22 bits),
 // scaled by 2^8 so that the small parts stay normal, and multiplied twice.  All
@@ -27,8 +33,7 @@ namespace nf4moe {
 
 namespace {
 
-constexpr int kMvThreads = 1024;
-constexpr int kMvWaves = kMvThreads / 64;
+constexpr int kMvWaves = 16;    // waves of a workgroup, at most
 constexpr int kMvTile = 16;     // output rows of one matrix step
 constexpr int kMvTokens = 16;   // rows of x of one matrix step
 constexpr int kMvChunk = 128;   // k of one lane-wide read
@@ -49,95 +54,31 @@ constexpr int mv_groups(int f) { return f == kMvfMX || f == kMvfInt32 ? 4 : f ==
 
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 
-// The rows of a tile as a buffer: reads beyond its end return 0 without
-// touching memory, which covers rows beyond N and tiles beyond the last.
-__device__ __forceinline__ Rsrc mv_rsrc(const void* p, int64_t offset, int64_t bytes) {
+__device__ __forceinline__ Rsrc mv_rsrc(const void* p, int64_t offset, uint32_t bytes) {
   char* at = const_cast<char*>(reinterpret_cast<const char*>(p)) + offset;
-  return __builtin_amdgcn_make_buffer_rsrc(at, 0, bytes > 0 ? (int)bytes : 0, 0x00020000);
+  return __builtin_amdgcn_make_buffer_rsrc(at, 0, (int)bytes, 0x00020000);
 }
 
-// Raw scales of a chunk's groups as they are read, and zeros, a byte each.  Nothing is
-// computed on them before they are used, so that a read can stay in flight.
-template <int kFmt, bool kWhole>
-struct MvScales {
-  static constexpr int kPer = mv_groups(kFmt);
-  uint32_t s[kPer];  // kWhole: packed as in memory
-  uint32_t z[kPer];  // kWhole: all in z[0]
-};
-
-// What a lane needs of a tile's scales: byte offsets of its row.
-struct MvScaleRow {
-  int size;  // bytes of a scale
-  int s, z;  // offset of the row's first scale, and first zero
-  int groups;
-};
-
-template <int kFmt, bool kWhole>
-__device__ __forceinline__ void mv_load_scales(Rsrc rs, Rsrc rz, const MvScaleRow& row, int c,
-                                               MvScales<kFmt, kWhole>& r) {
-  constexpr int kPer = mv_groups(kFmt);
-  if constexpr (kWhole) {
-    const int at = row.s + c * kPer * row.size;
-    if constexpr (kFmt == kMvfMX) {
-      r.s[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
-    } else if constexpr (!mv_int(kFmt)) {
-      const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
-      r.s[0] = v[0], r.s[1] = v[1];
-    } else if (row.size == 4) {
-      if constexpr (kPer == 4) {
-        const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
-        r.s[0] = v[0], r.s[1] = v[1], r.s[2] = v[2], r.s[3] = v[3];
-      } else if constexpr (kPer == 2) {
-        const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
-        r.s[0] = v[0], r.s[1] = v[1];
-      } else {
-        r.s[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
-      }
-    } else {
-      if constexpr (kPer == 4) {
-        const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
-        r.s[0] = v[0], r.s[1] = v[1];
-      } else if constexpr (kPer == 2) {
-        r.s[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
-      } else {
-        r.s[0] = __builtin_amdgcn_raw_buffer_load_b16(rs, at, 0, 0);
-      }
-    }
-    if constexpr (mv_int(kFmt)) {
-      const int zat = row.z + c * kPer;
-      if constexpr (kPer == 4) r.z[0] = __builtin_amdgcn_raw_buffer_load_b32(rz, zat, 0, 0);
-      else if constexpr (kPer == 2) r.z[0] = __builtin_amdgcn_raw_buffer_load_b16(rz, zat, 0, 0);
-      else r.z[0] = __builtin_amdgcn_raw_buffer_load_b8(rz, zat, 0, 0);
-    }
-  } else {
-#pragma unroll
-    for (int g = 0; g < kPer; ++g) {
-      // groups beyond the row (x is zero there) read its last one
-      const int i = c * kPer + g < row.groups ? c * kPer + g : row.groups - 1;
-      const int at = row.s + i * row.size;
-      if constexpr (kFmt == kMvfMX)
-        r.s[g] = __builtin_amdgcn_raw_buffer_load_b8(rs, at, 0, 0);
-      else if (!mv_int(kFmt) || row.size == 4)
-        r.s[g] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
-      else
-        r.s[g] = __builtin_amdgcn_raw_buffer_load_b16(rs, at, 0, 0);
-      if constexpr (mv_int(kFmt)) r.z[g] = __builtin_amdgcn_raw_buffer_load_b8(rz, row.z + i, 0, 0);
-    }
-  }
-}
-
-// Scale g of a chunk as fp32.
-template <int kFmt, bool kWhole>
-__device__ __forceinline__ float mv_scale(const MvScales<kFmt, kWhole>& r, int g, int dtype) {
-  if constexpr (kFmt == kMvfMX) {  // 2^(raw - 127), 255 is NaN
-    const uint32_t raw = kWhole ? (r.s[0] >> (8 * g)) & 0xffu : r.s[g];
+// Raw scale -> fp32.
+template <int kFmt>
+__device__ __forceinline__ float mv_scale(uint32_t raw, int dtype) {
+  if constexpr (kFmt == kMvfMX)  // 2^(raw - 127), 255 is NaN
     return __uint_as_float(raw == 0u ? 0x00400000u : raw == 255u ? 0x7fc00000u : raw << 23);
-  }
-  if (!mv_int(kFmt) || dtype == kF32) return __uint_as_float(r.s[g]);
-  const uint32_t raw = kWhole ? (r.s[g >> 1] >> (16 * (g & 1))) & 0xffffu : r.s[g];
+  if (!mv_int(kFmt) || dtype == kF32) return __uint_as_float(raw);
   return dtype == kBF16 ? bf16_bits_to_f32(raw)
                         : (float)__builtin_bit_cast(_Float16, (uint16_t)raw);
 }
+
+// The scales (fp32) and zeros (fp16) of kRows tiles x 16 kX chunks in LDS.
+// Rows are kStride words apart: 16 rows of one chunk lie in different banks.
+template <int kFmt, int kX, int kRows>
+struct MvStage {
+  static constexpr int kStride = (16 * kX + 1) * mv_groups(kFmt);
+  // elements of a thread: waves * kX chunks of each row over 64 * waves threads
+  static constexpr int kReads = (kRows * kMvTile * kX * mv_groups(kFmt) + 63) / 64;
+  float s[kRows * kMvTile * kStride];
+  _Float16 z[mv_int(kFmt) ? kRows * kMvTile * kStride : 2];
+};
 
 // Transposes 4 words x 4 lane rows of 16: lane row q, word s <-> lane row s, word q.
 __device__ __forceinline__ void quad_transpose(uint32_t (&d)[4]) {
@@ -155,51 +96,75 @@ struct MvX {
   f16x8 v[mv_split(kFmt) ? 2 : 1];
 };
 
-// tot += the products of one chunk of one row tile.  Steps beyond the end of the row
-// have x = 0.
-template <int kFmt, bool kWhole, int kRegs>
-__device__ __forceinline__ void mv_chunk(const MatvecArgs& a, const char* lut, uint32_t lane_off,
-                                         u32x4 w, const MvScales<kFmt, kWhole>& sc,
+// tot += the products of one chunk of one row tile, whose scales and zeros begin at
+// `scales` and `zeros`.  Steps beyond the end of the row have x = 0.
+template <int kFmt, int kRegs>
+__device__ __forceinline__ void mv_chunk(const char* lut, uint32_t lane_off, u32x4 w,
+                                         const float* scales, const _Float16* zeros,
                                          const MvX<kFmt> (&x)[4], float* tot) {
+  constexpr int kGroups = mv_groups(kFmt);
   uint32_t d[4] = {w.x, w.y, w.z, w.w};
   quad_transpose(d);
+  typedef float Scales __attribute__((ext_vector_type(kGroups == 1 ? 2 : kGroups)));
+  typedef _Float16 Zeros __attribute__((ext_vector_type(kGroups == 1 ? 2 : kGroups)));
+  float scale[kGroups];
+  f16x2 zero[kGroups];
+  if constexpr (kGroups == 1) {
+    scale[0] = scales[0];
+    if constexpr (mv_int(kFmt)) zero[0] = f16x2{zeros[0], zeros[0]};
+  } else {
+    const Scales v = *reinterpret_cast<const Scales*>(scales);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) scale[g] = v[g];
+    if constexpr (mv_int(kFmt)) {
+      const Zeros z = *reinterpret_cast<const Zeros*>(zeros);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) zero[g] = f16x2{z[g], z[g]};
+    }
+  }
+  // all table reads first, then the four steps, then their sums: each waits once
+  uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // table address: byte j of the codes in bits 8..15, the lane's slot below
+      const uint32_t at = __builtin_amdgcn_perm(d[s], lane_off, 0x0c0c0000u | ((4u + j) << 8));
+      if constexpr (mv_split(kFmt)) {
+        const u32x2 e = *reinterpret_cast<const u32x2*>(lut + at);
+        hi[s][j] = e.x;
+        lo[s][j] = e.y;
+      } else {
+        hi[s][j] = *reinterpret_cast<const uint32_t*>(lut + at);
+      }
+    }
+  f32x4 acc[4];
+  const f32x4 none = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const int g = s * mv_groups(kFmt) / 4;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    uint32_t at[4];
-    // table address: byte j of the codes in bits 8..15, the lane's slot below
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      at[j] = __builtin_amdgcn_perm(d[s], lane_off, 0x0c0c0000u | ((4u + j) << 8));
     if constexpr (mv_split(kFmt)) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x2 e = *reinterpret_cast<const u32x2*>(lut + at[2 * h]);
-        const u32x2 f = *reinterpret_cast<const u32x2*>(lut + at[2 * h + 1]);
-        const u32x4 b = {e.x, e.y, f.x, f.y};
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s].v[h], __builtin_bit_cast(f16x8, b), acc,
-                                                     0, 0, 0);
-      }
+      const u32x4 b0 = {hi[s][0], lo[s][0], hi[s][1], lo[s][1]};
+      const u32x4 b1 = {hi[s][2], lo[s][2], hi[s][3], lo[s][3]};
+      acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s].v[0], __builtin_bit_cast(f16x8, b0), none,
+                                                      0, 0, 0);
+      acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s].v[1], __builtin_bit_cast(f16x8, b1),
+                                                      acc[s], 0, 0, 0);
     } else {
-      uint32_t b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const uint32_t*>(lut + at[j]);
       if constexpr (mv_int(kFmt)) {
-        const uint32_t raw = kWhole ? (sc.z[0] >> (8 * g)) & 0xffu : sc.z[g];
-        const _Float16 z = (_Float16)(float)(a.zeros ? raw : 8u);
-        const f16x2 z2 = {z, z};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = half2_as_u32(u32_as_half2(b[j]) - z2);
+        for (int j = 0; j < 4; ++j)
+          hi[s][j] = half2_as_u32(u32_as_half2(hi[s][j]) - zero[s * kGroups / 4]);
       }
-      const u32x4 b4 = {b[0], b[1], b[2], b[3]};
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s].v[0], __builtin_bit_cast(f16x8, b4), acc, 0,
-                                                   0, 0);
+      const u32x4 b = {hi[s][0], hi[s][1], hi[s][2], hi[s][3]};
+      acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s].v[0], __builtin_bit_cast(f16x8, b), none,
+                                                      0, 0, 0);
     }
-    const float f = mv_scale<kFmt, kWhole>(sc, g, a.scale_dtype);
-#pragma unroll
-    for (int i = 0; i < kRegs; ++i) tot[i] = fmaf(f, acc[i], tot[i]);
   }
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i)
+      tot[i] = fmaf(scale[s * kGroups / 4], acc[s][i], tot[i]);
 }
 
 // The matrix unit's x operand of step s of chunk c: row m of the 16 is token
@@ -247,9 +212,8 @@ __device__ __forceinline__ void mv_fill(u32x4* lut, uint32_t* stage, int tid) {
     stage[tid] = pack_half2(hi, lo);
   }
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4096 / kMvThreads; ++i) {
-    const int u = i * kMvThreads + tid, b = u >> 4;  // 16 16-byte units an entry
+  for (int u = tid; u < 4096; u += blockDim.x) {
+    const int b = u >> 4;  // 16 16-byte units an entry
     const uint32_t first = stage[kFmt == kMvfMX ? b & 15 : b >> 4];
     const uint32_t second = stage[kFmt == kMvfMX ? b >> 4 : b & 15];
     const uint32_t h = (first & 0xffffu) | (second << 16);
@@ -261,19 +225,21 @@ __device__ __forceinline__ void mv_fill(u32x4* lut, uint32_t* stage, int tid) {
 
 }  // namespace
 
-// kWhole: rows are whole chunks and a chunk's scales one aligned read.  kRegs:
-// result registers of a lane (1: up to 4 tokens, 4: up to 16).  kCpw: chunks of a wave
-// whose x stays in registers (0: x is read again for every kRows tiles, any K).
-// kRows: tiles between two barriers.
-template <int kFmt, bool kWhole, int kRegs, int kCpw, int kRows>
-__global__ __launch_bounds__(kMvThreads) void matvec_kernel(MatvecArgs a) {
+// kRegs: result registers of a lane (1: up to 4 tokens, 4: up to 16).  kCpw: chunks of a
+// wave whose x stays in registers (0: any number, x is read with the codes).  kRows:
+// tiles of a round.  A round is one step, or (kCpw 0) one for every 16 chunks.
+template <int kFmt, int kRegs, int kCpw, int kRows>
+__global__ __launch_bounds__(64 * kMvWaves) void matvec_kernel(MatvecArgs a) {
   constexpr int kX = kCpw ? kCpw : 1;
-  constexpr int kOut = kRows * kRegs;  // result registers of a lane between barriers
+  constexpr int kOut = kRows * kRegs;  // result registers of a lane in a round
+  constexpr int kGroups = mv_groups(kFmt);
+  typedef MvStage<kFmt, kX, kRows> Stage;
   __shared__ u32x4 lut[4096];
   __shared__ float red[2][kMvWaves][kOut][64];
-  __shared__ uint32_t stage[16];
+  __shared__ __attribute__((aligned(16))) Stage stage[2];
+  __shared__ uint32_t levels[16];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
   const int64_t t0 = (int64_t)blockIdx.y * kMvTokens;
   const int nt = a.T - t0 < kMvTokens ? (int)(a.T - t0) : kMvTokens;
   const int chunks = (a.K + kMvChunk - 1) / kMvChunk;
@@ -281,102 +247,160 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(MatvecArgs a) {
   const int n_lane = lane & 15, q = lane >> 4;
   const uint32_t lane_off = mv_split(kFmt) ? (lane & 31) * 8 : lane * 4;
   const int row_bytes = a.K / 2;
-  MvScaleRow sr;
-  sr.groups = a.K / (kMvChunk / mv_groups(kFmt));
-  sr.size = kFmt == kMvfMX ? 1 : !mv_int(kFmt) || a.scale_dtype == kF32 ? 4 : 2;
-  sr.s = n_lane * sr.groups * sr.size;
-  sr.z = n_lane * sr.groups;
+  const int groups = a.K / (kMvChunk / kGroups);
+  const int size = kFmt == kMvfMX ? 1 : !mv_int(kFmt) || a.scale_dtype == kF32 ? 4 : 2;
   const uint8_t* zeros = a.zeros ? a.zeros : a.codes;  // read but not used
-
-  MvX<kFmt> x[kX][4];
-  u32x4 w[kRows][kX];
-  MvScales<kFmt, kWhole> sc[kRows][kX];
   const int lane_w = n_lane * row_bytes + 16 * q;
+  const int panels = kCpw ? 1 : (chunks + kMvWaves - 1) / kMvWaves;
+  const int grid_step = gridDim.x * kRows;
 
-  // reads chunk c of row tile `tile` (all zeros beyond the last tile)
-  const auto load = [&](int tile, int c, u32x4& wo, MvScales<kFmt, kWhole>& so) {
-    const int64_t n0 = (int64_t)tile * kMvTile;
-    const int64_t rows = a.N - n0 < kMvTile ? a.N - n0 : kMvTile;
-    const Rsrc rw = mv_rsrc(a.codes, n0 * row_bytes, rows * row_bytes);
-    const Rsrc rs = mv_rsrc(a.scales, n0 * sr.groups * sr.size, rows * sr.groups * sr.size);
-    const Rsrc rz = mv_rsrc(zeros, n0 * sr.groups, rows * sr.groups);
-    wo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                       rw, lane_w, c * (kMvChunk / 2), 0));
-    mv_load_scales<kFmt, kWhole>(rs, rz, sr, c, so);
-  };
-  const auto chunk_of = [&](int j) {
-    // a wave without a j-th chunk repeats the last one with x = 0
-    const int c = wave + j * kMvWaves;
+  // chunk j of this wave in a panel; a wave without one repeats the last with x = 0
+  const auto chunk_of = [&](int panel, int j) {
+    const int c = panel * kMvWaves + wave + j * waves;
     return c < chunks ? c : chunks - 1;
   };
+  // The rows of a round as buffers: reads beyond N return 0 without touching memory.
+  const auto rows_of = [&](int tile) {
+    const int64_t left = a.N - (int64_t)tile * kMvTile;
+    return (uint32_t)(left < 0 ? 0 : left < kMvTile * kRows ? left : kMvTile * kRows);
+  };
+  // codes of a step; a lane beyond the end of its row reads another row's (x is zero)
+  u32x4 w[kRows][kX];
+  const auto load_w = [&](int tile, int panel, int u, int j) {
+    const Rsrc r = mv_rsrc(a.codes, (int64_t)tile * kMvTile * row_bytes, rows_of(tile) * row_bytes);
+    w[u][j] = __builtin_bit_cast(
+        u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_w + u * kMvTile * row_bytes,
+                                                     chunk_of(panel, j) * (kMvChunk / 2), 0));
+  };
+  // scales and zeros of a step, element i of the workgroup: raw, then into LDS.  Beyond
+  // the end of a row its last scale is read (x is zero there).
+  uint32_t raw_s[Stage::kReads], raw_z[Stage::kReads];
+  const int seg = waves * kX * kGroups;                    // scales of a row
+  const uint32_t magic = ((1u << 20) + seg - 1) / seg;     // i / seg = i * magic >> 20, exact
+  const int stage_count = kRows * kMvTile * seg;           // for i up to 64 seg <= 2^13
+  const auto load_stage = [&](int tile, int panel) {
+    const int64_t first = (int64_t)tile * kMvTile * groups;
+    const uint32_t count = rows_of(tile) * groups;
+    const Rsrc rs = mv_rsrc(a.scales, first * size, count * size);
+    const Rsrc rz = mv_rsrc(zeros, first, count);
+#pragma unroll
+    for (int k = 0; k < Stage::kReads; ++k) {
+      const int i = tid + k * blockDim.x, row = (int)(i * magic >> 20);
+      const int g = panel * kMvWaves * kGroups + i - row * seg;
+      const int at = row * groups + (g < groups ? g : groups - 1);
+      if (kFmt == kMvfMX) raw_s[k] = __builtin_amdgcn_raw_buffer_load_b8(rs, at, 0, 0);
+      else if (size == 4) raw_s[k] = __builtin_amdgcn_raw_buffer_load_b32(rs, at * 4, 0, 0);
+      else raw_s[k] = __builtin_amdgcn_raw_buffer_load_b16(rs, at * 2, 0, 0);
+      if constexpr (mv_int(kFmt)) raw_z[k] = __builtin_amdgcn_raw_buffer_load_b8(rz, at, 0, 0);
+    }
+  };
+  const auto put_stage = [&](Stage& to) {
+#pragma unroll
+    for (int k = 0; k < Stage::kReads; ++k) {
+      const int i = tid + k * blockDim.x, row = (int)(i * magic >> 20);
+      if (i >= stage_count) break;
+      const int at = row * Stage::kStride + i - row * seg;
+      to.s[at] = mv_scale<kFmt>(raw_s[k], a.scale_dtype);
+      if constexpr (mv_int(kFmt)) to.z[at] = (_Float16)(float)(a.zeros ? raw_z[k] : 8u);
+    }
+  };
 
-  int tile = blockIdx.x * kRows;
-  if constexpr (kCpw > 0) {
+  // the step after (tile, panel)
+  const auto after = [&](int& tile, int& panel) {
+    const bool end = ++panel == panels;
+    if (end) panel = 0, tile += grid_step;
+    return end;
+  };
+
+  int tile = blockIdx.x * kRows, panel = 0;
+  int next_tile = tile, next_panel = panel;  // of the codes in flight
+  MvX<kFmt> x[kX][4];
+  load_stage(tile, 0);
 #pragma unroll
-    for (int j = 0; j < kX; ++j)
+  for (int j = 0; j < kX; ++j)
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) load(tile + u, chunk_of(j), w[u][j], sc[u][j]);
+    for (int u = 0; u < kRows; ++u) load_w(tile, 0, u, j);
 #pragma unroll
-    for (int j = 0; j < kX; ++j)
-      mv_load_x<kFmt, kRegs>(a, t0, nt, wave + j * kMvWaves, lane, x[j]);
-  }
-  mv_fill<kFmt>(lut, stage, tid);
+  for (int j = 0; j < kX; ++j)
+    mv_load_x<kFmt, kRegs>(a, t0, nt, wave + j * waves, lane, x[j]);
+  put_stage(stage[0]);
+  after(next_tile, next_panel);
+  load_stage(next_tile, next_panel);
+  mv_fill<kFmt>(lut, levels, tid);
   const char* table = reinterpret_cast<const char*>(lut);
   const float last = mv_split(kFmt) ? 1.0f / 256.0f : kFmt == kMvfFP4 ? 1.0f / 6.0f : 1.0f;
-  const int step = gridDim.x * kRows;
 
-  for (int buf = 0; tile < tiles; tile += step, buf ^= 1) {
-    float tot[kOut] = {};
+  float tot[kOut] = {};
+  for (int buf = 0, out = 0; tile < tiles; buf ^= 1) {
+    // the next step's codes, and the scales of the one after it, are in flight
+    // during this step
+    const bool end = panel + 1 == panels;
+    int ahead_tile = next_tile, ahead_panel = next_panel;
+    after(ahead_tile, ahead_panel);
+    put_stage(stage[buf ^ 1]);
+    load_stage(ahead_tile, ahead_panel);
+    const Stage& now = stage[buf];
     if constexpr (kCpw > 0) {
 #pragma unroll
       for (int j = 0; j < kX; ++j)
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
           const u32x4 w1 = w[u][j];
-          const MvScales<kFmt, kWhole> s1 = sc[u][j];
-          load(tile + step + u, chunk_of(j), w[u][j], sc[u][j]);
-          mv_chunk<kFmt, kWhole, kRegs>(a, table, lane_off, w1, s1, x[j], tot + u * kRegs);
+          load_w(next_tile, 0, u, j);
+          const int at = (u * kMvTile + n_lane) * Stage::kStride + (wave + j * waves) * kGroups;
+          mv_chunk<kFmt, kRegs>(table, lane_off, w1, now.s + at, now.z + at, x[j], tot + u * kRegs);
         }
     } else {
-      for (int c = wave; c < chunks; c += kMvWaves) {
+      MvX<kFmt> x1[4];
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) load(tile + u, c, w[u][0], sc[u][0]);
-        mv_load_x<kFmt, kRegs>(a, t0, nt, c, lane, x[0]);
+      for (int s = 0; s < 4; ++s) x1[s] = x[0][s];
+      mv_load_x<kFmt, kRegs>(a, t0, nt, next_panel * kMvWaves + wave, lane, x[0]);
 #pragma unroll
-        for (int u = 0; u < kRows; ++u)
-          mv_chunk<kFmt, kWhole, kRegs>(a, table, lane_off, w[u][0], sc[u][0], x[0],
-                                        tot + u * kRegs);
+      for (int u = 0; u < kRows; ++u) {
+        const u32x4 w1 = w[u][0];
+        load_w(next_tile, next_panel, u, 0);
+        const int at = (u * kMvTile + n_lane) * Stage::kStride + wave * kGroups;
+        mv_chunk<kFmt, kRegs>(table, lane_off, w1, now.s + at, now.z + at, x1, tot + u * kRegs);
       }
     }
+    if (end) {
 #pragma unroll
-    for (int i = 0; i < kOut; ++i) red[buf][wave][i][lane] = tot[i];
-    __syncthreads();  // red[buf] is written again two rounds on, after the next barrier
-    if (wave < kOut) {
-      float v = 0.f;
-#pragma unroll
-      for (int u = 0; u < kMvWaves; ++u) v += red[buf][u][wave][lane];
-      const int t = q * kRegs + wave % kRegs;
-      const int64_t n = (int64_t)(tile + wave / kRegs) * kMvTile + n_lane;
-      if (t < nt && n < a.N) {
-        v = v * last + (a.bias ? a.bias[n] : 0.f);
-        const int64_t i = (t0 + t) * a.N + n;
-        if (a.y_dtype == kF32) reinterpret_cast<float*>(a.y)[i] = v;
-        else if (a.y_dtype == kBF16) reinterpret_cast<uint16_t*>(a.y)[i] = f32_to_bf16_bits(v);
-        else reinterpret_cast<_Float16*>(a.y)[i] = (_Float16)v;
-      }
+      for (int i = 0; i < kOut; ++i) red[out][wave][i][lane] = tot[i], tot[i] = 0.f;
     }
+    // orders this step's LDS writes before their readers, and its reads of stage[buf] before
+    // the next step's writes; red[out] is written again two rounds on
+    __syncthreads();
+    if (end) {
+      for (int i = wave; i < kOut; i += waves) {
+        float v = 0.f;
+        for (int u = 0; u < waves; ++u) v += red[out][u][i][lane];
+        const int t = q * kRegs + i % kRegs;
+        const int64_t n = (int64_t)(tile + i / kRegs) * kMvTile + n_lane;
+        if (t < nt && n < a.N) {
+          v = v * last + (a.bias ? a.bias[n] : 0.f);
+          const int64_t at = (t0 + t) * a.N + n;
+          if (a.y_dtype == kF32) reinterpret_cast<float*>(a.y)[at] = v;
+          else if (a.y_dtype == kBF16) reinterpret_cast<uint16_t*>(a.y)[at] = f32_to_bf16_bits(v);
+          else reinterpret_cast<_Float16*>(a.y)[at] = (_Float16)v;
+        }
+      }
+      out ^= 1;
+    }
+    tile = next_tile, panel = next_panel;
+    next_tile = ahead_tile, next_panel = ahead_panel;
   }
 }
 
 namespace {
 
-template <int kFmt, bool kWhole, int kRegs, int kCpw, int kRows>
-void mv_go(const MatvecArgs& a, int nx, unsigned ny, hipStream_t s) {
-  hipLaunchKernelGGL((matvec_kernel<kFmt, kWhole, kRegs, kCpw, kRows>), dim3((unsigned)nx, ny),
-                     dim3(kMvThreads), 0, s, a);
+template <int kFmt, int kRegs, int kCpw, int kRows>
+void mv_go(const MatvecArgs& a, int nx, unsigned ny, int waves, hipStream_t s) {
+  const int rounds = ((a.N + kMvTile - 1) / kMvTile + kRows - 1) / kRows;
+  hipLaunchKernelGGL((matvec_kernel<kFmt, kRegs, kCpw, kRows>),
+                     dim3((unsigned)(nx < rounds ? nx : rounds), ny), dim3(64 * waves), 0, s, a);
 }
 
-template <int kFmt, bool kWhole, int kRegs>
+template <int kFmt, int kRegs>
 void mv_launch(const MatvecArgs& a, int cus, hipStream_t s) {
   constexpr int kMany = kRegs == 1 ? 4 : 2;
   const unsigned ny = (unsigned)((a.T + kMvTokens - 1) / kMvTokens);
@@ -385,28 +409,21 @@ void mv_launch(const MatvecArgs& a, int cus, hipStream_t s) {
   // that the blocks of one tile run on the same XCD and share its L2
   int nx = cus / (int)ny / 8 * 8;
   if (nx < 8) nx = 8;
-  const bool many = tiles >= 2 * kMany * nx;
-  const int rounds = many ? (tiles + kMany - 1) / kMany : tiles;
-  if (nx > rounds) nx = rounds;
-  const int per = (a.K + kMvChunk * kMvWaves - 1) / (kMvChunk * kMvWaves);
-  if (per <= 1 && many) mv_go<kFmt, kWhole, kRegs, 1, kMany>(a, nx, ny, s);
-  else if (per <= 1) mv_go<kFmt, kWhole, kRegs, 1, 1>(a, nx, ny, s);
-  else if (per <= 2) mv_go<kFmt, kWhole, kRegs, 2, 1>(a, nx, ny, s);
-  else if (many) mv_go<kFmt, kWhole, kRegs, 0, kMany>(a, nx, ny, s);
-  else mv_go<kFmt, kWhole, kRegs, 0, 1>(a, nx, ny, s);
+  const int chunks = (a.K + kMvChunk - 1) / kMvChunk;
+  const int per = (chunks + kMvWaves - 1) / kMvWaves;
+  const int waves = (chunks + per - 1) / per;
+  if (per <= 1 && tiles >= 2 * kMany * nx) mv_go<kFmt, kRegs, 1, kMany>(a, nx, ny, waves, s);
+  else if (per <= 1) mv_go<kFmt, kRegs, 1, 1>(a, nx, ny, waves, s);
+  else if (per <= 2 && kRegs == 1 && tiles >= 4 * nx) mv_go<kFmt, kRegs, 2, kRegs == 1 ? 2 : 1>(a, nx, ny, waves, s);
+  else if (per <= 2) mv_go<kFmt, kRegs, 2, 1>(a, nx, ny, waves, s);
+  else if (tiles >= 4 * nx) mv_go<kFmt, kRegs, 0, 2>(a, nx, ny, kMvWaves, s);
+  else mv_go<kFmt, kRegs, 0, 1>(a, nx, ny, kMvWaves, s);
 }
 
 template <int kFmt>
 void mv_launch_format(const MatvecArgs& a, int cus, hipStream_t s) {
-  constexpr int kPer = mv_groups(kFmt);
-  const int size = kFmt == kMvfMX ? 1 : !mv_int(kFmt) || a.scale_dtype == kF32 ? 4 : 2;
-  const int read = kPer * size < 4 ? kPer * size : 4;
-  const bool whole = a.K % kMvChunk == 0 && (uintptr_t)a.scales % read == 0 &&
-                     (uintptr_t)a.zeros % kPer == 0;
-  if (whole && a.T <= 4) mv_launch<kFmt, true, 1>(a, cus, s);
-  else if (whole) mv_launch<kFmt, true, 4>(a, cus, s);
-  else if (a.T <= 4) mv_launch<kFmt, false, 1>(a, cus, s);
-  else mv_launch<kFmt, false, 4>(a, cus, s);
+  if (a.T <= 4) mv_launch<kFmt, 1>(a, cus, s);
+  else mv_launch<kFmt, 4>(a, cus, s);
 }
 
 }  // namespace
