@@ -167,12 +167,12 @@ __device__ __forceinline__ void mv_chunk(const char* lut, uint32_t lane_off, u32
       tot[i] = fmaf(scale[s * kGroups / 4], acc[s][i], tot[i]);
 }
 
-// The matrix unit's x operand of step s of chunk c: row m of the 16 is token
-// (m / 4) kRegs + m % 4 where m % 4 < kRegs, so that the first kRegs result
-// registers of a lane hold all tokens.
-template <int kFmt, int kRegs>
-__device__ __forceinline__ void mv_load_x(const MatvecArgs& a, int64_t t0, int nt, int c, int lane,
-                                          MvX<kFmt> (&x)[4]) {
+// The matrix unit's x operand of step s of chunk c as it is read (zero beyond the row
+// or the tokens): row m of the 16 is token (m / 4) kRegs + m % 4 where m % 4 < kRegs,
+// so that the first kRegs result registers of a lane hold all tokens.
+template <int kRegs>
+__device__ __forceinline__ void mv_read_x(const MatvecArgs& a, int64_t t0, int nt, int c, int lane,
+                                          u32x4 (&v)[4]) {
   const int left = a.K - c * kMvChunk;
   const int m = lane & 15, q = lane >> 4;
   const int t = (m >> 2) * kRegs + (m & 3);
@@ -180,16 +180,22 @@ __device__ __forceinline__ void mv_load_x(const MatvecArgs& a, int64_t t0, int n
   const uint16_t* p = reinterpret_cast<const uint16_t*>(a.x) + (t0 + t) * a.K + c * kMvChunk + 8 * q;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (live && 32 * s < left) v = *reinterpret_cast<const u32x4*>(p + 32 * s);
+    v[s] = u32x4{0u, 0u, 0u, 0u};
+    if (live && 32 * s < left) v[s] = *reinterpret_cast<const u32x4*>(p + 32 * s);
+  }
+}
+
+template <int kFmt>
+__device__ __forceinline__ void mv_set_x(const MatvecArgs& a, const u32x4 (&raw)[4],
+                                         MvX<kFmt> (&x)[4]) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    u32x4 v = raw[s];
     if (a.x_bf16) {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        o[i] = pack_half2((_Float16)bf16_bits_to_f32(w[i] & 0xffffu),
-                          (_Float16)bf16_bits_to_f32(w[i] >> 16));
-      v = u32x4{o[0], o[1], o[2], o[3]};
+        v[i] = pack_half2((_Float16)bf16_bits_to_f32(v[i] & 0xffffu),
+                          (_Float16)bf16_bits_to_f32(v[i] >> 16));
     }
     if constexpr (mv_split(kFmt)) {
       x[s].v[0] = __builtin_bit_cast(f16x8, (u32x4{v.x, v.x, v.y, v.y}));
@@ -201,7 +207,7 @@ __device__ __forceinline__ void mv_load_x(const MatvecArgs& a, int64_t t0, int n
 }
 
 // The decode table: 256 byte values x 256 bytes, as 32 copies of two words
-// (nf4) or 64 of one.  Ends with a barrier.
+// (nf4) or 64 of one.  A barrier has to follow.
 template <int kFmt>
 __device__ __forceinline__ void mv_fill(u32x4* lut, uint32_t* stage, int tid) {
   const float nf4[16] = NF4MOE_LEVELS_INIT;
@@ -220,7 +226,6 @@ __device__ __forceinline__ void mv_fill(u32x4* lut, uint32_t* stage, int tid) {
     const uint32_t l = (first >> 16) | (second & 0xffff0000u);
     lut[u] = mv_split(kFmt) ? u32x4{h, l, h, l} : u32x4{h, h, h, h};
   }
-  __syncthreads();
 }
 
 }  // namespace
@@ -314,19 +319,23 @@ __global__ __launch_bounds__(64 * kMvWaves) void matvec_kernel(MatvecArgs a) {
 
   int tile = blockIdx.x * kRows, panel = 0;
   int next_tile = tile, next_panel = panel;  // of the codes in flight
-  MvX<kFmt> x[kX][4];
+  // x and the first steps' reads are in flight while the table is made
+  u32x4 raw_x[kX][4];
   load_stage(tile, 0);
+#pragma unroll
+  for (int j = 0; j < kX; ++j) mv_read_x<kRegs>(a, t0, nt, wave + j * waves, lane, raw_x[j]);
 #pragma unroll
   for (int j = 0; j < kX; ++j)
 #pragma unroll
     for (int u = 0; u < kRows; ++u) load_w(tile, 0, u, j);
-#pragma unroll
-  for (int j = 0; j < kX; ++j)
-    mv_load_x<kFmt, kRegs>(a, t0, nt, wave + j * waves, lane, x[j]);
+  mv_fill<kFmt>(lut, levels, tid);
   put_stage(stage[0]);
   after(next_tile, next_panel);
   load_stage(next_tile, next_panel);
-  mv_fill<kFmt>(lut, levels, tid);
+  __syncthreads();
+  MvX<kFmt> x[kX][4];
+#pragma unroll
+  for (int j = 0; j < kCpw; ++j) mv_set_x<kFmt>(a, raw_x[j], x[j]);
   const char* table = reinterpret_cast<const char*>(lut);
   const float last = mv_split(kFmt) ? 1.0f / 256.0f : kFmt == kMvfFP4 ? 1.0f / 6.0f : 1.0f;
 
@@ -351,16 +360,14 @@ __global__ __launch_bounds__(64 * kMvWaves) void matvec_kernel(MatvecArgs a) {
           mv_chunk<kFmt, kRegs>(table, lane_off, w1, now.s + at, now.z + at, x[j], tot + u * kRegs);
         }
     } else {
-      MvX<kFmt> x1[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) x1[s] = x[0][s];
-      mv_load_x<kFmt, kRegs>(a, t0, nt, next_panel * kMvWaves + wave, lane, x[0]);
+      mv_set_x<kFmt>(a, raw_x[0], x[0]);
+      mv_read_x<kRegs>(a, t0, nt, next_panel * kMvWaves + wave, lane, raw_x[0]);
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
         const u32x4 w1 = w[u][0];
         load_w(next_tile, next_panel, u, 0);
         const int at = (u * kMvTile + n_lane) * Stage::kStride + wave * kGroups;
-        mv_chunk<kFmt, kRegs>(table, lane_off, w1, now.s + at, now.z + at, x1, tot + u * kRegs);
+        mv_chunk<kFmt, kRegs>(table, lane_off, w1, now.s + at, now.z + at, x[0], tot + u * kRegs);
       }
     }
     if (end) {
