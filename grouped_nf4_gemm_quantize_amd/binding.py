@@ -553,12 +553,22 @@ def _need(t, what: str, dev, shape=None, dtype=None):
 def _call(dev, fn, *args) -> None:
     """One C call on the current stream of ``dev``, which is made the current
     device for it if it is not."""
+    cuda = _torch().cuda
+    if cuda.current_device() == dev.index:
+        status = fn(*args, _raw_stream(dev.index))
+    else:
+        with cuda.device(dev):
+            status = fn(*args, _raw_stream(dev.index))
+    if status != 0:
+        _check(status)
+
+
+def _raw_stream(index: int) -> int:
+    """The handle of the current stream.  torch's own accessor for launchers costs 0.1 us,
+    a Stream object 1.8 us of the 10 us that a small call takes on the host."""
     torch = _torch()
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
-        return
-    with torch.cuda.device(dev):
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def nbit_matvec(x, codes, scales, quant_type: str = "nf4", group: Optional[int] = None,
