@@ -22,8 +22,8 @@ namespace nf4moe {
 
 namespace {
 
-constexpr int kNormGroups = 512;  // workgroups (and partial rows) of the backward
-constexpr int kNormWaves = 8;     // waves of a workgroup of several rows
+constexpr int kNormWaves = 8;      // waves of a workgroup of several rows, forward
+constexpr int kNormBwdWaves = 16;  // and backward: fewer partial rows
 constexpr int kNormMaxWaves = 16;  // waves of a workgroup of one row
 
 typedef __amdgpu_buffer_rsrc_t Rsrc;
@@ -107,17 +107,22 @@ __device__ __forceinline__ void write8(Rsrc r, int dtype, int col, float (&v)[8]
 }
 
 // How the waves of a workgroup share rows: kRowWaves waves a row in workgroups of
-// kNormWaves, or (kRowWaves 0) all waves of a workgroup of any size.
+// kAll, or (0, -1) all waves of a workgroup of up to 8 or 16.
 template <int kRowWaves>
+constexpr int norm_waves(int all) {
+  return kRowWaves > 0 ? all : kRowWaves ? kNormMaxWaves : kNormMaxWaves / 2;
+}
+
+template <int kRowWaves, int kAll>
 struct NormShape {
-  static constexpr int kRows = kRowWaves ? kNormWaves / kRowWaves : 1;
-  static constexpr int kWaves = kRowWaves ? kNormWaves : kNormMaxWaves;
+  static constexpr int kRows = kRowWaves > 0 ? kAll / kRowWaves : 1;
+  static constexpr int kWaves = norm_waves<kRowWaves>(kAll);
   int lane, sub, part, row_waves;  // sub: row of the workgroup; part: wave of the row
   __device__ NormShape() {
     lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    row_waves = kRowWaves ? kRowWaves : blockDim.x >> 6;
-    sub = kRowWaves ? wave / row_waves : 0;
+    row_waves = kRowWaves > 0 ? kRowWaves : blockDim.x >> 6;
+    sub = kRowWaves > 0 ? wave / row_waves : 0;
     part = wave - sub * row_waves;
   }
   __device__ int col(int u) const { return ((u * row_waves + part) * 64 + lane) * 8; }
@@ -125,10 +130,9 @@ struct NormShape {
 
 // Sums of kN values over the waves of a row, in every lane.  A barrier has to come
 // between two uses of `red`.
-template <int kN, int kRowWaves>
-__device__ __forceinline__ void row_sum(float (&v)[kN],
-                                        float (&red)[3][NormShape<kRowWaves>::kWaves],
-                                        const NormShape<kRowWaves>& at) {
+template <int kN, int kRowWaves, int kAll>
+__device__ __forceinline__ void row_sum(float (&v)[kN], float (*red)[kNormMaxWaves],
+                                        const NormShape<kRowWaves, kAll>& at) {
 #pragma unroll
   for (int i = 0; i < kN; ++i) v[i] = wave_sum(v[i]);
   if constexpr (kRowWaves != 1) {
@@ -137,11 +141,21 @@ __device__ __forceinline__ void row_sum(float (&v)[kN],
 #pragma unroll
       for (int i = 0; i < kN; ++i) red[i][first + at.part] = v[i];
     __syncthreads();
+    if constexpr (kRowWaves > 0) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      float s = 0.f;
-      for (int w = 0; w < at.row_waves; ++w) s += red[i][first + w];
-      v[i] = s;
+      for (int i = 0; i < kN; ++i) {
+        v[i] = red[i][first];
+#pragma unroll
+        for (int w = 1; w < kRowWaves; ++w) v[i] += red[i][first + w];
+      }
+    } else {
+      // lane l of each 16 takes wave l's sum: one read for any number of waves
+      const int w = at.lane & 15;
+      const bool in = w < at.row_waves;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = in ? red[i][first + w] : 0.f;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = row16_sum(v[i]);
     }
   }
 }
@@ -155,9 +169,9 @@ __device__ __forceinline__ float rstd_of(float sum, int H, float eps) {
 
 // kRes, kY: element sizes of the residual and of y (2 where there is none).
 template <int kRes, int kY, int kVec, int kRowWaves>
-__global__ __launch_bounds__(64 * NormShape<kRowWaves>::kWaves) void block_norm_kernel(BlockNormArgs a) {
-  const NormShape<kRowWaves> at;
-  __shared__ float red[2][3][at.kWaves];
+__global__ __launch_bounds__(64 * norm_waves<kRowWaves>(kNormWaves)) void block_norm_kernel(BlockNormArgs a) {
+  const NormShape<kRowWaves, kNormWaves> at;
+  __shared__ float red[2][1][kNormMaxWaves];
   constexpr int kRows = at.kRows;
   const int ws = a.w_dtype == kF32 ? 4 : 2;
   const Rsrc r_pre = span_of(a.w_pre, 0, a.w_pre ? a.H * ws : 0);
@@ -203,7 +217,7 @@ __global__ __launch_bounds__(64 * NormShape<kRowWaves>::kWaves) void block_norm_
         for (int u = 0; u < kVec; ++u)
 #pragma unroll
           for (int i = 0; i < 8; ++i) s[0] += z[u][i] * z[u][i];
-        row_sum<1, kRowWaves>(s, red[0], at);
+        row_sum<1>(s, red[0], at);
         rstd = rstd_of(s[0], a.H, a.eps);
       }
       const Rsrc r_out = span_of(a.r_out, row * kRes, n * kRes);
@@ -230,7 +244,7 @@ __global__ __launch_bounds__(64 * NormShape<kRowWaves>::kWaves) void block_norm_
       for (int u = 0; u < kVec; ++u)
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[0] += r[u][i] * r[u][i];
-      row_sum<1, kRowWaves>(s, red[1], at);
+      row_sum<1>(s, red[1], at);
       const float rstd = rstd_of(s[0], a.H, a.eps);
       const Rsrc r_h = span_of(a.h, row * hs, n * hs);
 #pragma unroll
@@ -245,25 +259,34 @@ __global__ __launch_bounds__(64 * NormShape<kRowWaves>::kWaves) void block_norm_
   }
 }
 
-// A workgroup takes rows in turn with the others; its sums over them of the column
-// gradients go to row blockIdx.x of the partial sums (dw_pre, dw_post, dgate
-// by channel).  kDh: element size of dh (2 where there is none).
-template <int kRes, int kY, int kDh, int kVec, int kRowWaves>
-__global__ __launch_bounds__(64 * NormShape<kRowWaves>::kWaves, 4) void block_norm_bwd_kernel(BlockNormArgs a) {
-  const NormShape<kRowWaves> at;
-  constexpr int kRows = at.kRows, kCols = kVec * kRowWaves * 512;
-  __shared__ float red[2][3][at.kWaves];
+// One row's matrices as they are read.
+template <int kRes, int kY, int kDh, int kVec>
+struct NormRow {
+  Raw8<kRes> r[kVec], d[kVec];
+  Raw8<kY> y[kVec];
+  Raw8<kDh> h[kVec];
+  float gate;
+};
+
+// A workgroup takes rows in turn with the others, the next one's reads in flight; its
+// sums over them of the column gradients go to row blockIdx.x of the partial sums
+// (dw_pre, dw_post, dgate by channel).  kDh: element size of dh (2 where there is none).
+// All sums of a row are taken at once: with dr = d + rstd_r dh w_pre - k_r r and
+// q = gate w_post y, sum dr q = sum d q + rstd_r sum dh w_pre q - k_r sum r q.
+template <int kRes, int kY, int kDh, int kVec, int kRowWaves, bool kGate>
+__global__ __launch_bounds__(64 * norm_waves<kRowWaves>(kNormBwdWaves), kRowWaves ? 4 : 3) void
+block_norm_bwd_kernel(BlockNormArgs a) {
+  const NormShape<kRowWaves, kNormBwdWaves> at;
+  constexpr int kRows = at.kRows, kCols = kRowWaves > 0 ? kVec * kRowWaves * 512 : 0;
+  __shared__ float red[2][6][kNormMaxWaves];
   // partial sums of the waves that share columns
   __shared__ f32x4 all[kRows > 1 ? kRows / 2 : 1][kRows > 1 ? kCols / 4 : 1];
   const int ws = a.w_dtype == kF32 ? 4 : 2;
   const Rsrc r_pre = span_of(a.w_pre, 0, a.w_pre ? a.H * ws : 0);
   const Rsrc r_post = span_of(a.w_post, 0, a.w_post ? a.H * ws : 0);
-  const Rsrc r_gate = span_of(a.gate, 0, a.gate_axis == 2 ? a.H * 4 : 0);
-  float s_pre[kVec][8] = {}, s_post[kVec][8] = {}, s_gate[kVec][8] = {};
-  const float inv_h = 1.0f / (float)a.H;
-  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.T;
-       first += (int64_t)gridDim.x * kRows) {
-    const int64_t t = first + at.sub;
+  const Rsrc r_gate = span_of(a.gate, 0, kGate ? a.H * 4 : 0);
+  typedef NormRow<kRes, kY, kDh, kVec> Row;
+  const auto read = [&](int64_t t, Row& o) {
     const bool live = t < a.T;
     const int n = live ? a.H : 0;
     const int64_t row = live ? t * a.H : 0;
@@ -271,88 +294,102 @@ __global__ __launch_bounds__(64 * NormShape<kRowWaves>::kWaves, 4) void block_no
     const Rsrc r_dh = span_of(a.dh, row * kDh, a.dh ? n * kDh : 0);
     const Rsrc r_d = span_of(a.d_r_out, row * kRes, a.d_r_out ? n * kRes : 0);
     const Rsrc r_y = span_of(a.y, row * kY, a.y ? n * kY : 0);
-    Raw8<kRes> r0[kVec], d0[kVec];
-    Raw8<kY> y0[kVec];
-    Raw8<kDh> h0[kVec];
-    Raw8<4> w0[kVec], w1[kVec], g0[kVec];
 #pragma unroll
     for (int u = 0; u < kVec; ++u) {
-      fetch8<kRes>(r_r, at.col(u), r0[u]);
-      fetch8<kDh>(r_dh, at.col(u), h0[u]);
-      fetch8<kY>(r_y, at.col(u), y0[u]);
-      fetch8<kRes>(r_d, at.col(u), d0[u]);
+      fetch8<kRes>(r_r, at.col(u), o.r[u]);
+      fetch8<kDh>(r_dh, at.col(u), o.h[u]);
+      fetch8<kY>(r_y, at.col(u), o.y[u]);
+      fetch8<kRes>(r_d, at.col(u), o.d[u]);
     }
+    o.gate = a.gate_axis == 1 && live ? a.gate[t] : 1.f;
+  };
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t t = (int64_t)blockIdx.x * kRows + at.sub;
+  Row next;
+  read(t, next);
+  // the columns' weights; without w_post z is y: weight 1
+  float w1[kVec][8], w0[kVec][8], gc[kGate ? kVec : 1][8];
 #pragma unroll
-    for (int u = 0; u < kVec; ++u) {
-      fetch8_any(r_pre, ws, at.col(u), w1[u]);
-      fetch8_any(r_post, ws, at.col(u), w0[u]);
-      if (a.gate_axis == 2) fetch8<4>(r_gate, at.col(u), g0[u]);
+  for (int u = 0; u < kVec; ++u) {
+    Raw8<4> p, q;
+    fetch8_any(r_pre, ws, at.col(u), p);
+    fetch8_any(r_post, ws, at.col(u), q);
+    widen8<4>(p, a.w_dtype, w1[u]);
+    widen8<4>(q, a.w_dtype, w0[u]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w1[u][i] += a.w_offset;
+      w0[u][i] = a.w_post ? w0[u][i] + a.w_offset : 1.f;
     }
-    float gt = a.alpha;
-    if (a.gate_axis == 1 && live) gt *= a.gate[t];
-    float r[kVec][8], d[kVec][8], y[kVec][8], g[kVec][8], wv[8];
-    float s[3] = {0.f, 0.f, 0.f};  // r^2, dh * w * r, y^2
+    if constexpr (kGate) {
+      fetch8<4>(r_gate, at.col(u), p);
+      widen8<4>(p, kF32, gc[u]);
+    }
+  }
+  float s_pre[kVec][8] = {}, s_post[kVec][8] = {}, s_gate[kGate ? kVec : 1][8] = {};
+  const float inv_h = 1.0f / (float)a.H;
+  // waves whose row is beyond the last (t >= T) take part in the barriers only
+  for (int buf = 0; t - at.sub < a.T; t += step, buf ^= 1) {
+    const bool live = t < a.T;
+    const int n = live ? a.H : 0;
+    const int64_t row = live ? t * a.H : 0;
+    float r[kVec][8], d[kVec][8], y[kVec][8], g[kVec][8];
+    const float gt = a.alpha * next.gate;
 #pragma unroll
     for (int u = 0; u < kVec; ++u) {
-      widen8<kRes>(r0[u], a.res_dtype, r[u]);
-      widen8<kDh>(h0[u], a.h_dtype, g[u]);
-      widen8<kY>(y0[u], a.y_dtype, y[u]);
-      widen8<4>(w1[u], a.w_dtype, wv);
+      widen8<kRes>(next.r[u], a.res_dtype, r[u]);
+      widen8<kDh>(next.h[u], a.h_dtype, g[u]);
+      widen8<kY>(next.y[u], a.y_dtype, y[u]);
+      widen8<kRes>(next.d[u], a.res_dtype, d[u]);
+    }
+    read(t + step, next);
+    // r^2, dh w r, y^2; d q, dh w q, r q
+    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < kVec; ++u)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        const float hw = g[u][i] * w1[u][i];
+        const float q = (kGate ? gc[u][i] * w0[u][i] : w0[u][i]) * y[u][i];
         s[0] += r[u][i] * r[u][i];
-        s[1] += g[u][i] * (wv[i] + a.w_offset) * r[u][i];
+        s[1] += hw * r[u][i];
         s[2] += y[u][i] * y[u][i];
+        s[3] += d[u][i] * q;
+        s[4] += hw * q;
+        s[5] += r[u][i] * q;
       }
-    }
-    row_sum<3, kRowWaves>(s, red[0], at);
+    row_sum<6>(s, red[buf], at);
     // without w_pre (or a row) r and dh are zero here, and so is all they give
     const float rstd_r = a.w_pre && live ? rstd_of(s[0], a.H, a.eps) : 0.f;
     const float k_r = rstd_r * rstd_r * rstd_r * (s[1] * inv_h);
     const float rstd_y = !a.w_post ? 1.f : live ? rstd_of(s[2], a.H, a.eps) : 0.f;
-    float s2[2] = {0.f, 0.f};  // dz * w * y, dr * z
+    const float dr_q = s[3] + rstd_r * s[4] - k_r * s[5];
+    if (a.gate_axis == 1 && live && at.part == 0 && at.lane == 0)
+      a.dgate[t] = a.alpha * rstd_y * dr_q;
+    const float k_y = a.w_post ? rstd_y * rstd_y * rstd_y * (gt * dr_q * inv_h) : 0.f;
     const Rsrc r_out = span_of(a.r_out, row * kRes, n * kRes);
+    const Rsrc r_dy = span_of(a.h, row * kY, a.y ? n * kY : 0);
 #pragma unroll
     for (int u = 0; u < kVec; ++u) {
-      widen8<kRes>(d0[u], a.res_dtype, d[u]);
-      widen8<4>(w1[u], a.w_dtype, wv);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         s_pre[u][i] += g[u][i] * r[u][i] * rstd_r;
-        d[u][i] += rstd_r * g[u][i] * (wv[i] + a.w_offset) - r[u][i] * k_r;
-        // d is dr; r becomes dresidual
+        // d becomes dr, r dresidual
+        d[u][i] += rstd_r * g[u][i] * w1[u][i] - r[u][i] * k_r;
         r[u][i] = a.beta * d[u][i];
+        // g becomes the gradient dz of z, then dy
+        g[u][i] = gt * d[u][i];
+        const float yn = y[u][i] * rstd_y;
+        if constexpr (kGate) {
+          s_gate[u][i] += a.alpha * d[u][i] * (yn * w0[u][i]);
+          g[u][i] *= gc[u][i];
+        }
+        s_post[u][i] += g[u][i] * yn;
+        g[u][i] = rstd_y * (g[u][i] * w0[u][i]) - y[u][i] * k_y;
       }
       write8(r_out, a.res_dtype, at.col(u), r[u]);
-      if (!a.y) continue;
-      widen8<4>(w0[u], a.w_dtype, wv);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float w = a.w_post ? wv[i] + a.w_offset : 1.f;
-        const float z = y[u][i] * rstd_y * w;
-        s2[1] += d[u][i] * z;
-        s_gate[u][i] += a.alpha * d[u][i] * z;
-        // g becomes the gradient dz of z
-        g[u][i] = gt * d[u][i];
-        if (a.gate_axis == 2) g[u][i] *= __uint_as_float(g0[u].v[i >> 2][i & 3]);
-        s_post[u][i] += g[u][i] * y[u][i] * rstd_y;
-        g[u][i] *= w;
-        s2[0] += g[u][i] * y[u][i];
-      }
+      write8(r_dy, a.y_dtype, at.col(u), g[u]);
     }
-    if (a.y) {
-      row_sum<2, kRowWaves>(s2, red[1], at);
-      if (a.gate_axis == 1 && live && at.part == 0 && at.lane == 0) a.dgate[t] = a.alpha * s2[1];
-      const float k_y = a.w_post ? rstd_y * rstd_y * rstd_y * (s2[0] * inv_h) : 0.f;
-      const Rsrc r_dy = span_of(a.h, row * kY, n * kY);
-#pragma unroll
-      for (int u = 0; u < kVec; ++u) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[u][i] = rstd_y * g[u][i] - y[u][i] * k_y;
-        write8(r_dy, a.y_dtype, at.col(u), g[u]);
-      }
-    }
-    if constexpr (kRowWaves != 1) __syncthreads();  // `red` is written again for the next row
   }
   // the sums of waves that share columns, in halves: the upper half hands over
   const auto join = [&](float (&v)[kVec][8]) {
@@ -385,7 +422,7 @@ __global__ __launch_bounds__(64 * NormShape<kRowWaves>::kWaves, 4) void block_no
   };
   if (a.w_pre) put(s_pre, 0);
   if (a.w_post) put(s_post, 1);
-  if (a.gate_axis == 2) put(s_gate, 2);
+  if constexpr (kGate) put(s_gate, 2);
 }
 
 // out[c] = sum over the partial rows: 16 lanes of four columns, the 16 x 4 row
@@ -422,21 +459,29 @@ int norm_row_waves(int H) {
   return w == 3 ? 4 : w;
 }
 
-template <int kRes, int kY, int kVec, int kRowWaves>
-void norm_go(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
-  const int row_waves = norm_row_waves(a.H);
-  const dim3 block(64 * (kRowWaves ? kNormWaves : row_waves));
-  constexpr int kRows = NormShape<kRowWaves>::kRows;
-  const int64_t rounds = (a.T + kRows - 1) / kRows;
-  if (!bwd_groups)
-    hipLaunchKernelGGL((block_norm_kernel<kRes, kY, kVec, kRowWaves>),
-                       dim3((unsigned)(rounds < (1 << 20) ? rounds : (1 << 20))), block, 0, s, a);
-  else if (a.dh && a.h_dtype == kF32)
-    hipLaunchKernelGGL((block_norm_bwd_kernel<kRes, kY, 4, kVec, kRowWaves>), dim3(bwd_groups),
+template <int kRes, int kY, int kDh, int kVec, int kRowWaves>
+void norm_bwd_go(const BlockNormArgs& a, int groups, hipStream_t s) {
+  const dim3 block(64 * (kRowWaves > 0 ? kNormBwdWaves : norm_row_waves(a.H)));
+  if (a.gate_axis == 2)
+    hipLaunchKernelGGL((block_norm_bwd_kernel<kRes, kY, kDh, kVec, kRowWaves, true>), dim3(groups),
                        block, 0, s, a);
   else
-    hipLaunchKernelGGL((block_norm_bwd_kernel<kRes, kY, 2, kVec, kRowWaves>), dim3(bwd_groups),
+    hipLaunchKernelGGL((block_norm_bwd_kernel<kRes, kY, kDh, kVec, kRowWaves, false>), dim3(groups),
                        block, 0, s, a);
+}
+
+template <int kRes, int kY, int kVec, int kRowWaves>
+void norm_go(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
+  if (bwd_groups) {
+    if (a.dh && a.h_dtype == kF32) norm_bwd_go<kRes, kY, 4, kVec, kRowWaves>(a, bwd_groups, s);
+    else norm_bwd_go<kRes, kY, 2, kVec, kRowWaves>(a, bwd_groups, s);
+    return;
+  }
+  const dim3 block(64 * (kRowWaves > 0 ? kNormWaves : norm_row_waves(a.H)));
+  constexpr int kRows = NormShape<kRowWaves, kNormWaves>::kRows;
+  const int64_t rounds = (a.T + kRows - 1) / kRows;
+  hipLaunchKernelGGL((block_norm_kernel<kRes, kY, kVec, kRowWaves>),
+                     dim3((unsigned)(rounds < (1 << 20) ? rounds : (1 << 20))), block, 0, s, a);
 }
 
 template <int kRes, int kY>
@@ -446,8 +491,9 @@ void norm_sizes(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
     case 2: return norm_go<kRes, kY, 1, 2>(a, bwd_groups, s);
     case 4: return norm_go<kRes, kY, 1, 4>(a, bwd_groups, s);
   }
-  if (a.H <= 512 * kNormMaxWaves) norm_go<kRes, kY, 1, 0>(a, bwd_groups, s);
-  else norm_go<kRes, kY, 2, 0>(a, bwd_groups, s);
+  if (a.H <= 512 * kNormMaxWaves / 2) norm_go<kRes, kY, 1, 0>(a, bwd_groups, s);
+  else if (a.H <= 512 * kNormMaxWaves) norm_go<kRes, kY, 1, -1>(a, bwd_groups, s);
+  else norm_go<kRes, kY, 2, -1>(a, bwd_groups, s);
 }
 
 void norm_launch(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
@@ -460,11 +506,12 @@ void norm_launch(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
 
 }  // namespace
 
+// One workgroup of sixteen waves a compute unit, or two of up to eight.
 int block_norm_groups(int64_t T, int H) {
   const int waves = norm_row_waves(H);
-  const int64_t rows = waves <= 4 ? kNormWaves / waves : 1;
-  const int64_t rounds = (T + rows - 1) / rows;
-  return (int)(rounds < kNormGroups ? rounds : kNormGroups);
+  const int64_t rows = waves <= 4 ? kNormBwdWaves / waves : 1;
+  const int64_t rounds = (T + rows - 1) / rows, most = waves > 4 && waves <= 8 ? 512 : 256;
+  return (int)(rounds < most ? rounds : most);
 }
 
 hipError_t launch_block_norm(const BlockNormArgs& a, int num_cus, hipStream_t s) {
