@@ -43,6 +43,7 @@ constexpr int kFactorThreads = 1024;  // of the one
 constexpr int kFactorWaves = kFactorThreads / 64;
 constexpr int kFactorReads = 9;       // reads of four elements a thread: 36864 elements
 constexpr int kFactorFloats = 33792;  // LDS copy of u, with its padding
+constexpr int kSmallFactor = 16384;   // elements of a factor that one workgroup takes in any case
 
 __device__ __forceinline__ f64x4 mfma64(double a, double b, f64x4 c) {
   return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
@@ -621,8 +622,10 @@ hipError_t muon_go(const MuonArgs& a, int lds, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_muon(MuonArgs& a, int num_cus, hipStream_t s) {
-  // one workgroup a factor where half the compute units or more get one and all fit
-  int64_t factors = 0, floats = 0;
+  // One workgroup a factor where all fit, and either half the compute units or more get one, or
+  // factors are small: 64 factors of 8 x 2048 take 20-24 us in two launches, 128 of them 19-20
+  // in one; 64 of 16 x 2048 take 22-25 us in two, 128 of them 31 in one.
+  int64_t factors = 0, floats = 0, most = 0;
   bool vec = true;
   for (int i = 0; i < a.count; ++i) {
     MuonTensor& t = a.t[i];
@@ -631,10 +634,11 @@ hipError_t launch_muon(MuonArgs& a, int num_cus, hipStream_t s) {
     const int64_t need = t.rank_major ? (int64_t)t.r * t.lds_row : t.r * t.n + 16;
     floats = need > floats ? need : floats;
     factors += t.E;
+    most = t.r * t.n > most ? t.r * t.n : most;
     vec = vec && t.vec;
   }
   int lds = 0;
-  if (2 * factors >= num_cus && floats <= kFactorFloats) {
+  if (floats <= kFactorFloats && (2 * factors >= num_cus || most <= kSmallFactor)) {
     lds = (int)floats * 4;
     a.blocks = 0;
     for (int i = 0; i < a.count; ++i) {

@@ -41,7 +41,9 @@ def ns(u, rank_major, steps=5, eps=1e-7):
 @pytest.mark.parametrize("rank_major", [True, False])
 @pytest.mark.parametrize("E,r,n", [(1, 1, 1), (2, 1, 700), (3, 2, 65), (1, 3, 1000), (2, 5, 257),
                                    (4, 7, 31), (3, 8, 2048), (2, 9, 513), (1, 12, 64),
-                                   (2, 16, 4100), (5, 16, 16), (2, 16, 5), (1, 11, 3)])
+                                   (2, 16, 4100), (5, 16, 16), (2, 16, 5), (1, 11, 3),
+                                   (2, 3, 20001), (2, 6, 9000), (3, 16, 3333), (1, 1, 70000),
+                                   (260, 16, 2200)])
 def test_orthogonalize(gpu_lib, E, r, n, rank_major):
     u = factor(E, r, n, rank_major)
     o = gpu_lib.lora_orthogonalize(torch.from_numpy(u).to(DEV), rank_major=rank_major)
@@ -128,13 +130,16 @@ SHAPES = [(4, 8, 2048, True), (4, 8, 1024, False), (3, 5, 100, True), (2, 16, 77
 
 
 MANY = [(130, 8, 256, True), (130, 8, 256, False), (20, 5, 77, True), (30, 6, 51, False)]
+# factors beyond one workgroup, aligned and not
+BIG = [(2, 16, 4096, True), (2, 16, 2560, False), (1, 8, 8192, False), (3, 4, 512, True)]
+BIG_ODD = [(2, 16, 4099, True), (2, 7, 6001, False)]
 
 
 @pytest.mark.parametrize("wt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("nesterov", [True, False])
-@pytest.mark.parametrize("count", [1, 4, 8, "many"])
-def test_step(gpu_lib, wt, nesterov, count):
-    t = step_case(MANY if count == "many" else SHAPES[:count], wt)
+@pytest.mark.parametrize("shapes", [SHAPES[:1], SHAPES[:4], SHAPES, MANY, BIG, BIG_ODD])
+def test_step(gpu_lib, wt, nesterov, shapes):
+    t = step_case(shapes, wt)
     before = [{k: v.clone() if torch.is_tensor(v) else v for k, v in d.items()} for d in t]
     gpu_lib.lora_muon_step(t, lr=0.02, momentum=0.9, nesterov=nesterov, weight_decay=0.1)
     check_step(before, t, wt, 0.02, 0.9, nesterov, 0.1)
