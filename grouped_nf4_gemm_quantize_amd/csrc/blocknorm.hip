@@ -169,7 +169,7 @@ __device__ __forceinline__ float rstd_of(float sum, int H, float eps) {
 
 // kRes, kY: element sizes of the residual and of y (2 where there is none).
 template <int kRes, int kY, int kVec, int kRowWaves>
-__global__ __launch_bounds__(64 * norm_waves<kRowWaves>(kNormWaves)) void block_norm_kernel(BlockNormArgs a) {
+__global__ __launch_bounds__(64 * norm_waves<kRowWaves>(kNormWaves), kVec == 1 ? 8 : 4) void block_norm_kernel(BlockNormArgs a) {
   const NormShape<kRowWaves, kNormWaves> at;
   __shared__ float red[2][1][kNormMaxWaves];
   constexpr int kRows = at.kRows;
