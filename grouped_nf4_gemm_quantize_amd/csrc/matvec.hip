@@ -13,13 +13,16 @@
 // tile) in chunks of 128, chunk c going to wave c % waves.  A lane reads 16 consecutive
 // packed bytes (32 codes) of one row; four lane swaps then give each of the chunk's four
 // matrix steps 32 consecutive k, all of one scale group, whose sum is scaled in fp32.
-// A wave's part of x stays in registers from tile to tile, and the next tiles' codes
-// are in flight while a tile is computed.  The waves' sums meet in LDS.
+// A wave's part of x stays in registers from tile to tile (up to K = 4096), and the
+// next tiles' codes are in flight while a tile is computed.  The waves' sums meet in LDS.
+// Measured (one MI355X, a call among others): nf4 151936 x 2048, four tokens, fp32 out
+// 41 us = 4.3 TB/s of codes and scales; int4 28672 x 4096, one token 15.8 us = 3.9 TB/s; below
+// some 10 MB launch and first reads set the time (2048 x 2048, one token: 5.6 us).
 //
 // Scales and zeros go through LDS too: read by the wave that uses them, a chunk's few
 // bytes of 16 rows cost as many cache lines as its codes (28672 x 4096 int4, groups of 128,
 // one token: 28.7 us, without these reads 15.9 us).  The workgroup reads a round's
-// as consecutive elements instead, one round ahead.
+// as consecutive elements instead, two steps ahead (16.5 us).
 //
 // nf4's levels are no fp16 values: each is held as a sum of two (22 bits),
 // scaled by 2^8 so that the small parts stay normal, and multiplied twice.  All
@@ -409,7 +412,6 @@ void mv_go(const MatvecArgs& a, int nx, unsigned ny, int waves, hipStream_t s) {
 
 template <int kFmt, int kRegs>
 void mv_launch(const MatvecArgs& a, int cus, hipStream_t s) {
-  constexpr int kMany = kRegs == 1 ? 4 : 2;
   const unsigned ny = (unsigned)((a.T + kMvTokens - 1) / kMvTokens);
   const int tiles = (a.N + kMvTile - 1) / kMvTile;
   // one workgroup per compute unit, shared by the token blocks; a multiple of 8, so
@@ -418,17 +420,29 @@ void mv_launch(const MatvecArgs& a, int cus, hipStream_t s) {
   if (nx < 8) nx = 8;
   const int chunks = (a.K + kMvChunk - 1) / kMvChunk;
   const int per = (chunks + kMvWaves - 1) / kMvWaves;
+  // as few waves as take the chunks in as many turns
   const int waves = (chunks + per - 1) / per;
-  if (per <= 1 && tiles >= 2 * kMany * nx) mv_go<kFmt, kRegs, 1, kMany>(a, nx, ny, waves, s);
-  else if (per <= 1) mv_go<kFmt, kRegs, 1, 1>(a, nx, ny, waves, s);
-  else if (per <= 2 && kRegs == 1 && tiles >= 4 * nx) mv_go<kFmt, kRegs, 2, kRegs == 1 ? 2 : 1>(a, nx, ny, waves, s);
-  else if (per <= 2) mv_go<kFmt, kRegs, 2, 1>(a, nx, ny, waves, s);
-  else if (tiles >= 4 * nx) mv_go<kFmt, kRegs, 0, 2>(a, nx, ny, kMvWaves, s);
+  // Tiles of a round: several save barriers and reads of x and cost balance between
+  // workgroups; sixteen tokens' sums leave LDS for two.  nf4, us for one and several:
+  //   up to 4 tokens, K 2048, one | four: N 4096 5.7 | 8.3, 32768 13.3 | 14.0, 65536 23.5 | 21.3
+  //   16 tokens, K 2048, one | two: N 4096 7.0 | 7.7, 8192 8.7 | 7.9, 65536 31 | 25
+  //   one token, K 8192, one | two | four: N 4096 10.8 | 12.7 | -, 8192 17.5 | 14.0 | 18.5,
+  //   16384 33 | 24.0 | 20.8, 32768 64 | 44 | 40.5
+  // Where a wave has two chunks they are even (int4, K 4096, N 28672 17.0 | 16.9).
+  constexpr int kMany = kRegs == 1 ? 4 : 2;
+  if (per == 1 && tiles >= (kRegs == 1 ? 16 : 2) * nx)
+    mv_go<kFmt, kRegs, 1, kMany>(a, nx, ny, waves, s);
+  else if (per == 1) mv_go<kFmt, kRegs, 1, 1>(a, nx, ny, waves, s);
+  else if (per == 2) mv_go<kFmt, kRegs, 2, 1>(a, nx, ny, waves, s);
+  else if (tiles >= kMany * nx) mv_go<kFmt, kRegs, 0, kMany>(a, nx, ny, kMvWaves, s);
+  else if (kRegs == 1 && tiles >= 2 * nx) mv_go<kFmt, kRegs, 0, 2>(a, nx, ny, kMvWaves, s);
   else mv_go<kFmt, kRegs, 0, 1>(a, nx, ny, kMvWaves, s);
 }
 
 template <int kFmt>
 void mv_launch_format(const MatvecArgs& a, int cus, hipStream_t s) {
+  // results of up to four tokens are one register a lane: fewer sums (nf4, K 8192, N 8192: one
+  // token 14.0 us, sixteen 17.7)
   if (a.T <= 4) mv_launch<kFmt, 1>(a, cus, s);
   else mv_launch<kFmt, 4>(a, cus, s);
 }

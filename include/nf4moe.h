@@ -520,10 +520,13 @@ int moe_expert_forward_routing(void* workspace, int64_t T, int H, int I,
  *               and FP4, ignored for MXFP4);
  *   bias        nullable fp32 [N];
  *   y [T, N]    F32, BF16 or F16; must not overlap the inputs.
- * 16 rows of x share one read of the matrix; more rows read it again (mostly from
- * cache), so from about 128 rows on the grouped GEMM with E = 1 is the
- * better call.  No workspace.  The order of the sums depends on the sizes only:
- * results are the same from call to call.
+ * Non-finite x makes its row of y non-finite, a non-finite scale its column
+ * (an infinity may come out as NaN); no other results change.
+ * 16 rows of x share one read of the matrix, more rows read it again (mostly from
+ * cache): from 128 to 512 rows on, earlier for larger N, the grouped GEMM with E = 1
+ * is the better call (nf4 16384 x 2048: 64 rows 25 us against 39, 256 rows 73 against 53).
+ * No workspace.  The order of the sums depends on the sizes only: results are the
+ * same from call to call.
  * Alignment (else EINVAL): x and codes 16 bytes, scales, bias and y their
  * element.  T beyond NF4MOE_MATVEC_MAX_T, N beyond 2^31 - 65 or K beyond 2^24 ->
  * EOVERFLOW. */

@@ -86,13 +86,21 @@ def test_types_bias_and_no_zeros(gpu_lib, xt, out, sd):
     check(y, ref, mag, K, out)
 
 
-def test_many_row_tiles(gpu_lib):
-    """More output rows than one pass of the grid takes."""
-    N, K = 40003, 256
-    for T in (1, 5):
-        x, codes, st, s, z = make("nf4", 64, T, N, K)
-        ref, mag = oracle.matvec(x.float().numpy(), codes, s, "nf4", 64)
-        check(run(gpu_lib, x, codes, st, z, "nf4", 64, out_dtype=torch.float32), ref, mag, K, "f32")
+@pytest.mark.parametrize("N,K,T", [(40003, 256, 1), (40003, 256, 5), (70001, 128, 1), (70001, 128, 4),
+                                   (9007, 256, 16), (9007, 4224, 1), (16401, 4224, 2),
+                                   (16401, 4224, 9), (9007, 2112, 3), (5000, 4160, 33)])
+@pytest.mark.parametrize("qt,group", [("nf4", 64), ("int4", 32), ("mxfp4", 32)])
+def test_many_row_tiles(gpu_lib, qt, group, N, K, T):
+    """More output rows than one pass of the grid takes, in rounds of one to four
+    tiles; checked at the edges of the tiles and rounds and at some rows between."""
+    x, codes, st, s, z = make(qt, group, T, N, K)
+    y = run(gpu_lib, x, codes, st, z, qt, group, out_dtype=torch.float32)
+    rng = np.random.default_rng(8)
+    rows = np.unique(np.concatenate([np.arange(130), np.arange(4060, 4140), np.arange(N - 70, N),
+                                     rng.integers(0, N, 300)]))
+    ref, mag = oracle.matvec(x.float().numpy(), codes[rows], s[rows], qt, group,
+                             None if z is None else z[rows])
+    check(y[:, torch.from_numpy(rows).to(DEV)], ref, mag, K, "f32")
 
 
 def test_quantised_stack_slice_and_untouched_neighbours(gpu_lib):
