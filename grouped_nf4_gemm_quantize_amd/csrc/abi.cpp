@@ -1241,6 +1241,7 @@ int nbit_matvec(int quant_type, const void* x, int x_dtype, int64_t T, const uin
   if (T > NF4MOE_MATVEC_MAX_T || N > (int64_t)INT32_MAX - 64 || K > ((int64_t)1 << 24))
     return fail(NF4MOE_EOVERFLOW, "T=%lld, N=%lld or K=%lld is too large", (long long)T,
                 (long long)N, (long long)K);
+  if (y == x) return fail(NF4MOE_EINVAL, "y must not be x");
   const size_t sb = quant_type == kMvMXFP4 ? 1 : dtype_bytes(scale_dtype);
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, sb) || !aligned(bias, 4) ||
       !aligned(y, dtype_bytes(y_dtype)))
@@ -1323,6 +1324,10 @@ int block_norm_forward(const void* residual, int res_dtype, const void* y, int y
   if (!aligned(residual, 16) || !aligned(y, 16) || !aligned(w_pre, 16) || !aligned(w_post, 16) ||
       !aligned(r_out, 16) || !aligned(h, 16) || !aligned(gate, 4))
     return fail(NF4MOE_EINVAL, "misaligned buffer (16 bytes; gate 4)");
+  if (h != nullptr && (h == r_out || h == residual || (h == y && h_dtype != y_dtype)))
+    return fail(NF4MOE_EINVAL, "h may be y of the same type, and no other of the matrices");
+  if (r_out != nullptr && r_out == y)
+    return fail(NF4MOE_EINVAL, "r_out must not be y");
   int cus = 0;
   st = cu_count(&cus);
   if (st != NF4MOE_OK) return st;
@@ -1378,6 +1383,10 @@ int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const 
       !aligned(w_pre, 16) || !aligned(w_post, 16) || !aligned(dresidual, 16) || !aligned(dy, 16) ||
       !aligned(gate, 4) || !aligned(dgate, 4) || !aligned(dw_pre, 4) || !aligned(dw_post, 4))
     return fail(NF4MOE_EINVAL, "misaligned buffer (16 bytes; gate, dgate, dw_pre and dw_post 4)");
+  if (dresidual == dy || dresidual == y || dresidual == dh || dresidual == r)
+    return fail(NF4MOE_EINVAL, "dresidual may be d_r_out, and no other of the matrices");
+  if (dy != nullptr && (dy == r || dy == d_r_out || (dy == dh && y_dtype != h_dtype)))
+    return fail(NF4MOE_EINVAL, "dy may be y, or dh of the same type, and no other of the matrices");
   const size_t need = block_norm_backward_workspace(T, H);
   if (workspace == nullptr || ws_bytes < need)
     return fail(NF4MOE_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need,
@@ -1542,6 +1551,24 @@ int lora_muon_step(const nf4moe_muon_tensor* tensors, int count, double lr, doub
     t.w_dtype = s.w_dtype;
     t.w16_dtype = s.w16_dtype;
   }
+  // no output may be another array of the call: factors are updated at the same time
+  for (int i = 0; i < count; ++i) {
+    const void* out[3] = {tensors[i].m_out, tensors[i].w_out, tensors[i].w16};
+    for (int o = 0; o < 3; ++o) {
+      if (out[o] == nullptr) continue;
+      for (int j = 0; j < count; ++j) {
+        const nf4moe_muon_tensor& s = tensors[j];
+        const void* other[6] = {s.grad, s.m, s.w, s.m_out, s.w_out, s.w16};
+        for (int k = 0; k < 6; ++k) {
+          // itself, m_out in place of m, w_out in place of w
+          if (i == j && (k == 3 + o || (o < 2 && k == 1 + o))) continue;
+          if (out[o] == other[k])
+            return fail(NF4MOE_EINVAL, "tensors %d and %d: an output is another array of the call",
+                        i, j);
+        }
+      }
+    }
+  }
   return muon_run(m, workspace, ws_bytes, stream);
 }
 
@@ -1563,6 +1590,8 @@ int lora_orthogonalize(const void* u, int u_dtype, int E, int r, int64_t n, int 
     return fail(NF4MOE_EDTYPE, "unknown dtype (u %d, out %d)", u_dtype, out_dtype);
   if (!aligned(u, dtype_bytes(u_dtype)) || !aligned(out, dtype_bytes(out_dtype)))
     return fail(NF4MOE_EINVAL, "misaligned buffer (each needs its element)");
+  if (out == u && out_dtype != u_dtype)
+    return fail(NF4MOE_EINVAL, "out may be u only if the types agree");
   MuonArgs m{};
   m.count = 1;
   m.steps = ns_steps;

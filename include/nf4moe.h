@@ -549,7 +549,8 @@ int nbit_matvec(int quant_type, const void* x, int x_dtype, int64_t T,
  * w_post and the gate absent).  w_pre and h NULL: only r is computed.
  *   residual, r_out [T, H] of res_dtype; y [T, H] of y_dtype; h [T, H] of
  *               h_dtype (each F32, BF16 or F16); r_out may be residual (in
- *               place), h may be y if the types agree; no other overlap;
+ *               place), h may be y if the types agree; no other overlap (EINVAL
+ *               for equal pointers);
  *   w_pre, w_post  [H] of w_dtype (F32, BF16 or F16);
  *   gate        fp32: NF4MOE_GATE_TOKEN [T] or NF4MOE_GATE_CHANNEL [H];
  *               NF4MOE_GATE_NONE with NULL: 1;
@@ -584,12 +585,12 @@ int block_norm_forward(const void* residual, int res_dtype, const void* y, int y
  *   dgate       fp32 like gate; dw_pre, dw_post fp32 [H]: required exactly where
  *               their inputs are given.  dresidual may be d_r_out and dy
  *               may be y or dh (types agreeing), each element is read before it
- *               is written; no other overlap;
+ *               is written; no other overlap (EINVAL for equal pointers);
  *   workspace   block_norm_backward_workspace(T, H) bytes, 256-byte aligned
  *               (EWORKSPACE, EINVAL).
  * Sums over T are taken per workgroup and then over the workgroups in a fixed
- * order: results are the same from call to call.  Other arguments and errors as
- * in the forward.  block_norm_backward_workspace returns 0 for invalid sizes. */
+ * order: results are the same from call to call.  Two calls must not share a workspace
+ * while both run.  Other arguments and errors as in the forward.  block_norm_backward_workspace returns 0 for invalid sizes. */
 size_t block_norm_backward_workspace(int64_t T, int64_t H);
 int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const void* r,
                         int res_dtype, const void* y, int y_dtype, const float* gate,
@@ -615,12 +616,15 @@ int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const 
  *   w16             nullable: a second copy of w_out rounded to w16_dtype (BF16
  *                   or F16) once more, for fp32 w (the adapter the layer reads);
  *   r               1 .. NF4MOE_MAX_LORA_R; E, n >= 1 (r > n is allowed);
- *   tensors [host]  1 .. NF4MOE_MAX_MUON_TENSORS factors in one call, which
- *                   must not share outputs;
+ *   tensors [host]  1 .. NF4MOE_MAX_MUON_TENSORS factors in one call; but for m_out = m
+ *                   and w_out = w no output may overlap another array of the call
+ *                   (EINVAL for equal pointers);
  *   ns_steps        1 .. 16; lr, mu, weight_decay, scale, a, b, c finite,
  *                   ns_eps >= 0 (EINVAL);
  *   workspace       lora_muon_step_workspace(tensors, count) bytes, 256-byte
- *                   aligned; 0 for invalid arguments.
+ *                   aligned; 0 for invalid arguments.  Two calls must not share
+ *                   it while both run.
+ * lr and the other scalars are taken at the call: a captured call keeps them.
  * Pointers are aligned to their element.  r * n at most 2^29 and, a workgroup taking
  * 8192 elements of a factor, at most 2^20 workgroups a tensor (EOVERFLOW). */
 #define NF4MOE_MAX_MUON_TENSORS 8

@@ -23,7 +23,7 @@ def _refuse(lib, status, fn, defaults, changes):
 
 
 MATVEC = dict(qt=0, x=FAKE, xd=2, T=1, codes=FAKE, scales=FAKE, sd=0, zeros=None, group=64, N=5,
-              K=128, bias=None, y=FAKE, yd=1, stream=None)
+              K=128, bias=None, y=FAKE + 0x1000, yd=1, stream=None)
 
 
 @pytest.mark.parametrize("status,changes", [
@@ -35,14 +35,15 @@ MATVEC = dict(qt=0, x=FAKE, xd=2, T=1, codes=FAKE, scales=FAKE, sd=0, zeros=None
     (-5, dict(sd=1)), (-5, dict(qt=2, sd=7)), (-2, dict(K=96)), (-2, dict(qt=7, group=32, K=48)),
     (-2, dict(qt=2, group=128, K=192)), (-7, dict(T=262145)), (-7, dict(N=1 << 31)),
     (-7, dict(K=(1 << 24) + 64)), (-1, dict(x=FAKE + 8)), (-1, dict(codes=FAKE + 4)),
-    (-1, dict(scales=FAKE + 2)), (-1, dict(bias=FAKE + 2)), (-1, dict(y=FAKE + 1)),
+    (-1, dict(y=FAKE)), (-1, dict(scales=FAKE + 2)), (-1, dict(bias=FAKE + 2)), (-1, dict(y=FAKE + 1)),
     (-1, dict(qt=2, sd=2, scales=FAKE + 1))])
 def test_matvec_refuses(lib, status, changes):
     _refuse(lib, status, lib.nbit_matvec, MATVEC, changes)
 
 
-NORM = dict(res=FAKE, rd=1, y=FAKE, yd=1, gate=None, axis=0, w_pre=FAKE, w_post=FAKE, wd=1,
-            off=0.0, alpha=1.0, beta=1.0, eps=1e-6, T=4, H=64, r_out=FAKE, h=FAKE, hd=1,
+B, C, D, F = (FAKE + 0x1000 * i for i in range(1, 5))  # further arrays
+NORM = dict(res=FAKE, rd=1, y=B, yd=1, gate=None, axis=0, w_pre=FAKE, w_post=FAKE, wd=1,
+            off=0.0, alpha=1.0, beta=1.0, eps=1e-6, T=4, H=64, r_out=C, h=D, hd=1,
             stream=None)
 NORM_SHARED = [
     (-1, dict(T=0)), (-1, dict(H=0)), (-2, dict(H=68)), (-2, dict(H=16392)),
@@ -59,14 +60,15 @@ NORM_SHARED = [
     (-1, dict(y=None, r_out=None, w_post=None, w_pre=None, h=None)),
     (-1, dict(y=None, r_out=None, w_post=None, gate=FAKE, axis=1)), (-1, dict(w_pre=None)),
     (-1, dict(res=FAKE + 4)), (-1, dict(r_out=FAKE + 8)), (-1, dict(h=FAKE + 8)),
+    (-1, dict(h=C)), (-1, dict(h=FAKE)), (-1, dict(h=B, yd=0)), (-1, dict(r_out=B)),
     (-1, dict(gate=FAKE + 2, axis=1))])
 def test_block_norm_refuses(lib, status, changes):
     _refuse(lib, status, lib.block_norm_forward, NORM, changes)
 
 
-NORM_BWD = dict(dh=FAKE, hd=1, d_r=FAKE, r=FAKE, rd=1, y=FAKE, yd=1, gate=None, axis=0, w_pre=FAKE,
-                w_post=FAKE, wd=1, off=0.0, alpha=1.0, beta=1.0, eps=1e-6, T=4, H=64, dres=FAKE,
-                dy=FAKE, dgate=None, dw_pre=FAKE, dw_post=FAKE, ws=FAKE, wsb=1 << 30, stream=None)
+NORM_BWD = dict(dh=FAKE, hd=1, d_r=B, r=C, rd=1, y=D, yd=1, gate=None, axis=0, w_pre=FAKE,
+                w_post=FAKE, wd=1, off=0.0, alpha=1.0, beta=1.0, eps=1e-6, T=4, H=64, dres=F,
+                dy=F + 0x1000, dgate=None, dw_pre=FAKE, dw_post=FAKE, ws=FAKE, wsb=1 << 30, stream=None)
 
 
 @pytest.mark.parametrize("status,changes", [
@@ -76,6 +78,8 @@ NORM_BWD = dict(dh=FAKE, hd=1, d_r=FAKE, r=FAKE, rd=1, y=FAKE, yd=1, gate=None, 
     (-1, dict(gate=FAKE, axis=1)), (-1, dict(dh=None, d_r=None, w_pre=None, dw_pre=None)),
     (-1, dict(w_post=None)), (-1, dict(dh=FAKE + 8)), (-1, dict(d_r=FAKE + 8)),
     (-1, dict(dres=FAKE + 4)), (-1, dict(dy=FAKE + 4)), (-1, dict(dw_pre=FAKE + 2)),
+    (-1, dict(dres=D)), (-1, dict(dres=FAKE)), (-1, dict(dres=C)), (-1, dict(dres=F + 0x1000)),
+    (-1, dict(dy=C)), (-1, dict(dy=B)), (-1, dict(dy=FAKE, yd=0)),
     (-1, dict(dw_post=FAKE + 2)), (-6, dict(ws=None)), (-6, dict(wsb=0)), (-1, dict(ws=FAKE + 16))])
 def test_block_norm_backward_refuses(lib, status, changes):
     _refuse(lib, status, lib.block_norm_backward, NORM_BWD, changes)
@@ -91,7 +95,7 @@ def test_block_norm_backward_workspace_size(lib):
 
 
 def _tensor(**kw):
-    d = dict(grad=FAKE, m=FAKE, m_out=FAKE, w=FAKE, w_out=FAKE, w16=None, n=64, E=2, r=8,
+    d = dict(grad=FAKE, m=B, m_out=B, w=C, w_out=C, w16=None, n=64, E=2, r=8,
              rank_major=1, w_dtype=0, w16_dtype=0, scale=1.0)
     d.update(kw)
     return binding.MuonTensorStruct(*d.values())
@@ -118,6 +122,19 @@ def test_muon_step_refuses(lib, status, tensor, changes):
     _refuse(lib, status, lib.lora_muon_step, dict(MUON, t=arr), changes)
 
 
+@pytest.mark.parametrize("first,second", [
+    (dict(m_out=FAKE), {}), (dict(w_out=B), {}), (dict(w_out=FAKE), {}), (dict(m_out=C), {}),
+    (dict(w16=C, w16_dtype=1), {}), (dict(w16=B, w16_dtype=1), {}), ({}, {}),
+    ({}, dict(grad=B, m=D, m_out=D, w=F, w_out=F)), ({}, dict(m=D, m_out=D, w=F, w_out=C)),
+    ({}, dict(m=D, m_out=D, w=C, w_out=F)), (dict(w16=D, w16_dtype=1), dict(m=D, m_out=F, w=F + 4096,
+                                                                            w_out=F + 4096))])
+def test_muon_step_refuses_shared_outputs(lib, first, second):
+    """A tensor with itself, or the same array in two tensors."""
+    arr = (binding.MuonTensorStruct * 2)(_tensor(**first), _tensor(**second))
+    args = dict(MUON, t=arr, count=1 if first and not second else 2)
+    _refuse(lib, -1, lib.lora_muon_step, args, {})
+
+
 def test_muon_workspace_sizes(lib):
     arr = (binding.MuonTensorStruct * 2)(_tensor(), _tensor(r=16, n=1000, E=3))
     one = lib.lora_orthogonalize_workspace(2, 8, 64)
@@ -130,13 +147,13 @@ def test_muon_workspace_sizes(lib):
         assert lib.lora_orthogonalize_workspace(E, r, n) == 0
 
 
-ORTH = dict(u=FAKE, ud=0, E=2, r=8, n=64, rm=1, steps=5, a=3.4, b=-4.7, c=2.0, eps=1e-7, out=FAKE,
+ORTH = dict(u=FAKE, ud=0, E=2, r=8, n=64, rm=1, steps=5, a=3.4, b=-4.7, c=2.0, eps=1e-7, out=B,
             od=0, ws=FAKE, wsb=1 << 30, stream=None)
 
 
 @pytest.mark.parametrize("status,changes", [
     (-1, dict(u=None)), (-1, dict(out=None)), (-5, dict(ud=3)), (-5, dict(od=-1)),
-    (-1, dict(E=0)), (-1, dict(r=17)), (-1, dict(n=0)), (-1, dict(rm=2)), (-1, dict(steps=0)),
+    (-1, dict(out=FAKE, od=1)), (-1, dict(E=0)), (-1, dict(r=17)), (-1, dict(n=0)), (-1, dict(rm=2)), (-1, dict(steps=0)),
     (-1, dict(c=INF)), (-1, dict(u=FAKE + 2)), (-1, dict(od=1, out=FAKE + 1)),
     (-6, dict(wsb=0)), (-6, dict(ws=None)), (-7, dict(n=1 << 41))])
 def test_orthogonalize_refuses(lib, status, changes):
