@@ -183,15 +183,17 @@ def _torch():
     return torch
 
 
+_dtype_codes: dict = {}
+
+
 def _dtype_code(dt) -> int:
-    torch = _torch()
-    if dt == torch.float32:
-        return F32
-    if dt == torch.bfloat16:
-        return BF16
-    if dt == torch.float16:
-        return F16
-    raise TypeError(f"unsupported dtype {dt}")
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+    code = _dtype_codes.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    return code
 
 
 def _ptr(t) -> Optional[int]:
@@ -547,7 +549,9 @@ def _need(t, what: str, dev, shape=None, dtype=None):
         raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    return _ptr(t)
+    if dev.type != "cuda" or not t.is_contiguous():
+        return _ptr(t)  # raises
+    return t.data_ptr()
 
 
 def _call(dev, fn, *args) -> None:
@@ -561,6 +565,21 @@ def _call(dev, fn, *args) -> None:
             status = fn(*args, _raw_stream(dev.index))
     if status != 0:
         _check(status)
+
+
+def _workspace(given, need: int, dev):
+    """The caller's workspace, or a new one of ``need`` bytes (None for 0)."""
+    if given is not None or need == 0:
+        return given
+    torch = _torch()
+    return torch.empty(need, dtype=torch.uint8, device=dev)
+
+
+def _span(workspace, dev):
+    """Pointer and bytes of a workspace that may be None."""
+    if workspace is None:
+        return None, 0
+    return _need(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
 
 
 def _raw_stream(index: int) -> int:
@@ -678,16 +697,14 @@ def block_norm_backward(dh, d_r_out, r, y=None, w_pre=None, w_post=None, gate=No
         out["dw_pre"] = torch.empty(H, **f32)
     if w_post is not None:
         out["dw_post"] = torch.empty(H, **f32)
-    if workspace is None:
-        workspace = torch.empty(max(load().block_norm_backward_workspace(T, H), 1),
-                                dtype=torch.uint8, device=dev)
+    ws = _workspace(workspace, load().block_norm_backward_workspace(T, H), dev)
     ptr = lambda k: out[k].data_ptr() if k in out else None  # noqa: E731
     _call(dev, load().block_norm_backward,
           None if dh is None else _need(dh, "dh", dev, r.shape),
           F32 if dh is None else _dtype_code(dh.dtype),
           None if d_r_out is None else _need(d_r_out, "d_r_out", dev, r.shape, r.dtype),
           _ptr(r), _dtype_code(r.dtype), *args, ptr("dresidual"), ptr("dy"), ptr("dgate"),
-          ptr("dw_pre"), ptr("dw_post"), _need(workspace, "workspace", dev), workspace.numel())
+          ptr("dw_pre"), ptr("dw_post"), *_span(ws, dev))
     return out
 
 
@@ -703,12 +720,10 @@ def lora_orthogonalize(u, rank_major: bool = True, steps: int = 5, coeffs=NS_COE
     if out is None:
         out = torch.empty(u.shape, dtype=out_dtype or u.dtype, device=dev)
     lib = load()
-    if workspace is None:
-        workspace = torch.empty(max(lib.lora_orthogonalize_workspace(E, r, n), 1),
-                                dtype=torch.uint8, device=dev)
+    ws = _workspace(workspace, lib.lora_orthogonalize_workspace(E, r, n), dev)
     _call(dev, lib.lora_orthogonalize, _ptr(u), _dtype_code(u.dtype), E, r, n,
           int(bool(rank_major)), steps, *coeffs, eps, _need(out, "out", dev, u.shape),
-          _dtype_code(out.dtype), _need(workspace, "workspace", dev), workspace.numel())
+          _dtype_code(out.dtype), *_span(ws, dev))
     return out
 
 
@@ -748,8 +763,6 @@ def lora_muon_step(tensors, lr: float, momentum: float = 0.95, nesterov: bool = 
         s.rank_major = int(rank_major)
         s.scale = t.get("scale", 1.0)
     lib = load()
-    if workspace is None:
-        workspace = torch.empty(max(lib.lora_muon_step_workspace(arr, len(arr)), 1),
-                                dtype=torch.uint8, device=dev)
+    ws = _workspace(workspace, lib.lora_muon_step_workspace(arr, len(arr)), dev)
     _call(dev, lib.lora_muon_step, arr, len(arr), lr, momentum, int(bool(nesterov)), weight_decay,
-          steps, *coeffs, eps, _need(workspace, "workspace", dev), workspace.numel())
+          steps, *coeffs, eps, *_span(ws, dev))

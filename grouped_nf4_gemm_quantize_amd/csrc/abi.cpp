@@ -1458,9 +1458,11 @@ static size_t muon_gram_bytes(int E, int r, int64_t n) {
 // Places the tensors' workgroups and Gram parts, then launches.
 static int muon_run(MuonArgs& a, void* workspace, size_t ws_bytes, void* stream) {
   size_t need = 0;
+  bool small = true;
   a.blocks = 0;
   for (int i = 0; i < a.count; ++i) {
     MuonTensor& t = a.t[i];
+    small = small && muon_small(t.r, t.n);
     t.chunk_cols = muon_chunk_cols(t.E, t.n, t.r);
     t.chunks = (int)muon_chunks(t.E, t.n, t.r);
     // A factors: rows of four; B factors: a group of whole rows
@@ -1472,7 +1474,7 @@ static int muon_run(MuonArgs& a, void* workspace, size_t ws_bytes, void* stream)
     a.blocks += t.E * t.chunks;
     need += muon_gram_bytes(t.E, t.r, t.n);
   }
-  if (workspace == nullptr || ws_bytes < need)
+  if (!small && (workspace == nullptr || ws_bytes < need))
     return fail(NF4MOE_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                 workspace ? ws_bytes : (size_t)0);
   if (!aligned(workspace, 256)) return fail(NF4MOE_EINVAL, "workspace must be 256-byte aligned");
@@ -1487,11 +1489,13 @@ static int muon_run(MuonArgs& a, void* workspace, size_t ws_bytes, void* stream)
 size_t lora_muon_step_workspace(const nf4moe_muon_tensor* tensors, int count) {
   if (tensors == nullptr || count < 1 || count > NF4MOE_MAX_MUON_TENSORS) return 0;
   size_t need = 0;
+  bool small = true;
   for (int i = 0; i < count; ++i) {
     if (muon_shape_check(tensors[i].E, tensors[i].r, tensors[i].n) != NF4MOE_OK) return 0;
+    small = small && muon_small(tensors[i].r, tensors[i].n);
     need += muon_gram_bytes(tensors[i].E, tensors[i].r, tensors[i].n);
   }
-  return need;
+  return small ? 0 : need;
 }
 
 int lora_muon_step(const nf4moe_muon_tensor* tensors, int count, double lr, double mu,
@@ -1573,7 +1577,7 @@ int lora_muon_step(const nf4moe_muon_tensor* tensors, int count, double lr, doub
 }
 
 size_t lora_orthogonalize_workspace(int E, int r, int64_t n) {
-  if (muon_shape_check(E, r, n) != NF4MOE_OK) return 0;
+  if (muon_shape_check(E, r, n) != NF4MOE_OK || muon_small(r, n)) return 0;
   return muon_gram_bytes(E, r, n);
 }
 

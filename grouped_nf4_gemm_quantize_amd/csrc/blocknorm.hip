@@ -11,9 +11,13 @@
 // them.  r is rounded to its type before it is normalised, so h follows from what
 // is stored.
 //
+// Measured at 4096 x 2048, bf16, both norms and a token gate: 15.4 us = 4.4 TB/s.  With
+// branches between the reads (types and bounds decided by each) it took 31 us.
+//
 // The backward's sums over T stay in registers over a workgroup's rows, are added over
 // its waves in LDS and go to one partial row a workgroup; a second kernel adds
-// the partial rows.
+// the partial rows.  The same case: 29 us = 3.5 TB/s of the 12 bytes an element (26 us
+// and 4 us; the partial sums add 8 MB to 101).
 
 #include "common.h"
 #include "launch.h"

@@ -263,7 +263,7 @@ int block_norm_groups(int64_t T, int H);
 
 // ---- adapter update (muon.hip) ----------------------------------------------
 constexpr int kMuonMaxTensors = 8;
-constexpr int64_t kMuonMaxBlocks = 1 << 20;  // workgroups of one tensor
+constexpr int64_t kMuonMaxBlocks = 1 << 18;  // workgroups of one tensor
 struct MuonTensor {
   const void* g;  // gradient, or u itself (m null)
   const float* m;
@@ -292,6 +292,8 @@ struct MuonArgs {
   double lr, weight_decay, a, b, c, eps;
 };
 int muon_chunk_cols(int E, int64_t n, int r);
+// Whether one workgroup takes a factor in any case (no Gram parts in the workspace).
+inline bool muon_small(int r, int64_t n) { return r * n <= 16384; }
 hipError_t launch_muon(MuonArgs& a, int num_cus, hipStream_t s);
 
 }  // namespace nf4moe

@@ -22,11 +22,17 @@
 //    the result registers of a symmetric matrix (row 4 j + q, column i) are its operand
 //    registers (row i, column 4 j + q): no product needs an exchange between lanes.
 //
-// Bound by memory: 16 to 22 bytes an element.  Where a call has factors enough to
-// fill the card and each fits LDS, one workgroup takes a whole factor: one launch,
-// every array read once.  Otherwise two launches over (factor, chunk of the long axis):
-// the first updates m and leaves each chunk's part of u u^T in the workspace, the second
-// adds the parts in chunk order, does the algebra and applies P to its chunk.
+// Bound by memory: 16 to 22 bytes an element.  One workgroup takes a whole factor where
+// factors are small, or enough to fill the card and each fits LDS: one launch, every array
+// read once, u kept in LDS (A factors with rows 16 bytes longer, so that the 16 ranks
+// of a column lie in different banks).  Otherwise two launches over (factor, chunk of
+// the long axis): the first updates m and leaves each chunk's part of u u^T in the
+// workspace, the second adds the parts in chunk order, does the algebra and applies P
+// to its chunk.  Measured: four fp32 factors of each of 64 experts (H 2048, I 1024,
+// r 8; 81 MB) 24.5 us = 3.3 TB/s, bf16 factors of 128 experts (H 2048, I 768, r 16; 210 MB)
+// 79 us = 2.7 TB/s: a factor's fp64 products (8 k cycles each for u u^T and P u at 16 x
+// 2048) and the algebra (0.5 us a step) are not covered by another factor's reads.
+// 8 factors of 8 x 1000 take 11 us.
 
 #include "common.h"
 #include "launch.h"
@@ -43,7 +49,6 @@ constexpr int kFactorThreads = 1024;  // of the one
 constexpr int kFactorWaves = kFactorThreads / 64;
 constexpr int kFactorReads = 9;       // reads of four elements a thread: 36864 elements
 constexpr int kFactorFloats = 33792;  // LDS copy of u, with its padding
-constexpr int kSmallFactor = 16384;   // elements of a factor that one workgroup takes in any case
 
 __device__ __forceinline__ f64x4 mfma64(double a, double b, f64x4 c) {
   return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
@@ -606,9 +611,11 @@ namespace {
 template <bool kVec>
 hipError_t muon_go(const MuonArgs& a, int lds, hipStream_t s) {
   if (lds > 0) {
-    const void* k = reinterpret_cast<const void*>(muon_factor_kernel<kVec>);
-    hipError_t err = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (err != hipSuccess) return err;
+    if (lds > 32768) {  // beyond 64 KiB with the kernel's own
+      const void* k = reinterpret_cast<const void*>(muon_factor_kernel<kVec>);
+      hipError_t err = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      if (err != hipSuccess) return err;
+    }
     hipLaunchKernelGGL(muon_factor_kernel<kVec>, dim3(a.blocks), dim3(kFactorThreads), lds, s, a);
     return hipGetLastError();
   }
@@ -625,7 +632,8 @@ hipError_t launch_muon(MuonArgs& a, int num_cus, hipStream_t s) {
   // One workgroup a factor where all fit, and either half the compute units or more get one, or
   // factors are small: 64 factors of 8 x 2048 take 20-24 us in two launches, 128 of them 19-20
   // in one; 64 of 16 x 2048 take 22-25 us in two, 128 of them 31 in one.
-  int64_t factors = 0, floats = 0, most = 0;
+  int64_t factors = 0, floats = 0;
+  bool small = true;
   bool vec = true;
   for (int i = 0; i < a.count; ++i) {
     MuonTensor& t = a.t[i];
@@ -634,11 +642,11 @@ hipError_t launch_muon(MuonArgs& a, int num_cus, hipStream_t s) {
     const int64_t need = t.rank_major ? (int64_t)t.r * t.lds_row : t.r * t.n + 16;
     floats = need > floats ? need : floats;
     factors += t.E;
-    most = t.r * t.n > most ? t.r * t.n : most;
+    small = small && muon_small(t.r, t.n);
     vec = vec && t.vec;
   }
   int lds = 0;
-  if (floats <= kFactorFloats && (2 * factors >= num_cus || most <= kSmallFactor)) {
+  if (floats <= kFactorFloats && (2 * factors >= num_cus || small)) {
     lds = (int)floats * 4;
     a.blocks = 0;
     for (int i = 0; i < a.count; ++i) {

@@ -622,11 +622,12 @@ int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const 
  *   ns_steps        1 .. 16; lr, mu, weight_decay, scale, a, b, c finite,
  *                   ns_eps >= 0 (EINVAL);
  *   workspace       lora_muon_step_workspace(tensors, count) bytes, 256-byte
- *                   aligned; 0 for invalid arguments.  Two calls must not share
- *                   it while both run.
+ *                   aligned (NULL for 0: small factors need none, and the query gives
+ *                   0 for invalid arguments too).  Two calls must not share it
+ *                   while both run.
  * lr and the other scalars are taken at the call: a captured call keeps them.
  * Pointers are aligned to their element.  r * n at most 2^29 and, a workgroup taking
- * 8192 elements of a factor, at most 2^20 workgroups a tensor (EOVERFLOW). */
+ * 8192 elements of a factor, at most 2^18 workgroups a tensor (EOVERFLOW). */
 #define NF4MOE_MAX_MUON_TENSORS 8
 typedef struct {
   const float* grad;

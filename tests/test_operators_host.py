@@ -95,7 +95,7 @@ def test_block_norm_backward_workspace_size(lib):
 
 
 def _tensor(**kw):
-    d = dict(grad=FAKE, m=B, m_out=B, w=C, w_out=C, w16=None, n=64, E=2, r=8,
+    d = dict(grad=FAKE, m=B, m_out=B, w=C, w_out=C, w16=None, n=4096, E=2, r=8,
              rank_major=1, w_dtype=0, w16_dtype=0, scale=1.0)
     d.update(kw)
     return binding.MuonTensorStruct(*d.values())
@@ -116,7 +116,7 @@ MUON = dict(t=None, count=1, lr=0.1, mu=0.9, nesterov=1, wd=0.0, steps=5, a=3.4,
     (-1, dict(r=17), {}), (-1, dict(rank_major=2), {}), (-5, dict(w_dtype=4), {}),
     (-5, dict(w16=FAKE, w16_dtype=0), {}), (-1, dict(scale=NAN), {}), (-1, dict(grad=FAKE + 2), {}),
     (-1, dict(w=FAKE + 2), {}), (-1, dict(w16=FAKE + 1, w16_dtype=1), {}),
-    (-7, dict(n=1 << 40), {}), (-7, dict(E=1 << 30), {})])
+    (-7, dict(n=1 << 40), {}), (-7, dict(E=1 << 30), {}), (-7, dict(E=(1 << 18) + 1, n=64), {})])
 def test_muon_step_refuses(lib, status, tensor, changes):
     arr = (binding.MuonTensorStruct * 1)(_tensor(**tensor))
     _refuse(lib, status, lib.lora_muon_step, dict(MUON, t=arr), changes)
@@ -136,18 +136,21 @@ def test_muon_step_refuses_shared_outputs(lib, first, second):
 
 
 def test_muon_workspace_sizes(lib):
-    arr = (binding.MuonTensorStruct * 2)(_tensor(), _tensor(r=16, n=1000, E=3))
-    one = lib.lora_orthogonalize_workspace(2, 8, 64)
+    arr = (binding.MuonTensorStruct * 2)(_tensor(), _tensor(r=16, n=2000, E=3))
+    one = lib.lora_orthogonalize_workspace(2, 8, 4096)
     assert one >= 2 * 64 * 8
     assert lib.lora_muon_step_workspace(arr, 2) == one + lib.lora_orthogonalize_workspace(3, 16,
-                                                                                        1000)
+                                                                                        2000)
+    # small factors need none
+    assert lib.lora_orthogonalize_workspace(2, 8, 64) == 0
+    assert lib.lora_muon_step_workspace((binding.MuonTensorStruct * 1)(_tensor(n=64)), 1) == 0
     assert lib.lora_muon_step_workspace(arr, 0) == 0 and lib.lora_muon_step_workspace(None, 1) == 0
     assert lib.lora_muon_step_workspace((binding.MuonTensorStruct * 1)(_tensor(r=0)), 1) == 0
     for E, r, n in ((0, 8, 64), (2, 17, 64), (2, 8, 0)):
         assert lib.lora_orthogonalize_workspace(E, r, n) == 0
 
 
-ORTH = dict(u=FAKE, ud=0, E=2, r=8, n=64, rm=1, steps=5, a=3.4, b=-4.7, c=2.0, eps=1e-7, out=B,
+ORTH = dict(u=FAKE, ud=0, E=2, r=8, n=4096, rm=1, steps=5, a=3.4, b=-4.7, c=2.0, eps=1e-7, out=B,
             od=0, ws=FAKE, wsb=1 << 30, stream=None)
 
 
