@@ -549,7 +549,7 @@ def _need(t, what: str, dev, shape=None, dtype=None):
         raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if dev.type != "cuda" or not t.is_contiguous():
+    if not t.is_cuda or not t.is_contiguous():
         return _ptr(t)  # raises
     return t.data_ptr()
 
@@ -615,7 +615,7 @@ def nbit_matvec(x, codes, scales, quant_type: str = "nf4", group: Optional[int] 
     groups = (N, K // group)
     mx = quant_type == "mxfp4"
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype or x.dtype, device=dev)
+        out = torch.empty(T, N, dtype=out_dtype or x.dtype, device=dev)
     _call(dev, load().nbit_matvec, MATVEC_TYPES[quant_type], _ptr(x), _dtype_code(x.dtype), T,
           _need(codes, "codes", dev, (N, K // 2), torch.uint8),
           _need(scales, "scales", dev, groups, torch.uint8 if mx else None),
@@ -665,7 +665,7 @@ def block_norm(residual, y=None, w_pre=None, w_post=None, gate=None, gate_axis: 
     if y is not None and r_out is None:
         r_out = torch.empty_like(residual)
     if w_pre is not None and h is None:
-        h = torch.empty(residual.shape, dtype=h_dtype or residual.dtype, device=dev)
+        h = torch.empty_like(residual, dtype=h_dtype or residual.dtype)
     _call(dev, load().block_norm_forward, _ptr(residual), _dtype_code(residual.dtype), *args,
           None if r_out is None else _need(r_out, "r_out", dev, residual.shape, residual.dtype),
           None if h is None else _need(h, "h", dev, residual.shape),
@@ -687,16 +687,15 @@ def block_norm_backward(dh, d_r_out, r, y=None, w_pre=None, w_post=None, gate=No
     dev = r.device
     args = _norm_args(r, y, gate, gate_axis, w_pre, w_post, w_offset, alpha, beta, eps)
     T, H = r.shape
-    f32 = dict(dtype=torch.float32, device=dev)
     out = dict(dresidual=torch.empty_like(r))
     if y is not None:
         out["dy"] = torch.empty_like(y)
     if gate is not None:
-        out["dgate"] = torch.empty(gate.shape, **f32)
+        out["dgate"] = torch.empty_like(gate)
     if w_pre is not None:
-        out["dw_pre"] = torch.empty(H, **f32)
+        out["dw_pre"] = torch.empty_like(w_pre, dtype=torch.float32)
     if w_post is not None:
-        out["dw_post"] = torch.empty(H, **f32)
+        out["dw_post"] = torch.empty_like(w_post, dtype=torch.float32)
     ws = _workspace(workspace, load().block_norm_backward_workspace(T, H), dev)
     ptr = lambda k: out[k].data_ptr() if k in out else None  # noqa: E731
     _call(dev, load().block_norm_backward,
