@@ -510,11 +510,12 @@ void norm_launch(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
 
 }  // namespace
 
-// One workgroup of sixteen waves a compute unit, or two of up to eight.
+// One workgroup a compute unit: with two of six waves for 1531 x 2888 the partial rows cost more
+// than the waves gained (31 us, one 26.5).
 int block_norm_groups(int64_t T, int H) {
   const int waves = norm_row_waves(H);
   const int64_t rows = waves <= 4 ? kNormBwdWaves / waves : 1;
-  const int64_t rounds = (T + rows - 1) / rows, most = waves > 4 && waves <= 8 ? 512 : 256;
+  const int64_t rounds = (T + rows - 1) / rows, most = 256;
   return (int)(rounds < most ? rounds : most);
 }
 

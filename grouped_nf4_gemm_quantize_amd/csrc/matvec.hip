@@ -216,7 +216,14 @@ __device__ __forceinline__ void mv_fill(u32x4* lut, uint32_t* stage, int tid) {
   const float nf4[16] = NF4MOE_LEVELS_INIT;
   const float e2m1[16] = NF4MOE_E2M1_VALUES_INIT;
   if (tid < 16) {
-    const float v = mv_split(kFmt) ? 256.0f * nf4[tid] : mv_int(kFmt) ? (float)tid : e2m1[tid];
+    // selected from literals: a read of the levels would wait for the codes' reads
+    // issued before it
+    float v = (float)tid;
+    if constexpr (!mv_int(kFmt)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (tid == i) v = mv_split(kFmt) ? 256.0f * nf4[i] : e2m1[i];
+    }
     const _Float16 hi = (_Float16)v, lo = (_Float16)(v - (float)hi);
     stage[tid] = pack_half2(hi, lo);
   }
