@@ -116,6 +116,26 @@ def test_quantised_stack_slice_and_untouched_neighbours(gpu_lib):
     assert torch.all(buf[0] == 3.0) and torch.all(buf[6] == 3.0)
 
 
+@pytest.mark.parametrize("qt,group,K", [("int4", 128, 128), ("int4", 32, 96), ("mxfp4", 32, 32),
+                                        ("mxfp4", 32, 160), ("nf4", 64, 64)])
+def test_scales_zeros_bias_and_out_at_any_element(gpu_lib, qt, group, K):
+    """Scales, zeros, bias and y begin one row into larger arrays: only their own
+    element's alignment."""
+    T, N = 3, 21
+    sd = "f16" if qt == "int4" else "f32"
+    x, codes, st, s, z = make(qt, group, T, N + 1, K, sd=sd)
+    b = torch.randn(N + 1, generator=torch.Generator().manual_seed(4))
+    out = torch.zeros((T + 1) * N + 1, dtype=torch.bfloat16, device=DEV)
+    y = out[1:1 + T * N].view(T, N)
+    gpu_lib.nbit_matvec(x.to(DEV), torch.as_tensor(codes[1:]).to(DEV), st.to(DEV)[1:], quant_type=qt,
+                        group=group, zeros=None if z is None else torch.as_tensor(z).to(DEV)[1:],
+                        bias=b.to(DEV)[1:], out=y)
+    ref, mag = oracle.matvec(x.float().numpy(), codes[1:], s[1:], qt, group,
+                             None if z is None else z[1:], b.numpy()[1:])
+    check(y, ref, mag, K, "bf16")
+    assert out[0] == 0 and torch.count_nonzero(out[1 + T * N:]) == 0
+
+
 def test_zero_activations_and_zero_scales(gpu_lib):
     x, codes, st, s, z = make("nf4", 64, 3, 33, 128)
     x[1] = 0
@@ -142,8 +162,15 @@ def test_non_finite_inputs_stay_in_their_row_and_column(gpu_lib, qt, group):
     assert torch.equal(y[:, keep], clean[:, keep])
 
 
-def test_same_result_every_call_and_for_each_row_alone(gpu_lib):
-    """Rows do not depend on the batch they come in, within 16 rows."""
+def test_small_activations_keep_their_bits(gpu_lib):
+    """fp16 subnormals go through the matrix unit as they are."""
+    x, codes, st, s, z = make("fp4", 64, 2, 40, 128, xt="f16")
+    x = (x.float() * 2.0 ** -20).half()
+    ref, mag = oracle.matvec(x.float().numpy(), codes, s, "fp4", 64)
+    check(run(gpu_lib, x, codes, st, z, "fp4", 64, out_dtype=torch.float32), ref, mag, 128, "f32")
+
+
+def test_same_result_every_call(gpu_lib):
     x, codes, st, s, z = make("nf4", 64, 16, 333, 2048)
     y = run(gpu_lib, x, codes, st, z, "nf4", 64, out_dtype=torch.float32)
     for _ in range(2):

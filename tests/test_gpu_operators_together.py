@@ -180,3 +180,30 @@ def test_decode_step(gpu_lib):
     assert np.all(np.abs(host(h2) - ref) <= 40 * U * np.abs(ref) + half_spacing(ref, "bf16"))
     ref, mag = oracle.matvec(host(h2), wh[0].cpu().numpy(), sh[0].cpu().numpy(), "nf4", 64)
     assert np.all(np.abs(host(logits) - ref) <= (H / 32 + 64) * 2 * U * mag)
+
+
+def test_two_streams_at_once(gpu_lib):
+    """The same calls running on two streams do not disturb each other."""
+    g = torch.Generator(DEV).manual_seed(5)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    wo, so = gpu_lib.quantize(n(1, 4096, 2048) * 0.02)
+    res, y, w = n(700, 1024), n(700, 1024), n(1024)
+    dh, u, x = n(700, 1024), n(40, 16, 1500), n(5, 2048).half()
+
+    def work():
+        r, h = gpu_lib.block_norm(res, y=y, w_pre=w, w_post=w)
+        d = gpu_lib.block_norm_backward(dh, None, r, y=y, w_pre=w, w_post=w)
+        return [r, h, gpu_lib.nbit_matvec(x, wo[0], so[0]), gpu_lib.lora_orthogonalize(u),
+                *(d[k] for k in sorted(d))]
+
+    want = work()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(work())
+    torch.cuda.synchronize()
+    for out in got:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
