@@ -1328,9 +1328,6 @@ int block_norm_forward(const void* residual, int res_dtype, const void* y, int y
     return fail(NF4MOE_EINVAL, "h may be y of the same type, and no other of the matrices");
   if (r_out != nullptr && r_out == y)
     return fail(NF4MOE_EINVAL, "r_out must not be y");
-  int cus = 0;
-  st = cu_count(&cus);
-  if (st != NF4MOE_OK) return st;
   BlockNormArgs a{};
   a.residual = residual;
   a.y = y;
@@ -1350,7 +1347,7 @@ int block_norm_forward(const void* residual, int res_dtype, const void* y, int y
   a.alpha = alpha;
   a.beta = beta;
   a.eps = eps;
-  hipError_t err = launch_block_norm(a, cus, (hipStream_t)stream);
+  hipError_t err = launch_block_norm(a, (hipStream_t)stream);
   if (err != hipSuccess) return hip_fail(err, "block norm launch");
   return ok();
 }

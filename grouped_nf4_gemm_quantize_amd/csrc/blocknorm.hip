@@ -29,6 +29,7 @@ namespace {
 constexpr int kNormWaves = 8;      // waves of a workgroup of several rows, forward
 constexpr int kNormBwdWaves = 16;  // and backward: fewer partial rows
 constexpr int kNormMaxWaves = 16;  // waves of a workgroup of one row
+constexpr int kNormPartials = 256; // partial rows of the weight gradients, at most
 
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 
@@ -173,7 +174,8 @@ __device__ __forceinline__ float rstd_of(float sum, int H, float eps) {
 
 // kRes, kY: element sizes of the residual and of y (2 where there is none).
 template <int kRes, int kY, int kVec, int kRowWaves>
-__global__ __launch_bounds__(64 * norm_waves<kRowWaves>(kNormWaves), kVec == 1 ? 8 : 4) void block_norm_kernel(BlockNormArgs a) {
+__global__ __launch_bounds__(64 * norm_waves<kRowWaves>(kNormWaves), kVec == 1 ? 8 : 4) void
+block_norm_kernel(BlockNormArgs a) {
   const NormShape<kRowWaves, kNormWaves> at;
   __shared__ float red[2][1][kNormMaxWaves];
   constexpr int kRows = at.kRows;
@@ -363,14 +365,15 @@ block_norm_bwd_kernel(BlockNormArgs a) {
         s[5] += r[u][i] * q;
       }
     row_sum<6>(s, red[buf], at);
-    // without w_pre (or a row) r and dh are zero here, and so is all they give
+    // without w_pre (or a row) r and dh are zero here, and so is all they give.  The third
+    // power of a small row's rstd can pass fp32's range, its products with the sums do not.
     const float rstd_r = a.w_pre && live ? rstd_of(s[0], a.H, a.eps) : 0.f;
-    const float k_r = rstd_r * rstd_r * rstd_r * (s[1] * inv_h);
+    const float k_r = rstd_r * (rstd_r * (rstd_r * (s[1] * inv_h)));
     const float rstd_y = !a.w_post ? 1.f : live ? rstd_of(s[2], a.H, a.eps) : 0.f;
     const float dr_q = s[3] + rstd_r * s[4] - k_r * s[5];
     if (a.gate_axis == 1 && live && at.part == 0 && at.lane == 0)
       a.dgate[t] = a.alpha * rstd_y * dr_q;
-    const float k_y = a.w_post ? rstd_y * rstd_y * rstd_y * (gt * dr_q * inv_h) : 0.f;
+    const float k_y = a.w_post ? rstd_y * (rstd_y * (rstd_y * (gt * dr_q * inv_h))) : 0.f;
     const Rsrc r_out = span_of(a.r_out, row * kRes, n * kRes);
     const Rsrc r_dy = span_of(a.h, row * kY, a.y ? n * kY : 0);
 #pragma unroll
@@ -511,16 +514,16 @@ void norm_launch(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
 }  // namespace
 
 // One workgroup a compute unit: with two of six waves for 1531 x 2888 the partial rows cost more
-// than the waves gained (31 us, one 26.5).
+// than the waves gained (31 us, one 26.5).  Not the device's count: the workspace's size
+// follows from it, and is asked for without a device.
 int block_norm_groups(int64_t T, int H) {
   const int waves = norm_row_waves(H);
   const int64_t rows = waves <= 4 ? kNormBwdWaves / waves : 1;
-  const int64_t rounds = (T + rows - 1) / rows, most = 256;
-  return (int)(rounds < most ? rounds : most);
+  const int64_t rounds = (T + rows - 1) / rows;
+  return (int)(rounds < kNormPartials ? rounds : kNormPartials);
 }
 
-hipError_t launch_block_norm(const BlockNormArgs& a, int num_cus, hipStream_t s) {
-  (void)num_cus;
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s) {
   norm_launch(a, 0, s);
   return hipGetLastError();
 }

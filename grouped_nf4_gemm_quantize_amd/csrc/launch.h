@@ -256,7 +256,7 @@ struct BlockNormArgs {
   int res_dtype, y_dtype, h_dtype, w_dtype, gate_axis;
   float w_offset, alpha, beta, eps;
 };
-hipError_t launch_block_norm(const BlockNormArgs& a, int num_cus, hipStream_t s);
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s);
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, hipStream_t s);
 // Rows of partial sums that the backward of T rows writes per output.
 int block_norm_groups(int64_t T, int H);

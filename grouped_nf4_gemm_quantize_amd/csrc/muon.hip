@@ -515,7 +515,7 @@ __device__ __forceinline__ void whole_factor(const MuonArgs& a, const MuonTensor
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const Place pl = apply_place<kRank>(h, blk, k, lane);
-      f32x4 y;
+      f32x4 y;  // O in fp32: half a unit in 2^24 of a step that w absorbs scaled by lr
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = (float)(kRank ? o[e][k] : o[k][e]);
       if (wide) {

@@ -590,7 +590,8 @@ int block_norm_forward(const void* residual, int res_dtype, const void* y, int y
  *               (EWORKSPACE, EINVAL).
  * Sums over T are taken per workgroup and then over the workgroups in a fixed
  * order: results are the same from call to call.  Two calls must not share a workspace
- * while both run.  Other arguments and errors as in the forward.  block_norm_backward_workspace returns 0 for invalid sizes. */
+ * while both run.  Other arguments and errors as in the forward.
+ * block_norm_backward_workspace returns 0 for invalid sizes. */
 size_t block_norm_backward_workspace(int64_t T, int64_t H);
 int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const void* r,
                         int res_dtype, const void* y, int y_dtype, const float* gate,
@@ -608,7 +609,7 @@ int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const 
  *   X <- a X + b (X X^T) X + c (X X^T)^2 X;            O = X
  *   w' = w * (1 - lr * weight_decay) - lr * scale * O
  * The Gram matrix, the r x r products and O are computed in 64 bits, m' and u in
- * 32, and w' is rounded once to its type.  A factor whose u is zero has O = 0; one
+ * 32; O may be rounded to 32 before w', which is rounded once to its type.  A factor whose u is zero has O = 0; one
  * with a non-finite u gets NaN, and no other factor is touched by it.
  *   grad, m, m_out  fp32 [E, r, n] (rank_major = 1: the A factors) or
  *                   [E, n, r] (rank_major = 0: the B factors); m_out may be m;

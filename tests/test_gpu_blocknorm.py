@@ -129,6 +129,16 @@ def test_zero_rows_and_eps_zero(gpu_lib):
     both(gpu_lib, make(T, H), T, H, eps=0.0)
 
 
+def test_rows_of_small_values_without_eps(gpu_lib):
+    """rstd of some 1e14: its third power is beyond fp32, the gradients are not."""
+    T, H = 9, 520
+    c = make(T, H, res="f32", y="f32", h="f32")
+    c["residual"] *= 1e-14
+    c["y"] *= 1e-14
+    _, _, g = both(gpu_lib, c, T, H, res="f32", y="f32", h="f32", alpha=1e-14, eps=0.0)
+    assert all(torch.isfinite(v).all() for v in g.values())
+
+
 def test_non_finite_rows_stay_alone(gpu_lib):
     T, H = 9, 512
     c = make(T, H)
