@@ -6,10 +6,10 @@
 // Bound by memory: every matrix is read once and written once.  The waves of a
 // row hold it in registers, eight consecutive columns a lane (sixteen beyond 8192
 // columns): few registers, so that sixteen waves and their reads are in flight on a
-// compute unit.  All of a row's reads are issued together, before any of them is converted; they go through
-// buffer bounds, so that columns and rows beyond the end need no branch between
-// them.  r is rounded to its type before it is normalised, so h follows from what
-// is stored.
+// compute unit.  All of a row's reads are issued together, before any of them is
+// converted; they go through buffer bounds, so that columns and rows beyond the end
+// need no branch between them.  r is rounded to its type before it is normalised, so
+// h follows from what is stored.
 //
 // Measured at 4096 x 2048, bf16, both norms and a token gate: 15.4 us = 4.4 TB/s.  With
 // branches between the reads (types and bounds decided by each) it took 31 us.
@@ -265,25 +265,43 @@ block_norm_kernel(BlockNormArgs a) {
   }
 }
 
-// One row's matrices as they are read.
-template <int kRes, int kY, int kDh, int kVec>
+// A lane's part of one row's matrices as they are read.
+template <int kRes, int kY, int kDh>
 struct NormRow {
-  Raw8<kRes> r[kVec], d[kVec];
-  Raw8<kY> y[kVec];
-  Raw8<kDh> h[kVec];
-  float gate;
+  Raw8<kRes> r, d;
+  Raw8<kY> y;
+  Raw8<kDh> h;
 };
 
-// A workgroup takes rows in turn with the others, the next one's reads in flight; its
-// sums over them of the column gradients go to row blockIdx.x of the partial sums
-// (dw_pre, dw_post, dgate by channel).  kDh: element size of dh (2 where there is none).
+__device__ __forceinline__ f32x4 four(const float (&v)[8], int half) {
+  return f32x4{v[4 * half], v[4 * half + 1], v[4 * half + 2], v[4 * half + 3]};
+}
+
+// A lane's weights, with the offset; without w_post z is y: weight 1.
+struct NormCols {
+  float pre[8], post[8], gate[8];
+};
+
+// A workgroup takes rows in turn with the others; its sums over them of the column
+// gradients go to row blockIdx.x of the partial sums (dw_pre, dw_post, dgate by
+// channel).  kDh: element size of dh (2 where there is none).
 // All sums of a row are taken at once: with dr = d + rstd_r dh w_pre - k_r r and
 // q = gate w_post y, sum dr q = sum d q + rstd_r sum dh w_pre q - k_r sum r q.
+//
+// Registers: sixteen waves have 128 a lane, and a spill among the next row's reads waits for
+// them.  With eight columns a lane (kVec 1, kHold) the next row's reads are in flight and the
+// weights stay in registers; in LDS with a channel gate or fp32 rows of four waves
+// (kKeep; 2048 x 5120 fp32, channel gate 87 | 62 us).  With sixteen columns, values and
+// sums alone fill the registers: the row and its weights are read again (from L2) after the
+// row's sums, and two column sums are held in LDS (275 x 8536 fp16, channel gate 85 | 33 us, 53 x
+// 13808 fp32 55 | 23).
 template <int kRes, int kY, int kDh, int kVec, int kRowWaves, bool kGate>
 __global__ __launch_bounds__(64 * norm_waves<kRowWaves>(kNormBwdWaves), kRowWaves ? 4 : 3) void
 block_norm_bwd_kernel(BlockNormArgs a) {
   const NormShape<kRowWaves, kNormBwdWaves> at;
   constexpr int kRows = at.kRows, kCols = kRowWaves > 0 ? kVec * kRowWaves * 512 : 0;
+  constexpr bool kHold = kVec == 1;
+  constexpr bool kKeep = kHold && kRowWaves != 0 && (kGate || (kRes == 4 && kRowWaves == 4));
   __shared__ float red[2][6][kNormMaxWaves];
   // partial sums of the waves that share columns
   __shared__ f32x4 all[kRows > 1 ? kRows / 2 : 1][kRows > 1 ? kCols / 4 : 1];
@@ -291,79 +309,124 @@ block_norm_bwd_kernel(BlockNormArgs a) {
   const Rsrc r_pre = span_of(a.w_pre, 0, a.w_pre ? a.H * ws : 0);
   const Rsrc r_post = span_of(a.w_post, 0, a.w_post ? a.H * ws : 0);
   const Rsrc r_gate = span_of(a.gate, 0, kGate ? a.H * 4 : 0);
-  typedef NormRow<kRes, kY, kDh, kVec> Row;
-  const auto read = [&](int64_t t, Row& o) {
+  typedef NormRow<kRes, kY, kDh> Row;
+  // a column the compiler cannot know, where it would otherwise keep what is to be read again
+  const auto col_of = [&](int u) {
+    int col = at.col(u);
+    if constexpr (!kHold) asm volatile("" : "+v"(col));
+    return col;
+  };
+  const auto read = [&](int64_t t, int u, Row& o) {
     const bool live = t < a.T;
-    const int n = live ? a.H : 0;
+    const int n = live ? a.H : 0, col = col_of(u);
     const int64_t row = live ? t * a.H : 0;
-    const Rsrc r_r = span_of(a.residual, row * kRes, a.w_pre ? n * kRes : 0);
-    const Rsrc r_dh = span_of(a.dh, row * kDh, a.dh ? n * kDh : 0);
-    const Rsrc r_d = span_of(a.d_r_out, row * kRes, a.d_r_out ? n * kRes : 0);
-    const Rsrc r_y = span_of(a.y, row * kY, a.y ? n * kY : 0);
+    fetch8<kRes>(span_of(a.residual, row * kRes, a.w_pre ? n * kRes : 0), col, o.r);
+    fetch8<kDh>(span_of(a.dh, row * kDh, a.dh ? n * kDh : 0), col, o.h);
+    fetch8<kY>(span_of(a.y, row * kY, a.y ? n * kY : 0), col, o.y);
+    fetch8<kRes>(span_of(a.d_r_out, row * kRes, a.d_r_out ? n * kRes : 0), col, o.d);
+  };
+  const auto gate_of = [&](int64_t t) { return a.gate_axis == 1 && t < a.T ? a.gate[t] : 1.f; };
+  const auto columns = [&](int u, NormCols& w) {
+    Raw8<4> p, q, g;
+    const int col = col_of(u);
+    fetch8_any(r_pre, ws, col, p);
+    fetch8_any(r_post, ws, col, q);
+    if constexpr (kGate) fetch8<4>(r_gate, col, g);
+    widen8<4>(p, a.w_dtype, w.pre);
+    widen8<4>(q, a.w_dtype, w.post);
+    if constexpr (kGate) widen8<4>(g, kF32, w.gate);
 #pragma unroll
-    for (int u = 0; u < kVec; ++u) {
-      fetch8<kRes>(r_r, at.col(u), o.r[u]);
-      fetch8<kDh>(r_dh, at.col(u), o.h[u]);
-      fetch8<kY>(r_y, at.col(u), o.y[u]);
-      fetch8<kRes>(r_d, at.col(u), o.d[u]);
+    for (int i = 0; i < 8; ++i) {
+      w.pre[i] += a.w_offset;
+      w.post[i] = a.w_post ? w.post[i] + a.w_offset : 1.f;
     }
-    o.gate = a.gate_axis == 1 && live ? a.gate[t] : 1.f;
+  };
+  float r[8], d[8], y[8], g[8];
+  const auto widen = [&](const Row& o) {
+    widen8<kRes>(o.r, a.res_dtype, r);
+    widen8<kDh>(o.h, a.h_dtype, g);
+    widen8<kY>(o.y, a.y_dtype, y);
+    widen8<kRes>(o.d, a.res_dtype, d);
   };
   const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t t = (int64_t)blockIdx.x * kRows + at.sub;
   Row next;
-  read(t, next);
-  // the columns' weights; without w_post z is y: weight 1
-  float w1[kVec][8], w0[kVec][8], gc[kGate ? kVec : 1][8];
+  float next_gate = gate_of(t);
+  NormCols w;
+  // the weights in LDS, in the lane's own places, where they do not fit the registers
+  __shared__ f32x4 kept[3][2][kKeep ? 64 * kNormMaxWaves : 1];
+  const auto kept_columns = [&]() {
+    int at = threadIdx.x;
+    asm volatile("" : "+v"(at));  // read here, not before the loop
 #pragma unroll
-  for (int u = 0; u < kVec; ++u) {
-    Raw8<4> p, q;
-    fetch8_any(r_pre, ws, at.col(u), p);
-    fetch8_any(r_post, ws, at.col(u), q);
-    widen8<4>(p, a.w_dtype, w1[u]);
-    widen8<4>(q, a.w_dtype, w0[u]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w1[u][i] += a.w_offset;
-      w0[u][i] = a.w_post ? w0[u][i] + a.w_offset : 1.f;
+    for (int e = 0; e < 8; ++e) {
+      w.pre[e] = kept[0][e >> 2][at][e & 3];
+      w.post[e] = kept[1][e >> 2][at][e & 3];
+      if constexpr (kGate) w.gate[e] = kept[2][e >> 2][at][e & 3];
     }
-    if constexpr (kGate) {
-      fetch8<4>(r_gate, at.col(u), p);
-      widen8<4>(p, kF32, gc[u]);
+  };
+  if constexpr (kHold) {
+    read(t, 0, next);
+    columns(0, w);
+  }
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      kept[0][e][threadIdx.x] = four(w.pre, e);
+      kept[1][e][threadIdx.x] = four(w.post, e);
+      if constexpr (kGate) kept[2][e][threadIdx.x] = four(w.gate, e);
     }
   }
-  float s_pre[kVec][8] = {}, s_post[kVec][8] = {}, s_gate[kGate ? kVec : 1][8] = {};
+  // sums of the column gradients; of long rows the last two in LDS, in the lane's own places
+  float s_pre[kVec][8] = {}, s_post[8] = {}, s_gate[8] = {};
+  __shared__ f32x4 mine[kGate ? 2 : 1][kVec][2][kHold ? 1 : 64 * kNormMaxWaves];
+  const auto add_mine = [&](int which, int u, const float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mine[which][u][e][threadIdx.x] += four(v, e);
+  };
+  if constexpr (!kHold) {
+    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 2 * kVec; ++k) {
+      mine[0][k >> 1][k & 1][threadIdx.x] = none;
+      if constexpr (kGate) mine[1][k >> 1][k & 1][threadIdx.x] = none;
+    }
+  }
   const float inv_h = 1.0f / (float)a.H;
   // waves whose row is beyond the last (t >= T) take part in the barriers only
   for (int buf = 0; t - at.sub < a.T; t += step, buf ^= 1) {
     const bool live = t < a.T;
     const int n = live ? a.H : 0;
     const int64_t row = live ? t * a.H : 0;
-    float r[kVec][8], d[kVec][8], y[kVec][8], g[kVec][8];
-    const float gt = a.alpha * next.gate;
-#pragma unroll
-    for (int u = 0; u < kVec; ++u) {
-      widen8<kRes>(next.r[u], a.res_dtype, r[u]);
-      widen8<kDh>(next.h[u], a.h_dtype, g[u]);
-      widen8<kY>(next.y[u], a.y_dtype, y[u]);
-      widen8<kRes>(next.d[u], a.res_dtype, d[u]);
+    const float gt = a.alpha * next_gate;
+    if constexpr (kHold) {
+      widen(next);
+      read(t + step, 0, next);
     }
-    read(t + step, next);
+    next_gate = gate_of(t + step);
     // r^2, dh w r, y^2; d q, dh w q, r q
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < kVec; ++u)
+    for (int u = 0; u < kVec; ++u) {
+      if constexpr (!kHold) {
+        __builtin_amdgcn_sched_barrier(0);  // one u's values at a time
+        read(t, u, next);
+        columns(u, w);
+        widen(next);
+      }
+      if constexpr (kKeep) kept_columns();
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float hw = g[u][i] * w1[u][i];
-        const float q = (kGate ? gc[u][i] * w0[u][i] : w0[u][i]) * y[u][i];
-        s[0] += r[u][i] * r[u][i];
-        s[1] += hw * r[u][i];
-        s[2] += y[u][i] * y[u][i];
-        s[3] += d[u][i] * q;
+        const float hw = g[i] * w.pre[i];
+        const float q = (kGate ? w.gate[i] * w.post[i] : w.post[i]) * y[i];
+        s[0] += r[i] * r[i];
+        s[1] += hw * r[i];
+        s[2] += y[i] * y[i];
+        s[3] += d[i] * q;
         s[4] += hw * q;
-        s[5] += r[u][i] * q;
+        s[5] += r[i] * q;
       }
+    }
     row_sum<6>(s, red[buf], at);
     // without w_pre (or a row) r and dh are zero here, and so is all they give.  The third
     // power of a small row's rstd can pass fp32's range, its products with the sums do not.
@@ -378,24 +441,42 @@ block_norm_bwd_kernel(BlockNormArgs a) {
     const Rsrc r_dy = span_of(a.h, row * kY, a.y ? n * kY : 0);
 #pragma unroll
     for (int u = 0; u < kVec; ++u) {
+      if constexpr (!kHold) {
+        __builtin_amdgcn_sched_barrier(0);  // one u's values at a time
+        read(t, u, next);
+        columns(u, w);
+        widen(next);
+      }
+      if constexpr (kKeep) kept_columns();
+      float post[8], gate[8];  // this row's part of the sums
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        s_pre[u][i] += g[u][i] * r[u][i] * rstd_r;
+        s_pre[u][i] += g[i] * r[i] * rstd_r;
         // d becomes dr, r dresidual
-        d[u][i] += rstd_r * g[u][i] * w1[u][i] - r[u][i] * k_r;
-        r[u][i] = a.beta * d[u][i];
+        d[i] += rstd_r * g[i] * w.pre[i] - r[i] * k_r;
+        r[i] = a.beta * d[i];
         // g becomes the gradient dz of z, then dy
-        g[u][i] = gt * d[u][i];
-        const float yn = y[u][i] * rstd_y;
+        g[i] = gt * d[i];
+        const float yn = y[i] * rstd_y;
         if constexpr (kGate) {
-          s_gate[u][i] += a.alpha * d[u][i] * (yn * w0[u][i]);
-          g[u][i] *= gc[u][i];
+          gate[i] = a.alpha * d[i] * (yn * w.post[i]);
+          g[i] *= w.gate[i];
         }
-        s_post[u][i] += g[u][i] * yn;
-        g[u][i] = rstd_y * (g[u][i] * w0[u][i]) - y[u][i] * k_y;
+        post[i] = g[i] * yn;
+        g[i] = rstd_y * (g[i] * w.post[i]) - y[i] * k_y;
       }
-      write8(r_out, a.res_dtype, at.col(u), r[u]);
-      write8(r_dy, a.y_dtype, at.col(u), g[u]);
+      if constexpr (kHold) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s_post[i] += post[i];
+          if constexpr (kGate) s_gate[i] += gate[i];
+        }
+      } else {
+        add_mine(0, u, post);
+        if constexpr (kGate) add_mine(1, u, gate);
+      }
+      write8(r_out, a.res_dtype, at.col(u), r);
+      write8(r_dy, a.y_dtype, at.col(u), g);
     }
   }
   // the sums of waves that share columns, in halves: the upper half hands over
@@ -428,8 +509,17 @@ block_norm_bwd_kernel(BlockNormArgs a) {
     for (int u = 0; u < kVec; ++u) write8(r_part, kF32, at.col(u), v[u]);
   };
   if (a.w_pre) put(s_pre, 0);
-  if (a.w_post) put(s_post, 1);
-  if constexpr (kGate) put(s_gate, 2);
+#pragma unroll
+  for (int p = 1; p < (kGate ? 3 : 2); ++p) {
+#pragma unroll
+    for (int u = 0; u < kVec; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (kHold) s_pre[u][i] = p == 1 ? s_post[i] : s_gate[i];
+        else s_pre[u][i] = mine[p - 1][u][i >> 2][threadIdx.x][i & 3];
+      }
+    if (p == 2 || a.w_post) put(s_pre, p);
+  }
 }
 
 // out[c] = sum over the partial rows: 16 lanes of four columns, the 16 x 4 row
@@ -520,7 +610,9 @@ int block_norm_groups(int64_t T, int H) {
   const int waves = norm_row_waves(H);
   const int64_t rows = waves <= 4 ? kNormBwdWaves / waves : 1;
   const int64_t rounds = (T + rows - 1) / rows;
-  return (int)(rounds < kNormPartials ? rounds : kNormPartials);
+  // as few as finish in as many turns: fewer partial rows (275 x 8536 39 | 33 us)
+  const int64_t turns = (rounds + kNormPartials - 1) / kNormPartials;
+  return (int)((rounds + turns - 1) / turns);
 }
 
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s) {

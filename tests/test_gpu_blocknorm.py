@@ -89,6 +89,19 @@ def test_sizes(gpu_lib, T, H):
     both(gpu_lib, make(T, H), T, H)
 
 
+@pytest.mark.parametrize("H", [24, 512, 1000, 2048, 2888, 5120, 8200, 16384])
+@pytest.mark.parametrize("T", [2, 275])
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_channel_gate_sizes(gpu_lib, T, H, t):
+    """Every split of a row over waves, several rows a workgroup, with the sums over T."""
+    both(gpu_lib, make(T, H, res=t, y=t, h=t, gate="channel"), T, H, res=t, y=t, h=t, gate="channel")
+
+
+def test_many_long_rows(gpu_lib):
+    """Three rows of 16 columns a lane for most workgroups."""
+    both(gpu_lib, make(530, 8208), 530, 8208)
+
+
 @pytest.mark.parametrize("gate", ["none", "token", "channel"])
 @pytest.mark.parametrize("post", [True, False])
 @pytest.mark.parametrize("pre,d_r", [(True, True), (True, False), (False, True)])
