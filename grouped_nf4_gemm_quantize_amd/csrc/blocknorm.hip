@@ -16,7 +16,7 @@
 //
 // The backward's sums over T stay in registers over a workgroup's rows, are added over
 // its waves in LDS and go to one partial row a workgroup; a second kernel adds
-// the partial rows.  The same case: 29 us = 3.5 TB/s of the 12 bytes an element (26 us
+// the partial rows.  The same case: 28 us = 3.6 TB/s of the 12 bytes an element (24 us
 // and 4 us; the partial sums add 8 MB to 101).
 
 #include "common.h"
