@@ -111,23 +111,24 @@ __device__ __forceinline__ void write8(Rsrc r, int dtype, int col, float (&v)[8]
   __builtin_amdgcn_raw_buffer_store_b128(q, r, col * 2, 0, 0);
 }
 
-// How the waves of a workgroup share rows: kRowWaves waves a row in workgroups of
-// kAll, or (0, -1) all waves of a workgroup of up to 8 or 16.
+// How the waves of a workgroup share rows: kRowWaves waves a row in workgroups of kAll;
+// or five to eight waves a row (0), as many rows as kAll has eights; or all waves of
+// a workgroup of up to 16 (-1).
 template <int kRowWaves>
 constexpr int norm_waves(int all) {
-  return kRowWaves > 0 ? all : kRowWaves ? kNormMaxWaves : kNormMaxWaves / 2;
+  return kRowWaves >= 0 ? all : kNormMaxWaves;
 }
 
 template <int kRowWaves, int kAll>
 struct NormShape {
-  static constexpr int kRows = kRowWaves > 0 ? kAll / kRowWaves : 1;
+  static constexpr int kRows = kRowWaves > 0 ? kAll / kRowWaves : kRowWaves ? 1 : kAll / 8;
   static constexpr int kWaves = norm_waves<kRowWaves>(kAll);
   int lane, sub, part, row_waves;  // sub: row of the workgroup; part: wave of the row
   __device__ NormShape() {
     lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    row_waves = kRowWaves > 0 ? kRowWaves : blockDim.x >> 6;
-    sub = kRowWaves > 0 ? wave / row_waves : 0;
+    row_waves = kRowWaves > 0 ? kRowWaves : (blockDim.x >> 6) / kRows;
+    sub = kRowWaves > 0 ? wave / row_waves : kRows > 1 && wave >= row_waves;
     part = wave - sub * row_waves;
   }
   __device__ int col(int u) const { return ((u * row_waves + part) * 64 + lane) * 8; }
@@ -282,6 +283,14 @@ struct NormCols {
   float pre[8], post[8], gate[8];
 };
 
+// Waves of a backward's workgroup: sixteen, or eight for one row of five to eight waves with
+// fp32 residual and a channel gate, which need more than 128 registers (1531 x 2888, bf16 y: one
+// row 23.5 us, two 25.5; bf16 without a gate, 4096 x 2880: one 51, two 38).
+template <int kRes, int kRowWaves, bool kGate>
+constexpr int norm_bwd_waves() {
+  return kRowWaves == 0 && kRes == 4 && kGate ? 8 : kNormBwdWaves;
+}
+
 // A workgroup takes rows in turn with the others; its sums over them of the column
 // gradients go to row blockIdx.x of the partial sums (dw_pre, dw_post, dgate by
 // channel).  kDh: element size of dh (2 where there is none).
@@ -290,18 +299,22 @@ struct NormCols {
 //
 // Registers: sixteen waves have 128 a lane, and a spill among the next row's reads waits for
 // them.  With eight columns a lane (kVec 1, kHold) the next row's reads are in flight and the
-// weights stay in registers; in LDS with a channel gate or fp32 rows of four waves
+// weights stay in registers; in LDS with a channel gate or fp32 rows of four waves or more
 // (kKeep; 2048 x 5120 fp32, channel gate 87 | 62 us).  With sixteen columns, values and
 // sums alone fill the registers: the row and its weights are read again (from L2) after the
 // row's sums, and two column sums are held in LDS (275 x 8536 fp16, channel gate 85 | 33 us, 53 x
 // 13808 fp32 55 | 23).
 template <int kRes, int kY, int kDh, int kVec, int kRowWaves, bool kGate>
-__global__ __launch_bounds__(64 * norm_waves<kRowWaves>(kNormBwdWaves), kRowWaves ? 4 : 3) void
+__global__ __launch_bounds__(
+    64 * norm_waves<kRowWaves>((norm_bwd_waves<kRes, kRowWaves, kGate>())),
+    ((norm_bwd_waves<kRes, kRowWaves, kGate>()) == 8 ? 3 : 4)) void
 block_norm_bwd_kernel(BlockNormArgs a) {
-  const NormShape<kRowWaves, kNormBwdWaves> at;
-  constexpr int kRows = at.kRows, kCols = kRowWaves > 0 ? kVec * kRowWaves * 512 : 0;
+  constexpr int kAll = norm_bwd_waves<kRes, kRowWaves, kGate>();
+  const NormShape<kRowWaves, kAll> at;
+  constexpr int kRows = at.kRows, kCols = kVec * (kRowWaves > 0 ? kRowWaves : 8) * 512;
   constexpr bool kHold = kVec == 1;
-  constexpr bool kKeep = kHold && kRowWaves != 0 && (kGate || (kRes == 4 && kRowWaves == 4));
+  constexpr bool kKeep = kHold && kAll == kNormBwdWaves &&
+                         (kGate || (kRes == 4 && (kRowWaves == 4 || kRowWaves == 0)));
   __shared__ float red[2][6][kNormMaxWaves];
   // partial sums of the waves that share columns
   __shared__ f32x4 all[kRows > 1 ? kRows / 2 : 1][kRows > 1 ? kCols / 4 : 1];
@@ -548,30 +561,35 @@ __global__ __launch_bounds__(1024) void block_norm_reduce_kernel(BlockNormArgs a
 
 namespace {
 
-// Waves of a row, eight columns a lane: 1, 2 and 4 in workgroups of kNormWaves, more in one of
-// their own; sixteen columns a lane where they would be more than sixteen.
+// Waves of a row, eight columns a lane: 1, 2 and 4 in workgroups of kNormWaves (backward
+// kNormBwdWaves, which takes two rows of 5 to 8 as well), more in one of their own; sixteen
+// columns a lane where they would be more than sixteen.
 int norm_row_waves(int H) {
   const int vec = H > 512 * kNormMaxWaves ? 2 : 1;
   const int w = (H + 512 * vec - 1) / (512 * vec);
   return w == 3 ? 4 : w;
 }
 
-template <int kRes, int kY, int kDh, int kVec, int kRowWaves>
+template <int kRes, int kY, int kDh, int kVec, int kRowWaves, bool kGate>
 void norm_bwd_go(const BlockNormArgs& a, int groups, hipStream_t s) {
-  const dim3 block(64 * (kRowWaves > 0 ? kNormBwdWaves : norm_row_waves(a.H)));
-  if (a.gate_axis == 2)
-    hipLaunchKernelGGL((block_norm_bwd_kernel<kRes, kY, kDh, kVec, kRowWaves, true>), dim3(groups),
-                       block, 0, s, a);
-  else
-    hipLaunchKernelGGL((block_norm_bwd_kernel<kRes, kY, kDh, kVec, kRowWaves, false>), dim3(groups),
-                       block, 0, s, a);
+  constexpr int kAll = norm_bwd_waves<kRes, kRowWaves, kGate>();
+  constexpr int kRows = NormShape<kRowWaves, kAll>::kRows;
+  const dim3 block(64 * (kRowWaves > 0 ? kAll : norm_row_waves(a.H) * kRows));
+  hipLaunchKernelGGL((block_norm_bwd_kernel<kRes, kY, kDh, kVec, kRowWaves, kGate>), dim3(groups),
+                     block, 0, s, a);
+}
+
+template <int kRes, int kY, int kDh, int kVec, int kRowWaves>
+void norm_bwd_gate(const BlockNormArgs& a, int groups, hipStream_t s) {
+  if (a.gate_axis == 2) norm_bwd_go<kRes, kY, kDh, kVec, kRowWaves, true>(a, groups, s);
+  else norm_bwd_go<kRes, kY, kDh, kVec, kRowWaves, false>(a, groups, s);
 }
 
 template <int kRes, int kY, int kVec, int kRowWaves>
 void norm_go(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
   if (bwd_groups) {
-    if (a.dh && a.h_dtype == kF32) norm_bwd_go<kRes, kY, 4, kVec, kRowWaves>(a, bwd_groups, s);
-    else norm_bwd_go<kRes, kY, 2, kVec, kRowWaves>(a, bwd_groups, s);
+    if (a.dh && a.h_dtype == kF32) norm_bwd_gate<kRes, kY, 4, kVec, kRowWaves>(a, bwd_groups, s);
+    else norm_bwd_gate<kRes, kY, 2, kVec, kRowWaves>(a, bwd_groups, s);
     return;
   }
   const dim3 block(64 * (kRowWaves > 0 ? kNormWaves : norm_row_waves(a.H)));
@@ -604,11 +622,12 @@ void norm_launch(const BlockNormArgs& a, int bwd_groups, hipStream_t s) {
 }  // namespace
 
 // One workgroup a compute unit: with two of six waves for 1531 x 2888 the partial rows cost more
-// than the waves gained (31 us, one 26.5).  Not the device's count: the workspace's size
+// than the waves gained (31 us, one 26.5).  Counted for workgroups of sixteen waves; fewer
+// rows at a time take more turns.  Not the device's count: the workspace's size
 // follows from it, and is asked for without a device.
 int block_norm_groups(int64_t T, int H) {
   const int waves = norm_row_waves(H);
-  const int64_t rows = waves <= 4 ? kNormBwdWaves / waves : 1;
+  const int64_t rows = waves <= 4 ? kNormBwdWaves / waves : waves <= 8 ? 2 : 1;
   const int64_t rounds = (T + rows - 1) / rows;
   // as few as finish in as many turns: fewer partial rows (275 x 8536 39 | 33 us)
   const int64_t turns = (rounds + kNormPartials - 1) / kNormPartials;
@@ -625,7 +644,8 @@ hipError_t launch_block_norm_bwd(const BlockNormArgs& a, hipStream_t s) {
   norm_launch(a, groups, s);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || (!a.w_pre && !a.w_post && a.gate_axis != 2)) return err;
-  hipLaunchKernelGGL(block_norm_reduce_kernel, dim3((a.H + 63) / 64, 3), dim3(1024), 0, s, a, groups);
+  hipLaunchKernelGGL(block_norm_reduce_kernel, dim3((a.H + 63) / 64, 3), dim3(1024), 0, s, a,
+                     groups);
   return hipGetLastError();
 }
 
