@@ -31,6 +31,7 @@
 
 #include "common.h"
 #include "launch.h"
+#include "matvec_index.h"
 
 namespace nf4moe {
 
@@ -39,7 +40,6 @@ namespace {
 constexpr int kMvWaves = 16;    // waves of a workgroup, at most
 constexpr int kMvTile = 16;     // output rows of one matrix step
 constexpr int kMvTokens = 16;   // rows of x of one matrix step
-constexpr int kMvChunk = 128;   // k of one lane-wide read
 
 // What a kernel is compiled for: how the table's values are held, and the groups.
 enum MvFormat {
@@ -265,7 +265,7 @@ __global__ __launch_bounds__(64 * kMvWaves) void matvec_kernel(MatvecArgs a) {
   const int groups = a.K / (kMvChunk / kGroups);
   const int size = kFmt == kMvfMX ? 1 : !mv_int(kFmt) || a.scale_dtype == kF32 ? 4 : 2;
   const uint8_t* zeros = a.zeros ? a.zeros : a.codes;  // read but not used
-  const int lane_w = n_lane * row_bytes + 16 * q;
+  const int lane_row = n_lane * row_bytes;
   const int panels = kCpw ? 1 : (chunks + kMvWaves - 1) / kMvWaves;
   const int grid_step = gridDim.x * kRows;
 
@@ -279,13 +279,14 @@ __global__ __launch_bounds__(64 * kMvWaves) void matvec_kernel(MatvecArgs a) {
     const int64_t left = a.N - (int64_t)tile * kMvTile;
     return (uint32_t)(left < 0 ? 0 : left < kMvTile * kRows ? left : kMvTile * kRows);
   };
-  // codes of a step; a lane beyond the end of its row reads another row's (x is zero)
+  // codes of a step.  The whole offset is in the vector operand: the record count bounds
+  // that one, a scalar offset may be added after the check.
   u32x4 w[kRows][kX];
   const auto load_w = [&](int tile, int panel, int u, int j) {
     const Rsrc r = mv_rsrc(a.codes, (int64_t)tile * kMvTile * row_bytes, rows_of(tile) * row_bytes);
+    const int at = lane_row + mv_code_byte(chunk_of(panel, j), q, row_bytes);
     w[u][j] = __builtin_bit_cast(
-        u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_w + u * kMvTile * row_bytes,
-                                                     chunk_of(panel, j) * (kMvChunk / 2), 0));
+        u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at + u * kMvTile * row_bytes, 0, 0));
   };
   // scales and zeros of a step, element i of the workgroup: raw, then into LDS.  Beyond
   // the end of a row its last scale is read (x is zero there).
