@@ -612,8 +612,11 @@ template <bool kVec>
 hipError_t muon_go(const MuonArgs& a, int lds, hipStream_t s) {
   if (lds > 0) {
     if (lds > 32768) {  // beyond 64 KiB with the kernel's own
+      // The limit is the function's, not the launch's: always the same, so that a smaller call
+      // of another host thread does not lower it between here and the launch.
       const void* k = reinterpret_cast<const void*>(muon_factor_kernel<kVec>);
-      hipError_t err = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      hipError_t err = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                           kFactorFloats * 4);
       if (err != hipSuccess) return err;
     }
     hipLaunchKernelGGL(muon_factor_kernel<kVec>, dim3(a.blocks), dim3(kFactorThreads), lds, s, a);
