@@ -735,7 +735,7 @@ def lora_muon_step(tensors, lr: float, momentum: float = 0.95, nesterov: bool = 
     Each of ``tensors`` is a dict with ``grad`` and ``momentum`` (fp32), ``w`` (fp32,
     bf16 or fp16), all [E, r, n] (``rank_major=True``, the A factors) or [E, n, r]
     (False, the B factors), and optionally ``scale`` (of the update, default 1),
-    ``momentum_out``, ``w_out`` and ``w16`` (a bf16 or fp16 copy of the new fp32 w).
+    ``momentum_out``, ``w_out`` and ``w16`` (a bf16 or fp16 copy of the new w).
     """
     torch = _torch()
     if not 1 <= len(tensors) <= 8:

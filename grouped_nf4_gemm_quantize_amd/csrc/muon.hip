@@ -131,6 +131,16 @@ __device__ __forceinline__ void store4(void* p, int dtype, const Place& w, f32x4
   }
 }
 
+// What dtype holds of v: the 16-bit copy is taken of the weight as it is stored.
+__device__ __forceinline__ f32x4 held4(f32x4 v, int dtype) {
+  if (dtype != kF32) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = dtype == kBF16 ? bf16_bits_to_f32(f32_to_bf16_bits(v[e])) : (float)(_Float16)v[e];
+  }
+  return v;
+}
+
 // A factor's shape: slots, its columns c0 .. c0 + cols - 1 in hand, and the distance of its
 // ranks (A factors).
 struct Shape {
@@ -381,7 +391,7 @@ __device__ __forceinline__ void apply_factor(const MuonArgs& a, const MuonTensor
       }
       const Place pl = apply_place<kRank>(h, blk, k, lane);
       store4<kVec>(w_out, t.w_dtype, pl, o4[k]);
-      if (t.w16) store4<kVec>(w16, t.w16_dtype, pl, o4[k]);
+      if (t.w16) store4<kVec>(w16, t.w16_dtype, pl, held4(o4[k], t.w_dtype));
     }
     blk += kMuonWaves * kStep;
     if (blk < blocks) read(blk);
@@ -549,7 +559,7 @@ __device__ __forceinline__ void whole_factor(const MuonArgs& a, const MuonTensor
       for (int e = 0; e < 4; ++e) o[e] = (float)(keep * (double)wf[e] + step * (double)o[e]);
     }
     store4<kVec>(w_out, t.w_dtype, pl, o);
-    if (t.w16) store4<kVec>(w16, t.w16_dtype, pl, o);
+    if (t.w16) store4<kVec>(w16, t.w16_dtype, pl, held4(o, t.w_dtype));
   }
 }
 

@@ -614,8 +614,8 @@ int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const 
  *   grad, m, m_out  fp32 [E, r, n] (rank_major = 1: the A factors) or
  *                   [E, n, r] (rank_major = 0: the B factors); m_out may be m;
  *   w, w_out        the same layout, w_dtype F32, BF16 or F16; w_out may be w;
- *   w16             nullable: a second copy of w_out rounded to w16_dtype (BF16
- *                   or F16) once more, for fp32 w (the adapter the layer reads);
+ *   w16             nullable: w_out as it is stored, rounded once more to w16_dtype (BF16
+ *                   or F16), as for fp32 w the adapter that the layer reads;
  *   r               1 .. NF4MOE_MAX_LORA_R; E, n >= 1 (r > n is allowed);
  *   tensors [host]  1 .. NF4MOE_MAX_MUON_TENSORS factors in one call; but for m_out = m
  *                   and w_out = w no output may overlap another array of the call

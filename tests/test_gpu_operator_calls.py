@@ -50,3 +50,16 @@ def test_orthogonalize_from_two_threads(gpu_lib):
     assert not errors, errors
     for i in range(2):
         assert len(got[i]) == 40 and all(torch.equal(o, want[i]) for o in got[i])
+
+
+@pytest.mark.parametrize("shape,rank_major", [((130, 8, 256), True), ((130, 256, 8), False),
+                                              ((2, 16, 4096), True), ((2, 6001, 7), False)])
+@pytest.mark.parametrize("wt,ct", [(torch.bfloat16, torch.float16), (torch.float16, torch.bfloat16),
+                                   (torch.bfloat16, torch.bfloat16), (torch.float32, torch.float16)])
+def test_the_16_bit_copy_is_the_stored_weight_rounded(gpu_lib, shape, rank_major, wt, ct):
+    """One workgroup a factor and two launches, aligned and not."""
+    w = (0.05 * randn(*shape, seed=1)).to(wt)
+    copy = torch.zeros(shape, dtype=ct, device=DEV)
+    gpu_lib.lora_muon_step([dict(grad=randn(*shape, seed=2), momentum=randn(*shape, seed=3), w=w,
+                                 w16=copy, rank_major=rank_major)], lr=0.3)
+    assert torch.equal(copy, w.to(ct))
