@@ -14,6 +14,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <string>
 
 #include "../../include/nf4moe.h"
@@ -1207,6 +1208,13 @@ int moe_expert_forward_mxfp4(const void* x, int x_dtype, const float* router_log
 
 static bool is_float_dtype(int d) { return d == NF4MOE_F32 || d == NF4MOE_BF16 || d == NF4MOE_F16; }
 static size_t dtype_bytes(int d) { return d == NF4MOE_F32 ? 4 : 2; }
+// Whether p is given and one of the others.
+static bool is_any(const void* p, std::initializer_list<const void*> others) {
+  if (p == nullptr) return false;
+  for (const void* o : others)
+    if (o == p) return true;
+  return false;
+}
 
 int nbit_matvec(int quant_type, const void* x, int x_dtype, int64_t T, const uint8_t* codes,
                 const void* scales, int scale_dtype, const uint8_t* zeros, int group,
@@ -1241,7 +1249,8 @@ int nbit_matvec(int quant_type, const void* x, int x_dtype, int64_t T, const uin
   if (T > NF4MOE_MATVEC_MAX_T || N > (int64_t)INT32_MAX - 64 || K > ((int64_t)1 << 24))
     return fail(NF4MOE_EOVERFLOW, "T=%lld, N=%lld or K=%lld is too large", (long long)T,
                 (long long)N, (long long)K);
-  if (y == x) return fail(NF4MOE_EINVAL, "y must not be x");
+  if (is_any(y, {x, codes, scales, zeros, bias}))
+    return fail(NF4MOE_EINVAL, "y must not be one of the inputs");
   const size_t sb = quant_type == kMvMXFP4 ? 1 : dtype_bytes(scale_dtype);
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, sb) || !aligned(bias, 4) ||
       !aligned(y, dtype_bytes(y_dtype)))
@@ -1328,6 +1337,8 @@ int block_norm_forward(const void* residual, int res_dtype, const void* y, int y
     return fail(NF4MOE_EINVAL, "h may be y of the same type, and no other of the matrices");
   if (r_out != nullptr && r_out == y)
     return fail(NF4MOE_EINVAL, "r_out must not be y");
+  if (is_any(r_out, {w_pre, w_post, gate}) || is_any(h, {w_pre, w_post, gate}))
+    return fail(NF4MOE_EINVAL, "r_out and h must not be weights or the gate");
   BlockNormArgs a{};
   a.residual = residual;
   a.y = y;
@@ -1389,6 +1400,14 @@ int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const 
     return fail(NF4MOE_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                 workspace ? ws_bytes : (size_t)0);
   if (!aligned(workspace, 256)) return fail(NF4MOE_EINVAL, "workspace must be 256-byte aligned");
+  // the pairs the checks above leave: dresidual and dy may share with some matrices, others with none
+  const void* out[6] = {dgate, dw_pre, dw_post, workspace, dresidual, dy};
+  for (int i = 0; i < 6; ++i) {
+    bool equal = is_any(out[i], {w_pre, w_post, gate});
+    if (i < 4) equal = equal || is_any(out[i], {dh, d_r_out, r, y});
+    for (int j = 0; j < i; ++j) equal = equal || is_any(out[i], {out[j]});
+    if (equal) return fail(NF4MOE_EINVAL, "an output or the workspace is another array of the call");
+  }
   BlockNormArgs a{};
   a.residual = r;
   a.y = y;

@@ -519,7 +519,7 @@ int moe_expert_forward_routing(void* workspace, int64_t T, int H, int I,
  *   scales      [N, K/group]; scale_dtype is for INT4 (must be F32 for NF4
  *               and FP4, ignored for MXFP4);
  *   bias        nullable fp32 [N];
- *   y [T, N]    F32, BF16 or F16; must not overlap the inputs.
+ *   y [T, N]    F32, BF16 or F16; must not overlap the inputs (EINVAL for equal pointers).
  * Non-finite x makes its row of y non-finite, a non-finite scale its column
  * (an infinity may come out as NaN); no other results change.
  * 16 rows of x share one read of the matrix, more rows read it again (mostly from
