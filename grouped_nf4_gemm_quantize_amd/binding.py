@@ -675,21 +675,31 @@ def block_norm(residual, y=None, w_pre=None, w_post=None, gate=None, gate_axis: 
 
 def block_norm_backward(dh, d_r_out, r, y=None, w_pre=None, w_post=None, gate=None,
                         gate_axis: str = "token", alpha: float = 1.0, beta: float = 1.0,
-                        eps: float = 1e-6, w_offset: float = 0.0, workspace=None):
+                        eps: float = 1e-6, w_offset: float = 0.0, workspace=None,
+                        dresidual=None, dy=None):
     """Gradients of ``block_norm`` (see block_norm_backward in include/nf4moe.h) from
-    those of h and r (either may be None where the other is given); ``r`` is what
-    the forward returned.
+    those of h (None exactly where ``w_pre`` is) and r (None where nothing reaches it but
+    through h); ``r`` is what the forward returned.
 
     Returns a dict with ``dresidual`` and, where their inputs are given, ``dy``,
-    ``dgate``, ``dw_pre`` and ``dw_post`` (the last three fp32).
+    ``dgate``, ``dw_pre`` and ``dw_post`` (the last three fp32).  ``dresidual=`` may name
+    ``d_r_out`` and ``dy=`` may name ``y`` or ``dh`` (of y's type) as the place to write to.
     """
     torch = _torch()
     dev = r.device
     args = _norm_args(r, y, gate, gate_axis, w_pre, w_post, w_offset, alpha, beta, eps)
     T, H = r.shape
-    out = dict(dresidual=torch.empty_like(r))
+    if dresidual is None:
+        dresidual = torch.empty_like(r)
+    else:
+        _need(dresidual, "dresidual", dev, r.shape, r.dtype)
+    out = dict(dresidual=dresidual)
     if y is not None:
-        out["dy"] = torch.empty_like(y)
+        out["dy"] = torch.empty_like(y) if dy is None else dy
+        if dy is not None:
+            _need(dy, "dy", dev, y.shape, y.dtype)
+    elif dy is not None:
+        raise ValueError("dy is written only where y is given")
     if gate is not None:
         out["dgate"] = torch.empty_like(gate)
     if w_pre is not None:
