@@ -28,6 +28,9 @@
 // scaled by 2^8 so that the small parts stay normal, and multiplied twice.  All
 // other formats' values are exact in fp16 (fp4's 1/6 and the 2^-8 are applied to
 // the final sum).
+// fp4's and MXFP4's values are exact in bf16 too, so bf16 x is multiplied as it is.  For
+// nf4 it becomes fp16 (as in the expert stacks): bf16 parts of 22-bit levels would be
+// three products.  For int4 as well: code - zero in pairs is an fp16 operation, bf16 has none.
 
 #include "common.h"
 #include "launch.h"
@@ -45,17 +48,22 @@ constexpr int kMvTokens = 16;   // rows of x of one matrix step
 enum MvFormat {
   kMvfNF4,      // two fp16 tables, fp32 scales of 64
   kMvfFP4,      // fp32 scales of 64
+  kMvfFP4b,     // the same for bf16 x
   kMvfMX,       // e8m0 scales of 32
+  kMvfMXb,      // the same for bf16 x
   kMvfInt32,    // codes minus zeros, scales of 32, 64 or 128 of any float type
   kMvfInt64,
   kMvfInt128
 };
 constexpr bool mv_split(int f) { return f == kMvfNF4; }
+constexpr bool mv_mx(int f) { return f == kMvfMX || f == kMvfMXb; }
+constexpr bool mv_bf16(int f) { return f == kMvfFP4b || f == kMvfMXb; }  // products of bf16 values
 constexpr bool mv_int(int f) { return f >= kMvfInt32; }
 // scale groups of a chunk
-constexpr int mv_groups(int f) { return f == kMvfMX || f == kMvfInt32 ? 4 : f == kMvfInt128 ? 1 : 2; }
+constexpr int mv_groups(int f) { return mv_mx(f) || f == kMvfInt32 ? 4 : f == kMvfInt128 ? 1 : 2; }
 
 typedef __amdgpu_buffer_rsrc_t Rsrc;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ Rsrc mv_rsrc(const void* p, int64_t offset, uint32_t bytes) {
   char* at = const_cast<char*>(reinterpret_cast<const char*>(p)) + offset;
@@ -65,7 +73,7 @@ __device__ __forceinline__ Rsrc mv_rsrc(const void* p, int64_t offset, uint32_t 
 // Raw scale -> fp32.
 template <int kFmt>
 __device__ __forceinline__ float mv_scale(uint32_t raw, int dtype) {
-  if constexpr (kFmt == kMvfMX)  // 2^(raw - 127), 255 is NaN
+  if constexpr (mv_mx(kFmt))  // 2^(raw - 127), 255 is NaN
     return __uint_as_float(raw == 0u ? 0x00400000u : raw == 255u ? 0x7fc00000u : raw << 23);
   if (!mv_int(kFmt) || dtype == kF32) return __uint_as_float(raw);
   return dtype == kBF16 ? bf16_bits_to_f32(raw)
@@ -96,8 +104,18 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&d)[4]) {
 // a table entry as they are read.
 template <int kFmt>
 struct MvX {
-  f16x8 v[mv_split(kFmt) ? 2 : 1];
+  u32x4 v[mv_split(kFmt) ? 2 : 1];
 };
+
+template <int kFmt>
+__device__ __forceinline__ f32x4 mv_mfma(u32x4 x, u32x4 w, f32x4 c) {
+  if constexpr (mv_bf16(kFmt))
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x),
+                                                   __builtin_bit_cast(bf16x8, w), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x),
+                                                  __builtin_bit_cast(f16x8, w), c, 0, 0, 0);
+}
 
 // tot += the products of one chunk of one row tile, whose scales and zeros begin at
 // `scales` and `zeros`.  Steps beyond the end of the row have x = 0.
@@ -148,19 +166,15 @@ __device__ __forceinline__ void mv_chunk(const char* lut, uint32_t lane_off, u32
     if constexpr (mv_split(kFmt)) {
       const u32x4 b0 = {hi[s][0], lo[s][0], hi[s][1], lo[s][1]};
       const u32x4 b1 = {hi[s][2], lo[s][2], hi[s][3], lo[s][3]};
-      acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s].v[0], __builtin_bit_cast(f16x8, b0), none,
-                                                      0, 0, 0);
-      acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s].v[1], __builtin_bit_cast(f16x8, b1),
-                                                      acc[s], 0, 0, 0);
+      acc[s] = mv_mfma<kFmt>(x[s].v[0], b0, none);
+      acc[s] = mv_mfma<kFmt>(x[s].v[1], b1, acc[s]);
     } else {
       if constexpr (mv_int(kFmt)) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           hi[s][j] = half2_as_u32(u32_as_half2(hi[s][j]) - zero[s * kGroups / 4]);
       }
-      const u32x4 b = {hi[s][0], hi[s][1], hi[s][2], hi[s][3]};
-      acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s].v[0], __builtin_bit_cast(f16x8, b), none,
-                                                      0, 0, 0);
+      acc[s] = mv_mfma<kFmt>(x[s].v[0], u32x4{hi[s][0], hi[s][1], hi[s][2], hi[s][3]}, none);
     }
   }
 #pragma unroll
@@ -180,12 +194,13 @@ __device__ __forceinline__ void mv_read_x(const MatvecArgs& a, int64_t t0, int n
   const int m = lane & 15, q = lane >> 4;
   const int t = (m >> 2) * kRegs + (m & 3);
   const bool live = (m & 3) < kRegs && t < nt;
-  const uint16_t* p = reinterpret_cast<const uint16_t*>(a.x) + (t0 + t) * a.K + c * kMvChunk + 8 * q;
+  // beyond the end the offset is out of the buffer's bounds, and the read gives 0
+  const Rsrc r = mv_rsrc(a.x, t0 * a.K * 2, (uint32_t)(nt * a.K * 2));
+  const int at = (t * a.K + c * kMvChunk + 8 * q) * 2;
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    v[s] = u32x4{0u, 0u, 0u, 0u};
-    if (live && 32 * s < left) v[s] = *reinterpret_cast<const u32x4*>(p + 32 * s);
-  }
+  for (int s = 0; s < 4; ++s)
+    v[s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                         r, live && 32 * s < left ? at + 64 * s : 0x7ffffff0, 0, 0));
 }
 
 template <int kFmt>
@@ -194,17 +209,17 @@ __device__ __forceinline__ void mv_set_x(const MatvecArgs& a, const u32x4 (&raw)
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     u32x4 v = raw[s];
-    if (a.x_bf16) {
+    if (!mv_bf16(kFmt) && a.x_bf16) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         v[i] = pack_half2((_Float16)bf16_bits_to_f32(v[i] & 0xffffu),
                           (_Float16)bf16_bits_to_f32(v[i] >> 16));
     }
     if constexpr (mv_split(kFmt)) {
-      x[s].v[0] = __builtin_bit_cast(f16x8, (u32x4{v.x, v.x, v.y, v.y}));
-      x[s].v[1] = __builtin_bit_cast(f16x8, (u32x4{v.z, v.z, v.w, v.w}));
+      x[s].v[0] = u32x4{v.x, v.x, v.y, v.y};
+      x[s].v[1] = u32x4{v.z, v.z, v.w, v.w};
     } else {
-      x[s].v[0] = __builtin_bit_cast(f16x8, v);
+      x[s].v[0] = v;
     }
   }
 }
@@ -225,13 +240,13 @@ __device__ __forceinline__ void mv_fill(u32x4* lut, uint32_t* stage, int tid) {
         if (tid == i) v = mv_split(kFmt) ? 256.0f * nf4[i] : e2m1[i];
     }
     const _Float16 hi = (_Float16)v, lo = (_Float16)(v - (float)hi);
-    stage[tid] = pack_half2(hi, lo);
+    stage[tid] = mv_bf16(kFmt) ? f32_to_bf16_bits(v) : pack_half2(hi, lo);
   }
   __syncthreads();
   for (int u = tid; u < 4096; u += blockDim.x) {
     const int b = u >> 4;  // 16 16-byte units an entry
-    const uint32_t first = stage[kFmt == kMvfMX ? b & 15 : b >> 4];
-    const uint32_t second = stage[kFmt == kMvfMX ? b >> 4 : b & 15];
+    const uint32_t first = stage[mv_mx(kFmt) ? b & 15 : b >> 4];
+    const uint32_t second = stage[mv_mx(kFmt) ? b >> 4 : b & 15];
     const uint32_t h = (first & 0xffffu) | (second << 16);
     const uint32_t l = (first >> 16) | (second & 0xffff0000u);
     lut[u] = mv_split(kFmt) ? u32x4{h, l, h, l} : u32x4{h, h, h, h};
@@ -263,7 +278,7 @@ __global__ __launch_bounds__(64 * kMvWaves) void matvec_kernel(MatvecArgs a) {
   const uint32_t lane_off = mv_split(kFmt) ? (lane & 31) * 8 : lane * 4;
   const int row_bytes = a.K / 2;
   const int groups = a.K / (kMvChunk / kGroups);
-  const int size = kFmt == kMvfMX ? 1 : !mv_int(kFmt) || a.scale_dtype == kF32 ? 4 : 2;
+  const int size = mv_mx(kFmt) ? 1 : !mv_int(kFmt) || a.scale_dtype == kF32 ? 4 : 2;
   const uint8_t* zeros = a.zeros ? a.zeros : a.codes;  // read but not used
   const int lane_row = n_lane * row_bytes;
   const int panels = kCpw ? 1 : (chunks + kMvWaves - 1) / kMvWaves;
@@ -304,7 +319,7 @@ __global__ __launch_bounds__(64 * kMvWaves) void matvec_kernel(MatvecArgs a) {
       const int i = tid + k * blockDim.x, row = (int)(i * magic >> 20);
       const int g = panel * kMvWaves * kGroups + i - row * seg;
       const int at = row * groups + (g < groups ? g : groups - 1);
-      if (kFmt == kMvfMX) raw_s[k] = __builtin_amdgcn_raw_buffer_load_b8(rs, at, 0, 0);
+      if (mv_mx(kFmt)) raw_s[k] = __builtin_amdgcn_raw_buffer_load_b8(rs, at, 0, 0);
       else if (size == 4) raw_s[k] = __builtin_amdgcn_raw_buffer_load_b32(rs, at * 4, 0, 0);
       else raw_s[k] = __builtin_amdgcn_raw_buffer_load_b16(rs, at * 2, 0, 0);
       if constexpr (mv_int(kFmt)) raw_z[k] = __builtin_amdgcn_raw_buffer_load_b8(rz, at, 0, 0);
@@ -348,7 +363,7 @@ __global__ __launch_bounds__(64 * kMvWaves) void matvec_kernel(MatvecArgs a) {
 #pragma unroll
   for (int j = 0; j < kCpw; ++j) mv_set_x<kFmt>(a, raw_x[j], x[j]);
   const char* table = reinterpret_cast<const char*>(lut);
-  const float last = mv_split(kFmt) ? 1.0f / 256.0f : kFmt == kMvfFP4 ? 1.0f / 6.0f : 1.0f;
+  const float last = mv_split(kFmt) ? 1.0f / 256.0f : kFmt == kMvfFP4 || kFmt == kMvfFP4b ? 1.0f / 6.0f : 1.0f;
 
   float tot[kOut] = {};
   for (int buf = 0, out = 0; tile < tiles; buf ^= 1) {
@@ -459,7 +474,9 @@ void mv_launch_format(const MatvecArgs& a, int cus, hipStream_t s) {
 
 hipError_t launch_matvec(const MatvecArgs& a, int num_cus, hipStream_t s) {
   if (a.qt == kMvNF4) mv_launch_format<kMvfNF4>(a, num_cus, s);
+  else if (a.qt == kMvFP4 && a.x_bf16) mv_launch_format<kMvfFP4b>(a, num_cus, s);
   else if (a.qt == kMvFP4) mv_launch_format<kMvfFP4>(a, num_cus, s);
+  else if (a.qt == kMvMXFP4 && a.x_bf16) mv_launch_format<kMvfMXb>(a, num_cus, s);
   else if (a.qt == kMvMXFP4) mv_launch_format<kMvfMX>(a, num_cus, s);
   else if (a.group == 32) mv_launch_format<kMvfInt32>(a, num_cus, s);
   else if (a.group == 64) mv_launch_format<kMvfInt64>(a, num_cus, s);

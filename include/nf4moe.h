@@ -512,9 +512,10 @@ int moe_expert_forward_routing(void* workspace, int64_t T, int H, int I,
  *               NF4MOE_QT_MXFP4: e2m1 values, group 32, e8m0 scale bytes
  *               (255 is NaN), element 2i in the LOW nibble;
  *               element 2i is in the HIGH nibble for the other three;
- *   x [T, K]    F16 or BF16; enters the multiplication as fp16 (the range
- *               of the conventions above); T >= 1.  Products, sums and scales
- *               are fp32: levels are held to 22 bits and more;
+ *   x [T, K]    F16 or BF16, T >= 1.  Enters the multiplication as it is, but for BF16 x
+ *               of NF4 and INT4, which becomes fp16 (the range of the conventions
+ *               above).  Products, sums and scales are fp32: levels are held to 22 bits and
+ *               more;
  *   codes       [N, K/2]; K a multiple of `group` (ESHAPE), N >= 1, any;
  *   scales      [N, K/group]; scale_dtype is for INT4 (must be F32 for NF4
  *               and FP4, ignored for MXFP4);

@@ -120,3 +120,16 @@ def test_many_rows_of_x(gpu_lib, T, qt, group, N, K):
     x, codes, st, s, z = mv.make(qt, group, T, N, K)
     ref, mag = oracle.matvec(x.float().numpy(), codes, s, qt, group, z)
     mv.check(mv.run(gpu_lib, x, codes, st, z, qt, group, out_dtype=torch.float32), ref, mag, K, "f32")
+
+
+@pytest.mark.parametrize("power", [-100, -40, -20, 20, 100])
+@pytest.mark.parametrize("T,K", [(1, 256), (5, 256), (16, 2112), (3, 4416), (20, 6208)])
+@pytest.mark.parametrize("qt,group", [("fp4", 64), ("mxfp4", 32)])
+def test_bf16_rows_of_any_size(gpu_lib, qt, group, T, K, power):
+    """The values of fp4 and MXFP4 are bf16 numbers: x keeps its range and its bits."""
+    K = K // group * group
+    x, codes, st, s, z = mv.make(qt, group, T, 70, K)
+    x[:, ::7] *= 2.0 ** -20  # beside values a million times as large
+    x = x * 2.0 ** power
+    ref, mag = oracle.matvec(x.double().numpy(), codes, s, qt, group)
+    mv.check(mv.run(gpu_lib, x, codes, st, z, qt, group, out_dtype=torch.float32), ref, mag, K, "f32")
