@@ -446,14 +446,26 @@ void mv_launch(const MatvecArgs& a, int cus, hipStream_t s) {
   // as few waves as take the chunks in as many turns
   const int waves = (chunks + per - 1) / per;
   // Tiles of a round: several save barriers and reads of x and cost balance between
-  // workgroups; sixteen tokens' sums leave LDS for two.  nf4, us for one and several:
-  //   up to 4 tokens, K 2048, one | four: N 4096 5.7 | 8.3, 32768 13.3 | 14.0, 65536 23.5 | 21.3
-  //   16 tokens, K 2048, one | two: N 4096 7.0 | 7.7, 8192 8.7 | 7.9, 65536 31 | 25
-  //   one token, K 8192, one | two | four: N 4096 10.8 | 12.7 | -, 8192 17.5 | 14.0 | 18.5,
-  //   16384 33 | 24.0 | 20.8, 32768 64 | 44 | 40.5
-  // Where a wave has two chunks they are even (int4, K 4096, N 28672 17.0 | 16.9).
+  // workgroups; sixteen tokens' sums leave LDS for two.  us for one and several, in a graph:
+  //   up to 4 tokens, K 2048, one | four    nf4           MXFP4         int4 (128)
+  //     N 4096                              5.1 | 7.5     4.8 | 7.3     5.5 | 7.7
+  //     N 24576                             11.8 | 13.3   11.5 | 12.7   12.7 | 11.9
+  //     N 32768                             14.6 | 13.9   14.1 | 13.4   15.6 | 12.1
+  //     N 65536                             24.6 | 20.7   24.5 | 19.8   27.1 | 17.9
+  //   (int4 in groups of 32: N 24576 12.0 | 13.6, 32768 14.6 | 14.0)
+  //   16 tokens, K 2048, one | two: N 4096  6.4 | 7.2     6.1 | 7.1     6.5 | 7.4
+  //     N 8192                              8.0 | 7.3     7.6 | 7.2     7.8 | 7.5
+  //   64 tokens, K 2048, N 16384            27.6 | 21.9   27.6 | 22.6   27.4 | 21.6
+  //   one token, K 8192, one | two | four   nf4                  MXFP4
+  //     N 4096                              10.0 | 12.5 | 17.9   8.8 | 11.6 | 17.3
+  //     N 8192                              16.6 | 14.7 | 19.9   15.4 | 14.1 | 19.5
+  //     N 16384                             28.3 | 23.4 | 23.0   26.2 | 22.4 | 22.7
+  //     N 32768                             52.6 | 41.8 | 38.9   47.9 | 39.6 | 37.4
+  //   16 tokens, K 8192, one | two: N 4096  13.5 | 15.8   13.5 | 15.6
+  //     N 8192                              24.1 | 18.1   23.2 | 17.2
+  // Where a wave has two chunks of K they were even (int4, K 4096, N 28672 17.0 | 16.9).
   constexpr int kMany = kRegs == 1 ? 4 : 2;
-  if (per == 1 && tiles >= (kRegs == 1 ? 16 : 2) * nx)
+  if (per == 1 && tiles >= (kRegs == 1 ? 8 : 2) * nx)
     mv_go<kFmt, kRegs, 1, kMany>(a, nx, ny, waves, s);
   else if (per == 1) mv_go<kFmt, kRegs, 1, 1>(a, nx, ny, waves, s);
   else if (per == 2) mv_go<kFmt, kRegs, 2, 1>(a, nx, ny, waves, s);
@@ -464,8 +476,9 @@ void mv_launch(const MatvecArgs& a, int cus, hipStream_t s) {
 
 template <int kFmt>
 void mv_launch_format(const MatvecArgs& a, int cus, hipStream_t s) {
-  // results of up to four tokens are one register a lane: fewer sums (nf4, K 8192, N 8192: one
-  // token 14.0 us, sixteen 17.7)
+  // results of up to four tokens are one register a lane: fewer sums, and more tiles a round (one
+  // register | four, nf4: one token 4096x2048 5.0 | 5.5 us, four 65536x2048 21.0 | 24.1,
+  // 32768x8192 40.0 | 46.3; MXFP4 and int4 alike)
   if (a.T <= 4) mv_launch<kFmt, 1>(a, cus, s);
   else mv_launch<kFmt, 4>(a, cus, s);
 }
