@@ -3,10 +3,11 @@
 //   z = y * rstd(y) * (w_post + off),  r = beta * residual + alpha * gate * z,
 //   h = r * rstd(r) * (w_pre + off),   rstd(v) = 1 / sqrt(mean(v^2) + eps).
 //
-// Bound by memory: every matrix is read once and written once.  The waves of a
-// row hold it in registers, eight consecutive columns a lane (sixteen beyond 8192
-// columns): few registers, so that sixteen waves and their reads are in flight on a
-// compute unit.  All of a row's reads are issued together, before any of them is
+// Bound by memory: every matrix is read once (twice by the backward beyond 8192 columns)
+// and written once.  The waves of a row hold it in registers, eight consecutive columns a
+// lane (sixteen beyond 8192 columns): few registers, so that sixteen waves and their reads
+// are in flight on a compute unit.  A row has a wave at least: at 128 columns 48 of 64 lanes
+// have none (65536 x 128 bf16 39 us forward and 62 backward, against 13 and 19 for the bytes).  All of a row's reads are issued together, before any of them is
 // converted; they go through buffer bounds, so that columns and rows beyond the end
 // need no branch between them.  r is rounded to its type before it is normalised, so
 // h follows from what is stored.
@@ -284,8 +285,10 @@ struct NormCols {
 };
 
 // Waves of a backward's workgroup: sixteen, or eight for one row of five to eight waves with
-// fp32 residual and a channel gate, which need more than 128 registers (1531 x 2888, bf16 y: one
-// row 23.5 us, two 25.5; bf16 without a gate, 4096 x 2880: one 51, two 38).
+// fp32 residual and a channel gate, which need more than 128 registers.  us of one row | two, in a
+// graph: y fp32 1531 x 2888 27.1 | 31.8, 4096 x 2560 46.3 | 53.2, 2048 x 4096 39.6 | 48.6;
+// y bf16 1531 x 2888 28.4 | 28.7, 4096 x 2560 55.8 | 50.4, 4096 x 3584 57.2 | 63.0, 2048 x 4096
+// 35.3 | 43.3.  bf16 without a gate, 4096 x 2880: 51 | 38.
 template <int kRes, int kRowWaves, bool kGate>
 constexpr int norm_bwd_waves() {
   return kRowWaves == 0 && kRes == 4 && kGate ? 8 : kNormBwdWaves;
@@ -301,9 +304,13 @@ constexpr int norm_bwd_waves() {
 // them.  With eight columns a lane (kVec 1, kHold) the next row's reads are in flight and the
 // weights stay in registers; in LDS with a channel gate or fp32 rows of four waves or more
 // (kKeep; 2048 x 5120 fp32, channel gate 87 | 62 us).  With sixteen columns, values and
-// sums alone fill the registers: the row and its weights are read again (from L2) after the
+// sums alone fill the registers: the row and its weights are read again after the
 // row's sums, and two column sums are held in LDS (275 x 8536 fp16, channel gate 85 | 33 us, 53 x
-// 13808 fp32 55 | 23).
+// 13808 fp32 55 | 23).  The second reading is not all from L2: 512 x 16384 bf16 fetches 1.7 times
+// the matrices' bytes, 2.6 times with a channel gate.
+// Spills are fewer than without this, not gone: 38 of the 96 kernels have some.  Up to 8192
+// columns 8 to 40 bytes a lane, all but one with a channel gate; beyond, 20 to 36 bytes, 92 to
+// 116 with a channel gate; 16-bit rows without one have none up to 8192.
 template <int kRes, int kY, int kDh, int kVec, int kRowWaves, bool kGate>
 __global__ __launch_bounds__(
     64 * norm_waves<kRowWaves>((norm_bwd_waves<kRes, kRowWaves, kGate>())),

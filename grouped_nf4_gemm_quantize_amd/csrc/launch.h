@@ -293,7 +293,8 @@ struct MuonArgs {
 };
 int muon_chunk_cols(int E, int64_t n, int r);
 // Whether one workgroup takes a factor in any case (no Gram parts in the workspace).
-inline bool muon_small(int r, int64_t n) { return r * n <= 16384; }
+constexpr int kMuonSmall = 16384;
+inline bool muon_small(int r, int64_t n) { return r * n <= kMuonSmall; }
 hipError_t launch_muon(MuonArgs& a, int num_cus, hipStream_t s);
 
 }  // namespace nf4moe

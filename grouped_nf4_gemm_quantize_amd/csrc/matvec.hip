@@ -16,13 +16,13 @@
 // A wave's part of x stays in registers from tile to tile (up to K = 4096), and the
 // next tiles' codes are in flight while a tile is computed.  The waves' sums meet in LDS.
 // Measured (one MI355X, a call among others): nf4 151936 x 2048, four tokens, fp32 out
-// 41 us = 4.3 TB/s of codes and scales; int4 28672 x 4096, one token 15.8 us = 3.9 TB/s; below
-// some 10 MB launch and first reads set the time (2048 x 2048, one token: 5.6 us).
+// 39.9 us = 4.4 TB/s of codes and scales; int4 28672 x 4096, one token 16.2 us = 3.8 TB/s; below
+// some 10 MB launch and first reads set the time (2048 x 2048, one token: 4.9 us in a graph).
 //
 // Scales and zeros go through LDS too: read by the wave that uses them, a chunk's few
-// bytes of 16 rows cost as many cache lines as its codes (28672 x 4096 int4, groups of 128,
-// one token: 28.7 us, without these reads 15.9 us).  The workgroup reads a round's
-// as consecutive elements instead, two steps ahead (16.5 us).
+// bytes of 16 rows cost as many cache lines as its codes.  The workgroup reads a round's
+// as consecutive elements instead, two steps ahead: when this was changed, int4 28672 x 4096
+// in groups of 128, one token, went from 28.7 to 16.5 us (15.9 with no scales read at all).
 //
 // nf4's levels are no fp16 values: each is held as a sum of two (22 bits),
 // scaled by 2^8 so that the small parts stay normal, and multiplied twice.  All

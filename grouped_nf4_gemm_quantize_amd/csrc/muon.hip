@@ -32,7 +32,10 @@
 // r 8; 81 MB) 24.5 us = 3.3 TB/s, bf16 factors of 128 experts (H 2048, I 768, r 16; 210 MB)
 // 79 us = 2.7 TB/s: a factor's fp64 products (8 k cycles each for u u^T and P u at 16 x
 // 2048) and the algebra (0.5 us a step) are not covered by another factor's reads.
-// 8 factors of 8 x 1000 take 11 us.
+// 8 factors of 8 x 1000 take 11 us.  One tensor of a call whose elements are not four to an
+// aligned read (r n or its row no multiple of four, an unaligned pointer) puts the whole call on
+// the kernels with single reads, which spill 44 (factor) and 121 registers (apply): 64 experts'
+// factors of rank 7 (H 2048, I 768) take 42 us against 12 for the bytes.
 
 #include "common.h"
 #include "launch.h"
@@ -49,6 +52,8 @@ constexpr int kFactorThreads = 1024;  // of the one
 constexpr int kFactorWaves = kFactorThreads / 64;
 constexpr int kFactorReads = 9;       // reads of four elements a thread: 36864 elements
 constexpr int kFactorFloats = 33792;  // LDS copy of u, with its padding
+// Small factors, which get no workspace, always fit: rows of at most 7 elements more, 16 ranks.
+static_assert(kMuonSmall + 16 * 7 <= kFactorFloats, "small factors take one launch");
 
 __device__ __forceinline__ f64x4 mfma64(double a, double b, f64x4 c) {
   return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
@@ -525,7 +530,9 @@ __device__ __forceinline__ void whole_factor(const MuonArgs& a, const MuonTensor
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const Place pl = apply_place<kRank>(h, blk, k, lane);
-      f32x4 y;  // O in fp32: half a unit in 2^24 of a step that w absorbs scaled by lr
+      // O in fp32, as LDS has room for no more: half a unit in 2^24 of the step.  w' is
+      // rounded to its type after that, so where w is (nearly) zero it is rounded twice.
+      f32x4 y;
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = (float)(kRank ? o[e][k] : o[k][e]);
       if (wide) {

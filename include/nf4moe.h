@@ -508,7 +508,8 @@ int moe_expert_forward_routing(void* workspace, int64_t T, int H, int I,
  *               expert's [N, K] slice of a stack is a valid matrix);
  *               NF4MOE_QT_INT4: v = code (0..15), group 32, 64 or 128,
  *               scales F32, BF16 or F16, zeros uint8 [N, K/group] or NULL for 8
- *               everywhere (symmetric);
+ *               everywhere (symmetric).  The library reads this layout and does not
+ *               make it: the codes come from the caller's own quantiser;
  *               NF4MOE_QT_MXFP4: e2m1 values, group 32, e8m0 scale bytes
  *               (255 is NaN), element 2i in the LOW nibble;
  *               element 2i is in the HIGH nibble for the other three;
@@ -523,9 +524,10 @@ int moe_expert_forward_routing(void* workspace, int64_t T, int H, int I,
  *   y [T, N]    F32, BF16 or F16; must not overlap the inputs (EINVAL for equal pointers).
  * Non-finite x makes its row of y non-finite, a non-finite scale its column
  * (an infinity may come out as NaN); no other results change.
- * 16 rows of x share one read of the matrix, more rows read it again (mostly from
- * cache): from 128 to 512 rows on, earlier for larger N, the grouped GEMM with E = 1
- * is the better call (nf4 16384 x 2048: 64 rows 25 us against 39, 256 rows 73 against 53).
+ * 16 rows of x share one read of the matrix, more rows read and decode it again (from L2:
+ * 64 rows of nf4 16384 x 2048 fetch 21.0 MB, 16 rows 19.5).  The grouped GEMM with E = 1 is
+ * the better call from 128 rows on there (64 rows 23 us against 39, 128 rows 40 against 39,
+ * 256 rows 71 against 53), beyond 512 for 4096 x 4096 (74 against 94 there).
  * No workspace.  The order of the sums depends on the sizes only: results are the
  * same from call to call.
  * Alignment (else EINVAL): x and codes 16 bytes, scales, bias and y their
@@ -558,7 +560,8 @@ int nbit_matvec(int quant_type, const void* x, int x_dtype, int64_t T,
  *   H           a multiple of 8, at most 16384 (ESHAPE); T >= 1;
  *   eps >= 0, alpha, beta and w_offset finite (EINVAL).
  * All matrices and weights 16-byte aligned, gate 4 (else EINVAL).  Means and
- * sums are fp32.  One launch, no workspace. */
+ * sums are fp32: the squares of a row have to sum to less than 3.4e38, and with eps = 0
+ * rows below 1e-19 lose bits and a row of zeros gives NaN.  One launch, no workspace. */
 #define NF4MOE_GATE_NONE 0
 #define NF4MOE_GATE_TOKEN 1
 #define NF4MOE_GATE_CHANNEL 2
@@ -609,8 +612,11 @@ int block_norm_backward(const void* dh, int h_dtype, const void* d_r_out, const 
  *   X  = u / (|u|_F + ns_eps), then ns_steps times
  *   X <- a X + b (X X^T) X + c (X X^T)^2 X;            O = X
  *   w' = w * (1 - lr * weight_decay) - lr * scale * O
- * The Gram matrix, the r x r products and O are computed in 64 bits, m' and u in
- * 32; O may be rounded to 32 before w', which is rounded once to its type.  A factor whose u is zero has O = 0; one
+ * The Gram matrix, the r x r products and O are computed in 64 bits, m' and u in 32.  Where
+ * one workgroup takes a whole factor O is rounded to 32 before w', which is rounded to its
+ * type then.  Which way is taken, and with it the order of the 64-bit sums, follows from the
+ * sizes of all of the call's tensors and the device: the same call gives the same bits, a
+ * factor in other company may differ in the last.  A factor whose u is zero has O = 0; one
  * with a non-finite u gets NaN, and no other factor is touched by it.
  *   grad, m, m_out  fp32 [E, r, n] (rank_major = 1: the A factors) or
  *                   [E, n, r] (rank_major = 0: the B factors); m_out may be m;
