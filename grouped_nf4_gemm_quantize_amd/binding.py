@@ -598,7 +598,8 @@ def nbit_matvec(x, codes, scales, quant_type: str = "nf4", group: Optional[int] 
     ``codes`` is uint8 [N, K/2] and ``scales`` [N, K/group]: fp32 for ``"nf4"`` and
     ``"fp4"`` (what ``quantize`` returns, one expert's slice of it), fp32 / bf16 /
     fp16 for ``"int4"`` (``zeros`` uint8 [N, K/group], None: 8), e8m0 bytes for
-    ``"mxfp4"``.  ``bias`` is fp32 [N].  ``group`` defaults to 64 (32 for mxfp4).
+    ``"mxfp4"``.  ``bias`` is fp32 [N].  ``group`` defaults to 64 (32 for mxfp4).  ``x`` is bf16 or
+    fp16; bf16 x becomes fp16 for ``"nf4"`` and ``"int4"``.  int4 codes are made by the caller.
     """
     torch = _torch()
     if quant_type not in MATVEC_TYPES:

@@ -16,7 +16,7 @@
 // A wave's part of x stays in registers from tile to tile (up to K = 4096), and the
 // next tiles' codes are in flight while a tile is computed.  The waves' sums meet in LDS.
 // Measured (one MI355X, a call among others): nf4 151936 x 2048, four tokens, fp32 out
-// 39.9 us = 4.4 TB/s of codes and scales; int4 28672 x 4096, one token 16.2 us = 3.8 TB/s; below
+// 39.8 us = 4.4 TB/s of codes and scales; int4 28672 x 4096, one token 16.2 us = 3.8 TB/s; below
 // some 10 MB launch and first reads set the time (2048 x 2048, one token: 4.9 us in a graph).
 //
 // Scales and zeros go through LDS too: read by the wave that uses them, a chunk's few
