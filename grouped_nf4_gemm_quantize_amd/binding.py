@@ -17,6 +17,7 @@ from typing import Optional
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnf4moe.so")
 
 F32, BF16, F16 = 0, 1, 2
+MXFP4 = 3  # NF4MOE_MXFP4, activations of grouped_gemm_mx4
 NOALLOC_SCRATCH_BYTES = 32 << 20  # NF4MOE_NOALLOC_SCRATCH_BYTES
 EPI_NONE, EPI_SWIGLU, EPI_SWIGLU_BWD = 0, 1, 2
 
@@ -133,6 +134,21 @@ _SIGNATURES = {
     "lora_orthogonalize_workspace": (_c_size, [_c_int, _c_int, _c_i64]),
     "lora_orthogonalize": (_c_int, [_c_vp, _c_int, _c_int, _c_int, _c_i64, _c_int, _c_int, _c_f64,
                                     _c_f64, _c_f64, _c_f64, _c_vp, _c_int, _c_vp, _c_size,
+                                    _c_vp]),
+    "mxfp4_quantize": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp,
+                                _c_vp]),
+    "mxfp4_dequantize": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_int, _c_vp]),
+    "grouped_mx4_gemm_workspace": (_c_size, [_c_i64, _c_i64, _c_int]),
+    "grouped_mx4_gemm": (_c_int, [_c_vp, _c_int, _c_vp, _c_i64, _c_vp, _c_int, _c_vp, _c_vp,
+                                  _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp,
+                                  _c_vp, _c_int, _c_i64, _c_vp, _c_size, _c_vp]),
+    "moe_dispatch": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_i64, _c_int, _c_i64, _c_i64, _c_vp,
+                              _c_int, _c_vp]),
+    "moe_combine": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_i64, _c_int, _c_i64, _c_i64, _c_vp,
+                             _c_int, _c_vp]),
+    "moe_combine_backward": (_c_int, [_c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_i64, _c_int,
+                                      _c_i64, _c_i64, _c_vp, _c_int, _c_vp, _c_vp]),
+    "moe_route_backward": (_c_int, [_c_vp, _c_vp, _c_vp, _c_i64, _c_int, _c_int, _c_int, _c_vp,
                                     _c_vp]),
 }
 
@@ -776,3 +792,186 @@ def lora_muon_step(tensors, lr: float, momentum: float = 0.95, nesterov: bool = 
     ws = _workspace(workspace, lib.lora_muon_step_workspace(arr, len(arr)), dev)
     _call(dev, lib.lora_muon_step, arr, len(arr), lr, momentum, int(bool(nesterov)), weight_decay,
           steps, *coeffs, eps, *_span(ws, dev))
+
+
+# ---- MXFP4 blocks and their product -------------------------------------------
+
+def quantize_mxfp4(x, transpose: bool = False, codes=None, scales=None):
+    """x [R, K] or [E, R, K] (fp32, bf16 or fp16) -> MXFP4 ``(codes, scales)``, uint8 (see
+    mxfp4_quantize in include/nf4moe.h).
+
+    Blocks of 32 run along K: codes [.., R, K/2], scales [.., R, K/32]; with ``transpose``
+    along R, for the transposed matrix: [.., K, R/2] and [.., K, R/32].
+    """
+    torch = _torch()
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [R, K] or [E, R, K]")
+    dev = x.device
+    R, K = x.shape[-2:]
+    E = x.shape[0] if x.dim() == 3 else 1
+    n, m = (K, R) if transpose else (R, K)  # rows and blocked length of the result
+    if m % 32:
+        raise ValueError(f"the blocked axis must be a multiple of 32, got {m}")
+    lead = x.shape[:-2]
+    if codes is None:
+        codes = torch.empty((*lead, n, m // 2), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty((*lead, n, m // 32), dtype=torch.uint8, device=dev)
+    _call(dev, load().mxfp4_quantize, _ptr(x), _dtype_code(x.dtype), E, R, K,
+          int(bool(transpose)), _need(codes, "codes", dev, (*lead, n, m // 2), torch.uint8),
+          _need(scales, "scales", dev, (*lead, n, m // 32), torch.uint8))
+    return codes, scales
+
+
+def dequantize_mxfp4(codes, scales, dtype=None, out=None):
+    """What MXFP4 ``codes`` [.., K/2] and ``scales`` [.., K/32] stand for, [.., K] of ``dtype``
+    (default bf16); see mxfp4_dequantize in include/nf4moe.h."""
+    torch = _torch()
+    dev = codes.device
+    K = codes.shape[-1] * 2
+    shape = (*codes.shape[:-1], K)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=dev)
+    _call(dev, load().mxfp4_dequantize, _need(codes, "codes", dev, None, torch.uint8),
+          _need(scales, "scales", dev, (*codes.shape[:-1], K // 32), torch.uint8),
+          codes.numel() * 2 // K if K else 0, K, _need(out, "out", dev, shape),
+          _dtype_code(out.dtype))
+    return out
+
+
+def grouped_gemm_mx4(a, a_scales, blocks, scales, offsets, P: int, gather=None,
+                     gather_div: int = 1, swiglu: bool = False, row_scale=None, scatter=None,
+                     out=None, out_dtype=None, out_rows: Optional[int] = None, workspace=None):
+    """Grouped product of two MXFP4 operands (see grouped_mx4_gemm in include/nf4moe.h).
+
+    ``a``, ``a_scales`` are what ``quantize_mxfp4`` returns for the activation rows, or ``a`` is
+    the rows themselves, [rows, K] fp32, bf16 or fp16, with ``a_scales`` None: quantised by the
+    call.  ``blocks`` [E, N, K/2] and ``scales`` [E, N, K/32] are the stack.  ``out`` is
+    [out_rows (P), N or N/2], bf16 by default.
+    """
+    torch = _torch()
+    dev = a.device
+    if a.dim() != 2 or blocks.dim() != 3:
+        raise ValueError("a must be [rows, K] (codes: K/2) and blocks [E, N, K/2]")
+    E, N, K2 = blocks.shape
+    K = K2 * 2
+    rows = a.shape[0]
+    lib = load()
+    if a_scales is None:
+        code = _dtype_code(a.dtype)
+        ap = _need(a, "a", dev, (rows, K))
+        ws = _workspace(workspace, lib.grouped_mx4_gemm_workspace(rows, K, code), dev)
+    else:
+        code, ws = MXFP4, None
+        ap = _need(a, "a", dev, (rows, K2), torch.uint8)
+    n_out = N // 2 if swiglu else N
+    if out is None:
+        out = torch.empty((P if out_rows is None else out_rows, n_out),
+                          dtype=out_dtype or torch.bfloat16, device=dev)
+    i32 = torch.int32
+    _call(dev, lib.grouped_mx4_gemm, ap, code,
+          None if a_scales is None else _need(a_scales, "a_scales", dev, (rows, K // 32),
+                                              torch.uint8),
+          rows, None if gather is None else _need(gather, "gather", dev, (P,), i32), gather_div,
+          _need(blocks, "blocks", dev, None, torch.uint8),
+          _need(scales, "scales", dev, (E, N, K // 32), torch.uint8),
+          _need(offsets, "offsets", dev, (E + 1,), i32), E, P, N, K,
+          EPI_SWIGLU if swiglu else EPI_NONE,
+          None if row_scale is None else _need(row_scale, "row_scale", dev, (P,), torch.float32),
+          None if scatter is None else _need(scatter, "scatter", dev, (P,), i32),
+          _need(out, "out", dev, (out.shape[0], n_out)), _dtype_code(out.dtype), out.shape[0],
+          *_span(ws, dev))
+    return out
+
+
+# ---- token rows into expert order and back --------------------------------------
+
+def _pairs(t, what: str, dev, T: int, k: int, dtype):
+    """A [T, k] or flat [T * k] tensor: its pointer."""
+    return _need(t, what, dev, (T, k) if t.dim() == 2 else (T * k,), dtype)
+
+
+def moe_dispatch(x, pair_pos, k: int, w=None, rows: Optional[int] = None, out=None,
+                 out_dtype=None):
+    """Token rows to their pairs' places: out[pair_pos[t*k + j]] = w[t, j] * x[t] (see
+    moe_dispatch in include/nf4moe.h).
+
+    ``pair_pos`` is int32 [T*k] or [T, k] (``route_permute``'s, or any placement; entries
+    outside [0, rows) are dropped), ``w`` fp32 of as many or None.  ``rows`` defaults to
+    T*k.  Rows that no pair names keep what ``out`` held.
+    """
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    dev = x.device
+    T, H = x.shape
+    if out is None:
+        out = torch.empty((T * k if rows is None else rows, H), dtype=out_dtype or x.dtype,
+                          device=dev)
+    R = out.shape[0]
+    _call(dev, load().moe_dispatch, _ptr(x), _dtype_code(x.dtype),
+          _pairs(pair_pos, "pair_pos", dev, T, k, torch.int32),
+          None if w is None else _pairs(w, "w", dev, T, k, torch.float32), T, k, R, H,
+          _need(out, "out", dev, (R, H)), _dtype_code(out.dtype))
+    return out
+
+
+def moe_combine(rows, pair_pos, k: int, w=None, y=None, y_dtype=None):
+    """The pairs' rows back into tokens: y[t] = sum_j w[t, j] * rows[pair_pos[t*k + j]] (see
+    moe_combine in include/nf4moe.h).  Without ``w`` it is the gradient of ``moe_dispatch``."""
+    torch = _torch()
+    if rows.dim() != 2 or k < 1 or pair_pos.numel() % k:
+        raise ValueError("rows must be [R, H] and pair_pos [T, k]")
+    dev = rows.device
+    R, H = rows.shape
+    T = pair_pos.numel() // k
+    if y is None:
+        y = torch.empty((T, H), dtype=y_dtype or rows.dtype, device=dev)
+    _call(dev, load().moe_combine, _ptr(rows), _dtype_code(rows.dtype),
+          _pairs(pair_pos, "pair_pos", dev, T, k, torch.int32),
+          None if w is None else _pairs(w, "w", dev, T, k, torch.float32), T, k, R, H,
+          _need(y, "y", dev, (T, H)), _dtype_code(y.dtype))
+    return y
+
+
+def moe_combine_backward(dy, rows, pair_pos, k: int, w=None, drows=None, drows_dtype=None,
+                         need_drows: bool = True):
+    """Gradients of ``moe_combine`` (see moe_combine_backward in include/nf4moe.h): returns
+    ``(drows, dw)``, dw fp32 [T, k].  ``drows`` may be ``rows``; without ``need_drows`` it is
+    not computed (None)."""
+    torch = _torch()
+    if dy.dim() != 2 or rows.dim() != 2:
+        raise ValueError("dy must be [T, H] and rows [R, H]")
+    dev = dy.device
+    T, H = dy.shape
+    R = rows.shape[0]
+    if not need_drows:
+        drows = None
+    elif drows is None:
+        drows = torch.empty((R, H), dtype=drows_dtype or rows.dtype, device=dev)
+    dw = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _call(dev, load().moe_combine_backward, _ptr(dy), _dtype_code(dy.dtype),
+          _need(rows, "rows", dev, (R, H)), _dtype_code(rows.dtype),
+          _pairs(pair_pos, "pair_pos", dev, T, k, torch.int32),
+          None if w is None else _pairs(w, "w", dev, T, k, torch.float32), T, k, R, H,
+          None if drows is None else _need(drows, "drows", dev, (R, H)),
+          F32 if drows is None else _dtype_code(drows.dtype), dw.data_ptr())
+    return drows, dw
+
+
+def moe_route_backward(logits, ids, dw, renormalize: bool = True, dlogits=None):
+    """Gradient of ``route_permute``'s weights for its logits (see moe_route_backward in
+    include/nf4moe.h): ``ids`` int32 and ``dw`` fp32 [T, k] -> fp32 [T, E]."""
+    torch = _torch()
+    if logits.dim() != 2 or ids.dim() != 2:
+        raise ValueError("logits must be [T, E] and ids [T, k]")
+    dev = logits.device
+    T, E = logits.shape
+    k = ids.shape[1]
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    _call(dev, load().moe_route_backward, _need(logits, "logits", dev, None, torch.float32),
+          _need(ids, "ids", dev, (T, k), torch.int32),
+          _need(dw, "dw", dev, (T, k), torch.float32), T, E, k, int(bool(renormalize)),
+          _need(dlogits, "dlogits", dev, (T, E), torch.float32))
+    return dlogits

@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libnf4moe.so")
 ARCH = "gfx950"
 
 SOURCES = ["quantize.hip", "route.hip", "gemm.hip", "gemm16.hip", "dgrad.hip", "lora.hip", "gemv.hip",
-           "noalloc.hip", "matvec.hip", "blocknorm.hip", "muon.hip", "abi.cpp"]
+           "noalloc.hip", "matvec.hip", "blocknorm.hip", "muon.hip", "mxfp4.hip",
+           "mxgemm.hip", "dispatch.hip", "abi.cpp"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -1631,4 +1631,287 @@ int lora_orthogonalize(const void* u, int u_dtype, int E, int r, int64_t n, int 
   return muon_run(m, workspace, ws_bytes, stream);
 }
 
+// ---- MXFP4 blocks and their product --------------------------------------
+
+int mxfp4_quantize(const void* x, int x_dtype, int64_t E, int64_t R, int64_t K, int transpose,
+                   uint8_t* codes, uint8_t* scales, void* stream) {
+  if (x == nullptr || codes == nullptr || scales == nullptr)
+    return fail(NF4MOE_EINVAL, "x, codes and scales must be non-null");
+  if (E < 1 || R < 1 || K < 1)
+    return fail(NF4MOE_EINVAL, "E, R, K must be positive (got %lld, %lld, %lld)", (long long)E,
+                (long long)R, (long long)K);
+  if (transpose != 0 && transpose != 1)
+    return fail(NF4MOE_EINVAL, "transpose must be 0 or 1");
+  if (!is_float_dtype(x_dtype)) return fail(NF4MOE_EDTYPE, "x_dtype=%d is unknown", x_dtype);
+  if ((transpose ? R : K) % 32)
+    return fail(NF4MOE_ESHAPE, "the blocked axis (%lld) is not a multiple of 32",
+                (long long)(transpose ? R : K));
+  if (E > kMxMaxElems || R > kMxMaxElems / E || K > kMxMaxElems / E / R)
+    return fail(NF4MOE_EOVERFLOW, "E*R*K is too large");
+  if (transpose && (E > 65535 || K > ((int64_t)1 << 31) || R > ((int64_t)1 << 22)))
+    return fail(NF4MOE_EOVERFLOW, "transposed: E up to 65535, R up to 2^22, K up to 2^31");
+  if (is_any(codes, {x, scales}) || scales == x)
+    return fail(NF4MOE_EINVAL, "codes and scales must not be x or each other");
+  if (!aligned(x, transpose ? dtype_bytes(x_dtype) : 16) || !aligned(codes, 16))
+    return fail(NF4MOE_EINVAL, "misaligned buffer (x and codes need 16 bytes; transposed, x its "
+                               "element)");
+  hipError_t err = launch_mx_quantize(x, x_dtype, E, R, K, transpose != 0, codes, scales,
+                                      (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "mxfp4 quantize launch");
+  return ok();
+}
+
+int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t K, void* out,
+                     int out_dtype, void* stream) {
+  if (codes == nullptr || scales == nullptr || out == nullptr)
+    return fail(NF4MOE_EINVAL, "codes, scales and out must be non-null");
+  if (R < 1 || K < 1)
+    return fail(NF4MOE_EINVAL, "R and K must be positive (got %lld, %lld)", (long long)R,
+                (long long)K);
+  if (!is_float_dtype(out_dtype)) return fail(NF4MOE_EDTYPE, "out_dtype=%d is unknown", out_dtype);
+  if (K % 32) return fail(NF4MOE_ESHAPE, "K=%lld is not a multiple of 32", (long long)K);
+  if (R > kMxMaxElems || K > kMxMaxElems / R) return fail(NF4MOE_EOVERFLOW, "R*K is too large");
+  if (is_any(out, {codes, scales}))
+    return fail(NF4MOE_EINVAL, "out must not be one of the inputs");
+  if (!aligned(codes, 16) || !aligned(out, 16))
+    return fail(NF4MOE_EINVAL, "misaligned buffer (codes and out need 16 bytes)");
+  hipError_t err = launch_mx_dequantize(codes, scales, R * K, out, out_dtype, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "mxfp4 dequantize launch");
+  return ok();
+}
+
+static size_t mx_codes_bytes(int64_t rows, int64_t K) {
+  return align_up((size_t)rows * (size_t)(K / 2), 256);
+}
+
+size_t grouped_mx4_gemm_workspace(int64_t a_rows, int64_t K, int a_dtype) {
+  if (a_rows < 1 || K < 32 || K % 32 || !is_float_dtype(a_dtype) ||
+      a_rows > (int64_t)UINT32_MAX / (K / 2))
+    return 0;
+  return mx_codes_bytes(a_rows, K) + align_up((size_t)a_rows * (size_t)(K / 32), 256);
+}
+
+int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_t a_rows,
+                     const int32_t* gather, int gather_div, const uint8_t* blocks,
+                     const uint8_t* scales, const int32_t* expert_offsets, int E, int64_t P,
+                     int64_t N, int64_t K, int epilogue, const float* row_scale,
+                     const int32_t* scatter, void* out, int out_dtype, int64_t out_rows,
+                     void* workspace, size_t ws_bytes, void* stream) {
+  if (E < 1 || E > NF4MOE_MAX_EXPERTS)
+    return fail(E < 1 ? NF4MOE_EINVAL : NF4MOE_ESHAPE, "E=%d outside [1, %d]", E,
+                NF4MOE_MAX_EXPERTS);
+  if (P < 0 || a_rows < 0 || out_rows < 0)
+    return fail(NF4MOE_EINVAL, "P, a_rows and out_rows must be >= 0");
+  if (N < 16 || K < 32) return fail(NF4MOE_EINVAL, "N >= 16 and K >= 32 required");
+  if (K % 32) return fail(NF4MOE_ESHAPE, "K=%lld is not a multiple of 32", (long long)K);
+  if (N % 16) return fail(NF4MOE_ESHAPE, "N=%lld is not a multiple of 16", (long long)N);
+  if (epilogue != NF4MOE_EPI_NONE && epilogue != NF4MOE_EPI_SWIGLU)
+    return fail(NF4MOE_EINVAL, "unknown epilogue %d", epilogue);
+  if (epilogue == NF4MOE_EPI_SWIGLU && N % 32)
+    return fail(NF4MOE_ESHAPE, "SwiGLU needs N=2I with I a multiple of 16 (N=%lld)", (long long)N);
+  if (a_dtype != NF4MOE_MXFP4 && !is_float_dtype(a_dtype))
+    return fail(NF4MOE_EDTYPE, "a_dtype=%d must be MXFP4, F32, BF16 or F16", a_dtype);
+  if (!is_float_dtype(out_dtype)) return fail(NF4MOE_EDTYPE, "out_dtype=%d is unknown", out_dtype);
+  if (gather != nullptr && gather_div < 1)
+    return fail(NF4MOE_EINVAL, "gather_div must be >= 1");
+  if (P >= INT32_MAX || a_rows >= INT32_MAX || out_rows >= INT32_MAX || N > INT32_MAX / 2 ||
+      K > INT32_MAX / 2)
+    return fail(NF4MOE_EOVERFLOW, "P, a_rows, out_rows, N or K too large for 32-bit indexing");
+  // the kernel addresses activations and one expert's weights with 32-bit byte offsets
+  if (a_rows > (int64_t)UINT32_MAX / (K / 2) || N > (int64_t)UINT32_MAX / (K / 2))
+    return fail(NF4MOE_EOVERFLOW, "the activations' codes or one expert's exceed 4 GiB");
+  if (P == 0) return ok();
+  if (a == nullptr || blocks == nullptr || scales == nullptr || expert_offsets == nullptr ||
+      out == nullptr || a_rows == 0 || out_rows == 0)
+    return fail(NF4MOE_EINVAL, "a, blocks, scales, expert_offsets and out must be non-null and "
+                               "have rows");
+  if ((a_dtype == NF4MOE_MXFP4) != (a_scales != nullptr))
+    return fail(NF4MOE_EINVAL, "a_scales are given exactly if a is MXFP4");
+  if (gather == nullptr && a_rows < P)
+    return fail(NF4MOE_EINVAL, "a has %lld rows, P is %lld", (long long)a_rows, (long long)P);
+  if (is_any(out, {a, a_scales, gather, blocks, scales, expert_offsets, row_scale, scatter}))
+    return fail(NF4MOE_EINVAL, "out must not be one of the inputs");
+  if (!aligned(a, 16) || !aligned(blocks, 16) || !aligned(out, 16) || !aligned(gather, 4) ||
+      !aligned(expert_offsets, 4) || !aligned(row_scale, 4) || !aligned(scatter, 4))
+    return fail(NF4MOE_EINVAL, "misaligned buffer (a, blocks and out need 16 bytes; gather, "
+                               "expert_offsets, row_scale and scatter 4)");
+  MxGemmArgs g{};
+  g.a = (const uint8_t*)a;
+  g.a_scales = a_scales;
+  if (a_dtype != NF4MOE_MXFP4) {
+    const size_t need = grouped_mx4_gemm_workspace(a_rows, K, a_dtype);
+    if (workspace == nullptr || ws_bytes < need)
+      return fail(NF4MOE_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                  workspace ? ws_bytes : (size_t)0);
+    if (!aligned(workspace, 256))
+      return fail(NF4MOE_EINVAL, "workspace must be 256-byte aligned");
+    if (is_any(workspace, {a, gather, blocks, scales, expert_offsets, row_scale, scatter, out}))
+      return fail(NF4MOE_EINVAL, "the workspace must not be another array of the call");
+  }
+  int cus = 0;
+  const int st = cu_count(&cus);
+  if (st != NF4MOE_OK) return st;
+  if (a_dtype != NF4MOE_MXFP4) {
+    uint8_t* codes = (uint8_t*)workspace;
+    uint8_t* sc = codes + mx_codes_bytes(a_rows, K);
+    hipError_t err = launch_mx_quantize(a, a_dtype, 1, a_rows, K, false, codes, sc,
+                                        (hipStream_t)stream);
+    if (err != hipSuccess) return hip_fail(err, "mxfp4 quantize launch");
+    g.a = codes;
+    g.a_scales = sc;
+  }
+  g.a_rows = a_rows;
+  g.gather = gather;
+  g.gather_div = gather_div;
+  g.blocks = blocks;
+  g.scales = scales;
+  g.offsets = expert_offsets;
+  g.E = E;
+  g.P = P;
+  g.N = (int)N;
+  g.K = (int)K;
+  g.swiglu = epilogue == NF4MOE_EPI_SWIGLU;
+  g.row_scale = row_scale;
+  g.scatter = scatter;
+  g.out_rows = out_rows;
+  g.out = out;
+  g.out_dtype = out_dtype;
+  hipError_t err = launch_mx_gemm(g, cus, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "mxfp4 product launch");
+  return ok();
+}
+
+// ---- token rows into expert rows and back ---------------------------------
+
+static int dispatch_shape_check(int64_t T, int k, int64_t R, int64_t H) {
+  if (T < 1) return fail(NF4MOE_EINVAL, "T=%lld must be >= 1", (long long)T);
+  if (k < 1 || k > NF4MOE_MAX_TOPK)
+    return fail(NF4MOE_ETOPK, "k=%d outside [1, %d]", k, NF4MOE_MAX_TOPK);
+  if (R < 0 || H < 1) return fail(NF4MOE_EINVAL, "R must be >= 0 and H positive");
+  if (H % 8) return fail(NF4MOE_ESHAPE, "H=%lld is not a multiple of 8", (long long)H);
+  if (T > (int64_t)INT32_MAX / k || R > INT32_MAX || H > ((int64_t)1 << 24))
+    return fail(NF4MOE_EOVERFLOW, "T*k, R or H is too large");
+  return NF4MOE_OK;
+}
+
+int moe_dispatch(const void* x, int x_dtype, const int32_t* pair_pos, const float* w, int64_t T,
+                 int k, int64_t R, int64_t H, void* rows, int rows_dtype, void* stream) {
+  int st = dispatch_shape_check(T, k, R, H);
+  if (st != NF4MOE_OK) return st;
+  if (x == nullptr || pair_pos == nullptr || (rows == nullptr && R > 0))
+    return fail(NF4MOE_EINVAL, "x, pair_pos and rows must be non-null");
+  if (!is_float_dtype(x_dtype) || !is_float_dtype(rows_dtype))
+    return fail(NF4MOE_EDTYPE, "unknown dtype (x %d, rows %d)", x_dtype, rows_dtype);
+  if (is_any(rows, {x, pair_pos, w}))
+    return fail(NF4MOE_EINVAL, "rows must not be one of the inputs");
+  if (!aligned(x, 16) || !aligned(rows, 16) || !aligned(pair_pos, 4) || !aligned(w, 4))
+    return fail(NF4MOE_EINVAL, "misaligned buffer (x and rows need 16 bytes, pair_pos and w 4)");
+  if (R == 0) return ok();
+  DispatchArgs a{};
+  a.x = x;
+  a.pos = pair_pos;
+  a.w = w;
+  a.out = rows;
+  a.T = T;
+  a.R = R;
+  a.k = k;
+  a.H = (int)H;
+  a.x_dtype = x_dtype;
+  a.out_dtype = rows_dtype;
+  hipError_t err = launch_dispatch(a, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "dispatch launch");
+  return ok();
+}
+
+int moe_combine(const void* rows, int rows_dtype, const int32_t* pair_pos, const float* w,
+                int64_t T, int k, int64_t R, int64_t H, void* y, int y_dtype, void* stream) {
+  int st = dispatch_shape_check(T, k, R, H);
+  if (st != NF4MOE_OK) return st;
+  if ((rows == nullptr && R > 0) || pair_pos == nullptr || y == nullptr)
+    return fail(NF4MOE_EINVAL, "rows, pair_pos and y must be non-null");
+  if (!is_float_dtype(rows_dtype) || !is_float_dtype(y_dtype))
+    return fail(NF4MOE_EDTYPE, "unknown dtype (rows %d, y %d)", rows_dtype, y_dtype);
+  if (is_any(y, {rows, pair_pos, w}))
+    return fail(NF4MOE_EINVAL, "y must not be one of the inputs");
+  if (!aligned(rows, 16) || !aligned(y, 16) || !aligned(pair_pos, 4) || !aligned(w, 4))
+    return fail(NF4MOE_EINVAL, "misaligned buffer (rows and y need 16 bytes, pair_pos and w 4)");
+  DispatchArgs a{};
+  a.x = rows;
+  a.pos = pair_pos;
+  a.w = w;
+  a.out = y;
+  a.T = T;
+  a.R = R;
+  a.k = k;
+  a.H = (int)H;
+  a.x_dtype = rows_dtype;
+  a.out_dtype = y_dtype;
+  hipError_t err = launch_combine_rows(a, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "combine launch");
+  return ok();
+}
+
+int moe_combine_backward(const void* dy, int dy_dtype, const void* rows, int rows_dtype,
+                         const int32_t* pair_pos, const float* w, int64_t T, int k, int64_t R,
+                         int64_t H, void* drows, int drows_dtype, float* dw, void* stream) {
+  int st = dispatch_shape_check(T, k, R, H);
+  if (st != NF4MOE_OK) return st;
+  if (dy == nullptr || (rows == nullptr && R > 0) || pair_pos == nullptr || dw == nullptr)
+    return fail(NF4MOE_EINVAL, "dy, rows, pair_pos and dw must be non-null");
+  if (!is_float_dtype(dy_dtype) || !is_float_dtype(rows_dtype) || !is_float_dtype(drows_dtype))
+    return fail(NF4MOE_EDTYPE, "unknown dtype (dy %d, rows %d, drows %d)", dy_dtype, rows_dtype,
+                drows_dtype);
+  if (is_any(drows, {dy, pair_pos, w, dw}) || (is_any(drows, {rows}) && drows_dtype != rows_dtype))
+    return fail(NF4MOE_EINVAL, "drows may be rows of the same type, and no other array of the call");
+  if (is_any(dw, {dy, rows, pair_pos, w}))
+    return fail(NF4MOE_EINVAL, "dw must not be one of the inputs");
+  if (!aligned(dy, 16) || !aligned(rows, 16) || !aligned(drows, 16) || !aligned(pair_pos, 4) ||
+      !aligned(w, 4) || !aligned(dw, 4))
+    return fail(NF4MOE_EINVAL, "misaligned buffer (dy, rows and drows need 16 bytes, pair_pos, w "
+                               "and dw 4)");
+  DispatchArgs a{};
+  a.x = dy;
+  a.rows = rows;
+  a.pos = pair_pos;
+  a.w = w;
+  a.out = drows;
+  a.dw = dw;
+  a.T = T;
+  a.R = R;
+  a.k = k;
+  a.H = (int)H;
+  a.x_dtype = dy_dtype;
+  a.rows_dtype = rows_dtype;
+  a.out_dtype = drows_dtype;
+  hipError_t err = launch_combine_bwd(a, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "combine backward launch");
+  return ok();
+}
+
+int moe_route_backward(const float* logits, const int32_t* topk_ids, const float* dw, int64_t T,
+                       int E, int k, int renormalize, float* dlogits, void* stream) {
+  if (logits == nullptr || topk_ids == nullptr || dw == nullptr || dlogits == nullptr)
+    return fail(NF4MOE_EINVAL, "logits, topk_ids, dw and dlogits must be non-null");
+  int st = check_route_shape(T, E, k);
+  if (st != NF4MOE_OK) return st;
+  if (renormalize != 0 && renormalize != 1)
+    return fail(NF4MOE_EINVAL, "renormalize must be 0 or 1");
+  if (is_any(dlogits, {logits, topk_ids, dw}))
+    return fail(NF4MOE_EINVAL, "dlogits must not be one of the inputs");
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(dw, 4) || !aligned(dlogits, 4))
+    return fail(NF4MOE_EINVAL, "misaligned buffer (each needs 4 bytes)");
+  RouteBwdArgs a{};
+  a.logits = logits;
+  a.ids = topk_ids;
+  a.dw = dw;
+  a.dlogits = dlogits;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.renormalize = renormalize;
+  hipError_t err = launch_route_bwd(a, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "route backward launch");
+  return ok();
+}
+
 }  // extern "C"

@@ -1,0 +1,226 @@
+// Token rows into the experts' rows and back, with the routing weights, and the
+// gradients (moe_dispatch, moe_combine, moe_combine_backward, moe_route_backward).
+// Pair p = t k + j has its row at pos[p]; one outside [0, R) has none.
+//   dispatch          rows[pos[p]] = w[p] x[t]
+//   combine           y[t] = sum_j w[p] rows[pos[p]], j ascending, fp32
+//   combine backward  drows[pos[p]] = w[p] dy[t],  dw[p] = <dy[t], rows[pos[p]]>
+//   route backward    weights over the k chosen:  dl[id_j] += w_j (dw_j - sum_i w_i dw_i)
+//                     weights of the softmax p over all:  dl[e] = p_e (g_e - sum_j p_j dw_j),
+//                     g_e the sum of dw_j with id_j = e
+//
+// All go by token, so that a token's row is read (or written) once for its k pairs.
+// Bound by memory.
+
+#include "common.h"
+#include "launch.h"
+#include "mfma_common.h"
+
+namespace nf4moe {
+
+namespace {
+
+// Eight consecutive elements at element index i.
+template <int kT>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+  if constexpr (kT == kF32) {
+    const f32x4* q = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p) + i);
+    const f32x4 a = q[0], b = q[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = a[j];
+      v[4 + j] = b[j];
+    }
+  } else {
+    unpack8<kT == kBF16>(
+        *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(p) + i), v);
+  }
+}
+
+__device__ __forceinline__ bool has_row(int32_t at, int64_t R) {
+  return at >= 0 && at < R;
+}
+
+}  // namespace
+
+// A workgroup takes `toks` tokens (one if a row has 256 chunks of eight or more).
+template <int kX, int kRows>
+__global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs g, int c8, int toks) {
+  const int tl = c8 < 256 ? threadIdx.x / c8 : 0;
+  const int c0 = threadIdx.x - tl * c8;
+  const int64_t t = (int64_t)blockIdx.x * toks + tl;
+  if (tl >= toks || t >= g.T) return;
+  const int32_t* pos = g.pos + t * g.k;
+  for (int c = c0; c < c8; c += 256) {
+    float v[8];
+    load8<kX>(g.x, t * g.H + c * 8, v);
+    for (int j = 0; j < g.k; ++j) {
+      const int32_t at = pos[j];
+      if (!has_row(at, g.R)) continue;
+      float o[8];
+      const float w = g.w ? g.w[t * g.k + j] : 1.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = g.w ? w * v[i] : v[i];
+      store8<kRows>(g.out, (int64_t)at * g.H + c * 8, o);
+    }
+  }
+}
+
+template <int kRows, int kY>
+__global__ __launch_bounds__(256) void combine_rows_kernel(DispatchArgs g, int c8, int toks) {
+  const int tl = c8 < 256 ? threadIdx.x / c8 : 0;
+  const int c0 = threadIdx.x - tl * c8;
+  const int64_t t = (int64_t)blockIdx.x * toks + tl;
+  if (tl >= toks || t >= g.T) return;
+  const int32_t* pos = g.pos + t * g.k;
+  for (int c = c0; c < c8; c += 256) {
+    float y[8] = {};
+    for (int j = 0; j < g.k; ++j) {
+      const int32_t at = pos[j];
+      if (!has_row(at, g.R)) continue;
+      float v[8];
+      load8<kRows>(g.x, (int64_t)at * g.H + c * 8, v);
+      const float w = g.w ? g.w[t * g.k + j] : 1.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] += w * v[i];
+    }
+    store8<kY>(g.out, t * g.H + c * 8, y);
+  }
+}
+
+// A workgroup takes one token; the pairs' products go eight pairs at a time.
+template <int kDy, int kRows, int kD>
+__global__ __launch_bounds__(256) void combine_bwd_kernel(DispatchArgs g, int c8) {
+  __shared__ float s_sum[4][8];
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t* pos = g.pos + t * g.k;
+  for (int j0 = 0; j0 < g.k; j0 += 8) {
+    float sum[8] = {};
+    for (int c = threadIdx.x; c < c8; c += 256) {
+      float dy[8];
+      load8<kDy>(g.x, t * g.H + c * 8, dy);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int32_t at = j0 + j < g.k ? pos[j0 + j] : -1;
+        if (!has_row(at, g.R)) continue;
+        const int64_t i0 = (int64_t)at * g.H + c * 8;
+        float v[8];
+        load8<kRows>(g.rows, i0, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[j] += dy[i] * v[i];
+        if (g.out) {
+          const float w = g.w ? g.w[t * g.k + j0 + j] : 1.f;
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = w * dy[i];
+          store8<kD>(g.out, i0, o);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float s = wave_sum(sum[j]);
+      if (lane == 0) s_sum[wave][j] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x < 8 && j0 + (int)threadIdx.x < g.k) {
+      const int j = threadIdx.x;
+      g.dw[t * g.k + j0 + j] = (s_sum[0][j] + s_sum[1][j]) + (s_sum[2][j] + s_sum[3][j]);
+    }
+    __syncthreads();
+  }
+}
+
+// A wave takes one token.
+template <bool kRenorm>
+__global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs g) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= g.T) return;
+  const float* l = g.logits + t * g.E;
+  int id = -1;
+  float dw = 0.f;
+  if (lane < g.k) {
+    id = g.ids[t * g.k + lane];
+    if (id < 0 || id >= g.E) id = -1;
+    if (id >= 0) dw = g.dw[t * g.k + lane];
+  }
+  const float mine = id >= 0 ? l[id] : -INFINITY;
+  float top = mine, all = 0.f;
+  if constexpr (!kRenorm) {
+    for (int e = lane; e < g.E; e += 64) top = fmaxf(top, l[e]);
+  }
+  top = wave_max(top);
+  const float ex = id >= 0 ? __expf(mine - top) : 0.f;
+  if constexpr (kRenorm) {
+    all = wave_sum(ex);
+  } else {
+    for (int e = lane; e < g.E; e += 64) all += __expf(l[e] - top);
+    all = wave_sum(all);
+  }
+  const float w = id >= 0 ? ex / all : 0.f;
+  const float mean = wave_sum(w * dw);
+  const float mine_g = kRenorm ? w * (dw - mean) : dw;
+  for (int e = lane; e - lane < g.E; e += 64) {
+    float v = 0.f;
+    for (int j = 0; j < g.k; ++j) {
+      const int ij = __builtin_amdgcn_readlane(id, j);
+      const float gj = lane_f(mine_g, j);
+      if (ij == e) v += gj;
+    }
+    if (e < g.E) {
+      if constexpr (!kRenorm) v = __expf(l[e] - top) / all * (v - mean);
+      g.dlogits[t * g.E + e] = v;
+    }
+  }
+}
+
+namespace {
+
+#define NF4MOE_BY_TYPE(dtype, T, ...)          \
+  if ((dtype) == kF32) {                       \
+    constexpr int T = kF32;                    \
+    __VA_ARGS__;                               \
+  } else if ((dtype) == kBF16) {               \
+    constexpr int T = kBF16;                   \
+    __VA_ARGS__;                               \
+  } else {                                     \
+    constexpr int T = kF16;                    \
+    __VA_ARGS__;                               \
+  }
+
+}  // namespace
+
+hipError_t launch_dispatch(const DispatchArgs& g, hipStream_t s) {
+  const int c8 = g.H / 8, toks = c8 < 256 ? 256 / c8 : 1;
+  const dim3 grid((unsigned)((g.T + toks - 1) / toks));
+  NF4MOE_BY_TYPE(g.x_dtype, kX, NF4MOE_BY_TYPE(g.out_dtype, kO,
+      hipLaunchKernelGGL((dispatch_kernel<kX, kO>), grid, dim3(256), 0, s, g, c8, toks)))
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_rows(const DispatchArgs& g, hipStream_t s) {
+  const int c8 = g.H / 8, toks = c8 < 256 ? 256 / c8 : 1;
+  const dim3 grid((unsigned)((g.T + toks - 1) / toks));
+  NF4MOE_BY_TYPE(g.x_dtype, kX, NF4MOE_BY_TYPE(g.out_dtype, kO,
+      hipLaunchKernelGGL((combine_rows_kernel<kX, kO>), grid, dim3(256), 0, s, g, c8, toks)))
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_bwd(const DispatchArgs& g, hipStream_t s) {
+  const dim3 grid((unsigned)g.T);
+  NF4MOE_BY_TYPE(g.x_dtype, kX, NF4MOE_BY_TYPE(g.rows_dtype, kR, NF4MOE_BY_TYPE(g.out_dtype, kO,
+      hipLaunchKernelGGL((combine_bwd_kernel<kX, kR, kO>), grid, dim3(256), 0, s, g, g.H / 8))))
+  return hipGetLastError();
+}
+
+hipError_t launch_route_bwd(const RouteBwdArgs& g, hipStream_t s) {
+  const dim3 grid((unsigned)((g.T + 3) / 4));
+  if (g.renormalize)
+    hipLaunchKernelGGL(route_bwd_kernel<true>, grid, dim3(256), 0, s, g);
+  else
+    hipLaunchKernelGGL(route_bwd_kernel<false>, grid, dim3(256), 0, s, g);
+  return hipGetLastError();
+}
+
+}  // namespace nf4moe

@@ -236,6 +236,60 @@ struct MatvecArgs {
 };
 hipError_t launch_matvec(const MatvecArgs& a, int num_cus, hipStream_t s);
 
+// ---- MXFP4 blocks and their product (mxfp4.hip, mxgemm.hip) -------------------
+constexpr int64_t kMxMaxElems = (int64_t)1 << 41;  // of one call: 2^30 workgroups of 2048
+hipError_t launch_mx_quantize(const void* x, int x_dtype, int64_t E, int64_t R, int64_t K,
+                              bool cols, uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, void* out,
+                                int out_dtype, hipStream_t s);
+
+struct MxGemmArgs {
+  const uint8_t* a;         // [a_rows, K / 2] codes
+  const uint8_t* a_scales;  // [a_rows, K / 32]
+  int64_t a_rows;
+  const int32_t* gather;    // nullable
+  int gather_div;
+  const uint8_t* blocks;    // [E, N, K / 2]
+  const uint8_t* scales;    // [E, N, K / 32]
+  const int32_t* offsets;   // [E + 1]
+  int E;
+  int64_t P;
+  int N, K;
+  int swiglu;
+  const float* row_scale;   // nullable
+  const int32_t* scatter;   // nullable
+  int64_t out_rows;
+  void* out;
+  int out_dtype;
+};
+hipError_t launch_mx_gemm(const MxGemmArgs& g, int num_cus, hipStream_t s);
+
+// ---- token rows into expert rows and back (dispatch.hip) ----------------------
+struct DispatchArgs {
+  const void* x;        // dispatch: token rows; combine: expert rows; backward: dy
+  const void* rows;     // backward: expert rows
+  const int32_t* pos;   // [T, k] row of each pair
+  const float* w;       // nullable [T, k]
+  void* out;            // dispatch: rows; combine: y; backward: drows (nullable)
+  float* dw;            // backward
+  int64_t T, R;         // tokens, expert rows
+  int k, H;
+  int x_dtype, rows_dtype, out_dtype;
+};
+hipError_t launch_dispatch(const DispatchArgs& g, hipStream_t s);
+hipError_t launch_combine_rows(const DispatchArgs& g, hipStream_t s);
+hipError_t launch_combine_bwd(const DispatchArgs& g, hipStream_t s);
+
+struct RouteBwdArgs {
+  const float* logits;
+  const int32_t* ids;
+  const float* dw;
+  float* dlogits;
+  int64_t T;
+  int E, k, renormalize;
+};
+hipError_t launch_route_bwd(const RouteBwdArgs& g, hipStream_t s);
+
 // ---- norms around a block (blocknorm.hip) -----------------------------------
 struct BlockNormArgs {
   const void* residual;  // forward: residual; backward: the stored r

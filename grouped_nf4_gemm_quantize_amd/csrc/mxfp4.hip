@@ -1,0 +1,232 @@
+// MXFP4 blocks made of 16- and 32-bit values and read back (mxfp4_quantize,
+// mxfp4_dequantize).  A block is 32 values along the contraction axis:
+//   e = max(floor(log2 max|x|) - 2, -127);  code = e2m1(x / 2^e), ties to even,
+//   beyond 6 saturated;  scale byte = e + 127, 255 (NaN) for a block with an
+//   infinity or a NaN.
+// floor(log2) is the exponent field of the largest magnitude; the division by a
+// power of two is exact and the conversion instructions do it and the rounding.
+//
+// Bound by memory: 2.53 bytes an element for bf16 one way, and the same back.
+
+#include "common.h"
+#include "launch.h"
+#include "mfma_common.h"
+
+namespace nf4moe {
+
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// The scale byte of a block whose largest magnitude has these fp32 bits (infinity
+// or NaN: 255), and the power of two the conversion divides by.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+  const uint32_t e = top >> 23;
+  return top >= 0x7f800000u ? 255u : e > 2u ? e - 2u : 0u;
+}
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __uint_as_float(byte == 0u ? 0x400000u : byte == 255u ? 0x3f800000u : byte << 23);
+}
+
+// fp32 bits of the magnitude of the larger element of a 16-bit pair's magnitudes.
+template <int kT>
+__device__ __forceinline__ uint32_t wide_bits(uint32_t mag16) {
+  if constexpr (kT == kBF16) return mag16 << 16;
+  else return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)mag16));
+}
+
+__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                __builtin_bit_cast(u16x2, b)));
+}
+
+// Two elements (one 16-bit word pair) to the codes of byte kSel of `old`.
+template <int kT, int kSel>
+__device__ __forceinline__ uint32_t cvt_pair(uint32_t old, uint32_t pair, float scale) {
+  if constexpr (kT == kBF16)
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2, pair), scale,
+                                                     kSel);
+  else
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, u32_as_half2(pair), scale, kSel);
+}
+
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+  return (uint32_t)dpp_i<kCtrl>((int)v);
+}
+
+// Eight consecutive values of a lane, four lanes a block.
+template <int kT>
+struct Eight {
+  u32x4 v[kT == kF32 ? 2 : 1];
+};
+
+template <int kT>
+__device__ __forceinline__ void load_eight(const void* x, int64_t i, Eight<kT>& o) {
+  const u32x4* p = reinterpret_cast<const u32x4*>(x) + i * (kT == kF32 ? 2 : 1);
+#pragma unroll
+  for (int j = 0; j < (kT == kF32 ? 2 : 1); ++j) o.v[j] = p[j];
+}
+
+template <int kT>
+__device__ __forceinline__ uint32_t eight_codes(const Eight<kT>& x, uint32_t& byte) {
+  uint32_t top;
+  if constexpr (kT == kF32) {
+    top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, x.v[j >> 2][j & 3] & 0x7fffffffu);
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = pk_max_u16(m, x.v[0][j] & 0x7fff7fffu);
+    top = max(m & 0xffffu, m >> 16);
+  }
+  top = max(top, dpp_u<kDppXor1>(top));
+  top = max(top, dpp_u<kDppXor2>(top));
+  if constexpr (kT != kF32) top = wide_bits<kT>(top);
+  byte = scale_byte(top);
+  const float s = scale_value(byte);
+  uint32_t c = 0;
+  if constexpr (kT == kF32) {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(x.v[0][0]), __uint_as_float(x.v[0][1]), s, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(x.v[0][2]), __uint_as_float(x.v[0][3]), s, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(x.v[1][0]), __uint_as_float(x.v[1][1]), s, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(x.v[1][2]), __uint_as_float(x.v[1][3]), s, 3);
+  } else {
+    c = cvt_pair<kT, 0>(c, x.v[0][0], s);
+    c = cvt_pair<kT, 1>(c, x.v[0][1], s);
+    c = cvt_pair<kT, 2>(c, x.v[0][2], s);
+    c = cvt_pair<kT, 3>(c, x.v[0][3], s);
+  }
+  return byte == 255u ? 0u : c;
+}
+
+// Blocks along the rows: the matrix is a flat run of blocks, eight values a lane.
+template <int kT>
+__global__ __launch_bounds__(256) void mx_quantize_kernel(const void* x, int64_t n8,
+                                                          uint32_t* codes, uint8_t* scales) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  // n8 is a multiple of 4, so the lanes of a block are in or out together
+  if (i >= n8) return;
+  Eight<kT> v;
+  load_eight<kT>(x, i, v);
+  uint32_t byte;
+  const uint32_t c = eight_codes<kT>(v, byte);
+  codes[i] = c;
+  if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+}
+
+// Blocks along the columns of [R, K]: a lane takes 32 rows of one column.
+template <int kT>
+__global__ __launch_bounds__(256) void mx_quantize_cols_kernel(const void* x, int64_t R, int64_t K,
+                                                               uint8_t* codes, uint8_t* scales) {
+  const int64_t col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  const int64_t rb = ((int64_t)blockIdx.y * 4 + (threadIdx.x >> 6)), blocks = R / 32;
+  if (col >= K || rb >= blocks) return;
+  const int64_t e = blockIdx.z;
+  const int64_t at = (e * R + rb * 32) * K + col;
+  uint32_t v[32];
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if constexpr (kT == kF32) v[j] = reinterpret_cast<const uint32_t*>(x)[at + j * K];
+    else v[j] = reinterpret_cast<const uint16_t*>(x)[at + j * K];
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) top = max(top, v[j] & (kT == kF32 ? 0x7fffffffu : 0x7fffu));
+  if constexpr (kT != kF32) top = wide_bits<kT>(top);
+  const uint32_t byte = scale_byte(top);
+  const float s = scale_value(byte);
+  u32x4 c;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w = 0;
+    if constexpr (kT == kF32) {
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, __uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1]), s, 0);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, __uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3]), s, 1);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, __uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5]), s, 2);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, __uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7]), s, 3);
+    } else {
+      w = cvt_pair<kT, 0>(w, v[8 * q] | v[8 * q + 1] << 16, s);
+      w = cvt_pair<kT, 1>(w, v[8 * q + 2] | v[8 * q + 3] << 16, s);
+      w = cvt_pair<kT, 2>(w, v[8 * q + 4] | v[8 * q + 5] << 16, s);
+      w = cvt_pair<kT, 3>(w, v[8 * q + 6] | v[8 * q + 7] << 16, s);
+    }
+    c[q] = byte == 255u ? 0u : w;
+  }
+  const int64_t ob = (e * K + col) * blocks + rb;
+  reinterpret_cast<u32x4*>(codes)[ob] = c;
+  scales[ob] = (uint8_t)byte;
+}
+
+template <int kSel>
+__device__ __forceinline__ void two_values(uint32_t c, float s, float* v) {
+  const f32x2 p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, kSel);
+  v[0] = p.x;
+  v[1] = p.y;
+}
+
+template <int kOut>
+__global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* codes,
+                                                            const uint8_t* scales, int64_t n8,
+                                                            void* out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;
+  const uint32_t c = codes[i];
+  const uint32_t byte = scales[i >> 2];
+  const float s = scale_value(byte);
+  float v[8];
+  two_values<0>(c, s, v);
+  two_values<1>(c, s, v + 2);
+  two_values<2>(c, s, v + 4);
+  two_values<3>(c, s, v + 6);
+  if (byte == 255u) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(0x7fc00000u);
+  }
+  store8<kOut>(out, i * 8, v);
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const void* x, int x_dtype, int64_t E, int64_t R, int64_t K,
+                              bool cols, uint8_t* codes, uint8_t* scales, hipStream_t s) {
+  if (!cols) {
+    const int64_t n8 = E * R * K / 8;
+    const dim3 grid((unsigned)((n8 + 255) / 256));
+    uint32_t* c = reinterpret_cast<uint32_t*>(codes);
+    if (x_dtype == kF32)
+      hipLaunchKernelGGL(mx_quantize_kernel<kF32>, grid, dim3(256), 0, s, x, n8, c, scales);
+    else if (x_dtype == kBF16)
+      hipLaunchKernelGGL(mx_quantize_kernel<kBF16>, grid, dim3(256), 0, s, x, n8, c, scales);
+    else
+      hipLaunchKernelGGL(mx_quantize_kernel<kF16>, grid, dim3(256), 0, s, x, n8, c, scales);
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)((K + 63) / 64), (unsigned)((R / 32 + 3) / 4), (unsigned)E);
+  if (x_dtype == kF32)
+    hipLaunchKernelGGL(mx_quantize_cols_kernel<kF32>, grid, dim3(256), 0, s, x, R, K, codes, scales);
+  else if (x_dtype == kBF16)
+    hipLaunchKernelGGL(mx_quantize_cols_kernel<kBF16>, grid, dim3(256), 0, s, x, R, K, codes, scales);
+  else
+    hipLaunchKernelGGL(mx_quantize_cols_kernel<kF16>, grid, dim3(256), 0, s, x, R, K, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, void* out,
+                                int out_dtype, hipStream_t s) {
+  const int64_t n8 = n / 8;
+  const dim3 grid((unsigned)((n8 + 255) / 256));
+  const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
+  if (out_dtype == kF32)
+    hipLaunchKernelGGL(mx_dequantize_kernel<kF32>, grid, dim3(256), 0, s, c, scales, n8, out);
+  else if (out_dtype == kBF16)
+    hipLaunchKernelGGL(mx_dequantize_kernel<kBF16>, grid, dim3(256), 0, s, c, scales, n8, out);
+  else
+    hipLaunchKernelGGL(mx_dequantize_kernel<kF16>, grid, dim3(256), 0, s, c, scales, n8, out);
+  return hipGetLastError();
+}
+
+}  // namespace nf4moe

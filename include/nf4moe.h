@@ -663,6 +663,109 @@ int lora_orthogonalize(const void* u, int u_dtype, int E, int r, int64_t n, int 
                        int ns_steps, double a, double b, double c, double ns_eps, void* out,
                        int out_dtype, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- MXFP4 blocks: quantised and read back ------------------------------------
+ * Blocks of 32 values along the contraction axis, as the OCP microscaling format has
+ * them:  e = max(floor(log2 max|x|) - 2, -127);  code = e2m1(x / 2^e), to nearest, ties to
+ * the even code, magnitudes beyond 6 saturated (the largest of a block lies in [4, 8) * 2^e);
+ * scale byte = e + 127.  A block of zeros has scale byte 0; one with an infinity or NaN has
+ * 255, which reads back as NaN everywhere.  Layout as the MXFP4 stacks above:
+ *   x [E, R, K]   F32, BF16 or F16;
+ *   transpose 0   blocks along K (a multiple of 32): codes [E, R, K/2], scales [E, R, K/32];
+ *   transpose 1   blocks along R (a multiple of 32, K any): codes [E, K, R/2], scales
+ *                 [E, K, R/32], the quantised transpose: with a stack [E, N, K] quantised so,
+ *                 grouped_mx4_gemm gives the input gradient dx = dy . W of its own product
+ *                 (dy quantised along N).
+ * The bytes are the same on every run and device.  Alignment (else EINVAL): x 16 bytes
+ * (transposed: its element), codes 16.  No output may be another array of the call.
+ * E*R*K at most 2^41; transposed E <= 65535, R <= 2^22, K <= 2^31 (EOVERFLOW). */
+int mxfp4_quantize(const void* x, int x_dtype, int64_t E, int64_t R, int64_t K, int transpose,
+                   uint8_t* codes, uint8_t* scales, void* stream);
+/* out [R, K] of out_dtype (F32, BF16 or F16) = e2m1 value * 2^(scale - 127), rounded once (fp16:
+ * beyond its range infinite); scale 255 is NaN.  codes [R, K/2], scales [R, K/32], K a multiple
+ * of 32; a stack is E*R rows.  codes and out 16-byte aligned, out no input (EINVAL). */
+int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t K, void* out,
+                     int out_dtype, void* stream);
+
+/* ---- grouped product of two MXFP4 operands -------------------------------------
+ * grouped_mxfp4_gemm with activations of 4 bits too, on the matrix unit's scaled 4-bit
+ * instructions (four times the rate of 16-bit ones):
+ *   out_row(i)[n] = sum over blocks b of 2^(sa[src(i), b] + s[e, n, b] - 254)
+ *                   * sum_{k in b} va[src(i), k] * v[e, n, k]
+ * for rows expert_offsets[e] <= i < expert_offsets[e+1].  Products and the sums inside a
+ * block are exact, the scaled blocks are added in fp32.
+ *   a [a_rows, .] NF4MOE_MXFP4: codes [a_rows, K/2] with a_scales [a_rows, K/32], as
+ *                 mxfp4_quantize writes them; F32, BF16 or F16: [a_rows, K], a_scales NULL,
+ *                 quantised by the call just so (into the workspace);
+ *   gather, gather_div   as for grouped_nf4_gemm: src(i) = gather[i] / gather_div.  An index
+ *                 outside [0, a_rows) reads some row of a, and no memory outside it;
+ *   blocks, scales   the stack [E, N, K/2], [E, N, K/32]; N a multiple of 16, K of 32 (ESHAPE);
+ *   expert_offsets   device int32 [E+1], non-decreasing from 0; rows at and beyond
+ *                 min(offsets[E], P) are not written;
+ *   epilogue      NF4MOE_EPI_NONE or _SWIGLU (N = 2I, I a multiple of 16: out has I columns);
+ *   row_scale     nullable fp32 [P], multiplies output row i;
+ *   scatter       nullable int32 [P]: row i goes to row scatter[i] of out; rows outside
+ *                 [0, out_rows) are not written (as without scatter), two rows to one place give
+ *                 one or a mix of them;
+ *   out           [out_rows, N or I] F32, BF16 or F16; no input of the call (EINVAL);
+ *   workspace     grouped_mx4_gemm_workspace(a_rows, K, a_dtype) bytes, 256-byte aligned (NULL
+ *                 for MXFP4 activations).  Two calls must not share it while both run.
+ * Scale byte 255 on either side makes what it multiplies NaN: its row, or its column for the
+ * expert's rows.  The order of the sums depends on the sizes only: results are the same from
+ * call to call.  P = 0 does nothing.  Alignment (else EINVAL): a, blocks and out 16 bytes,
+ * scales 1, the others 4.  The codes of a, and of one expert, at most 4 GiB (EOVERFLOW).
+ * grouped_mx4_gemm_workspace returns 0 for MXFP4 and for invalid arguments. */
+#define NF4MOE_MXFP4 3 /* a_dtype of grouped_mx4_gemm only */
+size_t grouped_mx4_gemm_workspace(int64_t a_rows, int64_t K, int a_dtype);
+int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_t a_rows,
+                     const int32_t* gather, int gather_div, const uint8_t* blocks,
+                     const uint8_t* scales, const int32_t* expert_offsets, int E, int64_t P,
+                     int64_t N, int64_t K, int epilogue, const float* row_scale,
+                     const int32_t* scatter, void* out, int out_dtype, int64_t out_rows,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- token rows into expert order and back, with gradients ----------------------
+ * What moe_expert_forward does around its products, for callers that run their own between:
+ * pair p = t*k + j of token t has its row at pair_pos[p] (moe_route_permute's pair_pos, or any
+ * other placement: rows padded to tiles, pairs dropped over a capacity).  An entry outside
+ * [0, R) has no row: it is not dispatched, adds nothing to y and has dw = 0.  Rows that no pair
+ * names are left as they were.
+ *   moe_dispatch           rows[pair_pos[p]] = w[p] * x[t]
+ *   moe_combine            y[t] = sum_j w[p] * rows[pair_pos[p]], j ascending
+ *   moe_combine_backward   drows[pair_pos[p]] = w[p] * dy[t];  dw[p] = <dy[t], rows[pair_pos[p]]>
+ * The gradient of a dispatch is moe_combine of the rows' gradient with the same w, and with
+ * weights dw is moe_combine_backward's of (x, rows' gradient) with drows NULL.
+ *   x, y, dy [T, H], rows, drows [R, H]   each F32, BF16 or F16 (own types); H a multiple of
+ *                 8 (ESHAPE), at most 2^24; rows may be NULL for R = 0;
+ *   pair_pos      int32 [T, k]; two pairs must not name one row in moe_dispatch and for
+ *                 drows (it would hold one or a mix of theirs); 1 <= k <= NF4MOE_MAX_TOPK;
+ *   w             nullable fp32 [T, k]: 1;
+ *   dw            fp32 [T, k];  drows may be NULL, or rows itself (of one type; pairs must not
+ *                 share rows then).
+ * Products and sums are fp32, rounded once; a row's NaN reaches only its token.  No workspace, one
+ * launch, the same results from call to call.  Matrices 16-byte aligned, pair_pos, w and dw 4;
+ * no output may be another array of the call but drows = rows (EINVAL for equal pointers).
+ * T*k and R up to 2^31 - 1 (EOVERFLOW). */
+int moe_dispatch(const void* x, int x_dtype, const int32_t* pair_pos, const float* w, int64_t T,
+                 int k, int64_t R, int64_t H, void* rows, int rows_dtype, void* stream);
+int moe_combine(const void* rows, int rows_dtype, const int32_t* pair_pos, const float* w,
+                int64_t T, int k, int64_t R, int64_t H, void* y, int y_dtype, void* stream);
+int moe_combine_backward(const void* dy, int dy_dtype, const void* rows, int rows_dtype,
+                         const int32_t* pair_pos, const float* w, int64_t T, int k, int64_t R,
+                         int64_t H, void* drows, int drows_dtype, float* dw, void* stream);
+
+/* The gradient of moe_route_permute's weights for the router's logits: from dw [T, k] (fp32,
+ * dL/dtopk_w, as moe_combine_backward gives it),
+ *   renormalize 1   w = softmax over the k chosen logits:  dlogits[id_j] = w_j (dw_j -
+ *                   sum_i w_i dw_i), 0 elsewhere;
+ *   renormalize 0   w_j = p[id_j], p the softmax over all E:  dlogits[e] = p_e (g_e - sum_j
+ *                   p[id_j] dw_j), g_e = dw_j where id_j = e, else 0.
+ * The choice of the experts has no gradient.  logits and dlogits fp32 [T, E], topk_ids int32
+ * [T, k] (one outside [0, E) takes no part: as if dw were 0 and, renormalised, its logit -inf);
+ * a chosen expert's logit must be finite, others may be -inf.  dlogits is no input (EINVAL);
+ * sizes as for moe_route_permute, everything 4-byte aligned.  One launch, no workspace. */
+int moe_route_backward(const float* logits, const int32_t* topk_ids, const float* dw, int64_t T,
+                       int E, int k, int renormalize, float* dlogits, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -73,6 +73,8 @@ from .mxfp4 import (  # noqa: F401
     unpack_mx,
     pack_mx,
     dequantize_mxfp4,
+    quantize_mxfp4,
+    grouped_gemm_mx4,
     grouped_gemm_mxfp4,
     moe_forward_mxfp4,
 )
@@ -95,4 +97,4 @@ from .nbit8 import (  # noqa: F401
     dequantize_blockwise8,
 )
 from .matvec import matvec, matvec_weight  # noqa: F401
-from . import blocknorm, muon  # noqa: F401
+from . import blocknorm, dispatch, muon  # noqa: F401

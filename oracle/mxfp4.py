@@ -71,6 +71,50 @@ def dequantize_mxfp4(blocks: np.ndarray, scales: np.ndarray) -> np.ndarray:
     return vals * sc
 
 
+def quantize_mxfp4(x):
+    """x [..., K] -> (bytes [..., K/2], scales [..., K/32]) by the format's own rule: the
+    scale's exponent is the largest magnitude's less e2m1's largest (2), at least -127;
+    elements go to the nearest of the grid, ties to the even code, beyond it to its end.
+    A block with an infinity or a NaN has scale 255 and codes 0."""
+    x = np.asarray(x, dtype=np.float64)
+    b = x.reshape(*x.shape[:-1], -1, MX_BLOCK)
+    bad = ~np.isfinite(b).all(-1)
+    b = np.where(bad[..., None], 0.0, b)
+    top = np.abs(b).max(-1)
+    _, ex = np.frexp(top)  # top = m * 2**ex, m in [0.5, 1)
+    e = np.where(top > 0, np.maximum(ex - 1 - 2, -127), -127)
+    q = np.abs(np.ldexp(b, -e[..., None]))
+    grid = e2m1_value(np.arange(8))
+    d = np.abs(q[..., None] - grid)  # exact: few bits each
+    near = d == d.min(-1, keepdims=True)
+    odd = np.arange(8) % 2
+    code = np.argmin(np.where(near, odd, 2), -1)  # of two at a tie the even one
+    code = code | (np.signbit(b).astype(np.int64) << 3)
+    code = np.where(bad[..., None], 0, code).reshape(x.shape)
+    return pack_mx(code), np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def grouped_gemm_mx4(a_blocks, a_scales, blocks, scales, offsets, gather=None, gather_div=1,
+                     swiglu=False):
+    """Both operands MXFP4: ``grouped_gemm_mxfp4`` on the values the rows stand for.
+    Returns (out, the sum of the terms' magnitudes of each pre-activation)."""
+    a = dequantize_mxfp4(a_blocks, a_scales)
+    w = dequantize_mxfp4(blocks, scales)
+    offsets = np.asarray(offsets, dtype=np.int64)
+    P = int(offsets[-1])
+    src = np.arange(P) if gather is None else np.asarray(gather, dtype=np.int64)[:P] // gather_div
+    pre, mag = np.zeros((P, w.shape[1])), np.zeros((P, w.shape[1]))
+    for e in range(w.shape[0]):
+        at = slice(int(offsets[e]), int(offsets[e + 1]))
+        pre[at] = a[src[at]] @ w[e].T
+        mag[at] = np.abs(a[src[at]]) @ np.abs(w[e]).T
+    if not swiglu:
+        return pre, mag
+    z, u = np.split(pre, 2, axis=1)
+    with np.errstate(over="ignore"):
+        return z / (1.0 + np.exp(-z)) * u, (pre, mag)
+
+
 def grouped_gemm_mxfp4(a, blocks, scales, offsets, gather=None, gather_div=1,
                        swiglu=False, row_scale=None):
     """The grouped GEMM of ``oracle.moe.grouped_gemm`` on MXFP4 weights."""
