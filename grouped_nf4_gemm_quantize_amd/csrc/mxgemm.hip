@@ -29,6 +29,24 @@ __shared__ int32_t s_tiles[kMaxExperts + 1];
 __shared__ int32_t s_wsum[kWaves];
 __shared__ float s_part[kWaves][2][16][17];
 
+// Two values rounded to the nearest 16-bit ones.
+template <int kOut>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  if constexpr (kOut == kBF16) return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+  else return pack_half2((_Float16)a, (_Float16)b);
+}
+
+template <int kOut>
+__device__ __forceinline__ void store4(void* out, int64_t idx, const float (&v)[4]) {
+  if constexpr (kOut == kF32) {
+    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(out) + idx) = f32x4{v[0], v[1], v[2], v[3]};
+  } else {
+    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(out) + idx) =
+        u32x2{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3])};
+  }
+}
+
 __device__ __forceinline__ i32x8 codes8(u32x4 v) {
   return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
 }
@@ -117,6 +135,330 @@ __global__ __launch_bounds__(kThreads) void mx_small_kernel(MxGemmArgs g, int n_
   }
 }
 
+// ---- many rows: tiles through LDS ---------------------------------------------------
+
+namespace {
+
+// A tile: WM x WN waves, each MT x NT accumulator tiles of 32 x 32 (v_mfma_scale 32x32x64, the
+// weights first: a lane holds row lane & 31, columns 8 (j / 4) + 4 (lane / 32) + j % 4).
+template <int kWM, int kWN, int kMT, int kNT, int kRing, int kPerCu>
+struct Tile {
+  static constexpr int PER_CU = kPerCu;  // workgroups on a compute unit
+  static constexpr int WM = kWM, WN = kWN, MT = kMT, NT = kNT, RING = kRing;
+  static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
+  static constexpr int BM = WM * MT * 32, BN = WN * NT * 32;
+  static_assert(BM % (16 * WAVES) == 0 && BN % (16 * WAVES) == 0, "whole copies a wave");
+  static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;   // 128 codes of a row
+  static constexpr int A_DMA = BM / 16 / WAVES, B_DMA = BN / 16 / WAVES;  // copies of 1 KB a wave
+  static constexpr int S_GROUPS = (BM + BN) / 64;  // of 64 rows' scale words, a copy each
+  static constexpr int S_DMA = (S_GROUPS + WAVES - 1) / WAVES;  // a wave (the last group's twice)
+  static constexpr int SCALES = (BM + BN) * 4;
+};
+
+// With kSplit a row's scale bytes lie in two words: a stage has both.
+template <class T, bool kSplit>
+constexpr int stage_bytes = T::A_BYTES + T::B_BYTES + (kSplit ? 2 : 1) * T::SCALES;
+
+template <class T>
+struct Copies {
+  i32x4 a_rsrc, b_rsrc, sa_rsrc, sb_rsrc;
+  uint32_t a_off[T::A_DMA], b_off[T::B_DMA], s_off[T::S_DMA];
+};
+
+// Step kb into the stage at LDS address st.  Scales: the aligned word that holds the step's first
+// byte, and with kSplit the next one too.
+template <class T, bool kSplit>
+__device__ __forceinline__ void issue(const Copies<T>& c, int kb, uint32_t st, int wave) {
+#pragma unroll
+  for (int i = 0; i < T::A_DMA; ++i)
+    dma16(c.a_rsrc, c.a_off[i], (uint32_t)kb * 64u, st + (wave * T::A_DMA + i) * 1024);
+#pragma unroll
+  for (int i = 0; i < T::B_DMA; ++i)
+    dma16(c.b_rsrc, c.b_off[i], (uint32_t)kb * 64u,
+          st + T::A_BYTES + (wave * T::B_DMA + i) * 1024);
+#pragma unroll
+  for (int i = 0; i < T::S_DMA; ++i) {
+    // rows 64 g .. of the activations, then of the weights
+    const int g = min(wave * T::S_DMA + i, T::S_GROUPS - 1);
+    const i32x4 rsrc = g * 64 < T::BM ? c.sa_rsrc : c.sb_rsrc;
+    const uint32_t at = st + T::A_BYTES + T::B_BYTES + g * 256;
+    dma4(rsrc, c.s_off[i], (uint32_t)kb * 4u, at);
+    if constexpr (kSplit) dma4(rsrc, c.s_off[i], (uint32_t)kb * 4u + 4u, at + T::SCALES);
+  }
+}
+
+template <class T, bool kSplit>
+constexpr int copies_of_step = T::A_DMA + T::B_DMA + T::S_DMA * (kSplit ? 2 : 1);
+
+// The four scale bytes of a row's step, the two of this lane's blocks at bytes 0 and 2.
+template <class T, bool kSplit>
+__device__ __forceinline__ int scale_word(const char* st, int row, uint32_t shift, uint32_t mask,
+                                          uint32_t lane_shift) {
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(st + T::A_BYTES + T::B_BYTES) + row;
+  uint32_t v = p[0];
+  if constexpr (kSplit) v = __builtin_amdgcn_alignbyte(p[T::SCALES / 4], v, shift) & mask;
+  return (int)(v >> lane_shift);
+}
+
+template <class T>
+struct Frags {
+  u32x4 a[T::MT], b[T::NT];
+};
+
+template <class T, int M>
+__device__ __forceinline__ void load_frags(const char* st, uint32_t ro, uint32_t a_base,
+                                           uint32_t b_base, Frags<T>& f) {
+  if constexpr (M == 0) return;
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+    f.a[m] = *reinterpret_cast<const u32x4*>(st + a_base + m * 2048 + ro);
+#pragma unroll
+  for (int n = 0; n < T::NT; ++n)
+    f.b[n] = *reinterpret_cast<const u32x4*>(st + T::A_BYTES + b_base + n * 2048 + ro);
+}
+
+template <class T, int M, int kHalf>
+__device__ __forceinline__ void multiply(const Frags<T>& f, const int (&sa)[T::MT],
+                                         const int (&sb)[T::NT],
+                                         f32x16 (&acc)[M ? M : 1][T::NT]) {
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int n = 0; n < T::NT; ++n)
+      acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          codes8(f.b[n]), codes8(f.a[m]), acc[m][n], 4, 4, 2 * kHalf, sb[n], 2 * kHalf, sa[m]);
+}
+
+// Where a wave finds its operands in a stage, and its rows' scale bytes in their first words.
+template <class T>
+struct Place {
+  uint32_t ro[2], a_base, b_base;
+  int a_row, b_row;  // this lane's first row among the stage's scale words
+  uint32_t a_shift[T::MT], b_shift;
+  uint32_t last_mask, lane_shift;
+};
+
+// The k loop of a tile for a wave with M row tiles that hold rows.  Step kb goes to stage kb %
+// RING; the prologue issues RING steps.  The barrier of a step stands between its halves, where
+// every wave has read the stage: the copies of step kb + RING go there then, and the next
+// step's first half is read, which has to have landed.  Nothing past the last step is copied
+// (the prologue repeats the last where there are fewer).
+template <class T, int M, bool kSplit>
+__device__ __forceinline__ void kloop(const Copies<T>& c, const Place<T>& p, int nk,
+                                      const char* ring, uint32_t ring_at, int wave,
+                                      f32x16 (&acc)[M ? M : 1][T::NT]) {
+  constexpr int kStep = copies_of_step<T, kSplit>;
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int n = 0; n < T::NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[m][n][j] = 0.f;
+  wait_vm_barrier<(T::RING - 1) * kStep>();
+  Frags<T> f0, f1;
+  load_frags<T, M>(ring, p.ro[0], p.a_base, p.b_base, f0);
+  int at = 0;
+  for (int kb = 0; kb < nk; ++kb) {
+    const int nat = at == T::RING - 1 ? 0 : at + 1;
+    const char* st = ring + at * (stage_bytes<T, kSplit>);
+    const uint32_t mask = kSplit && kb == nk - 1 ? p.last_mask : ~0u;
+    int sa[T::MT], sb[T::NT];
+    if constexpr (M > 0) {
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        sa[m] = scale_word<T, kSplit>(st, p.a_row + m * 32, p.a_shift[m], mask, p.lane_shift);
+#pragma unroll
+      for (int n = 0; n < T::NT; ++n)
+        sb[n] = scale_word<T, kSplit>(st, p.b_row + n * 32, p.b_shift, mask, p.lane_shift);
+    }
+    load_frags<T, M>(st, p.ro[1], p.a_base, p.b_base, f1);
+    multiply<T, M, 0>(f0, sa, sb, acc);
+    if (kb + T::RING - 1 < nk) wait_vm_barrier<(T::RING - 2) * kStep>();
+    else wait_vm_barrier<0>();
+    if (kb + T::RING < nk) issue<T, kSplit>(c, kb + T::RING, ring_at + at * (stage_bytes<T, kSplit>), wave);
+    load_frags<T, M>(ring + nat * (stage_bytes<T, kSplit>), p.ro[0], p.a_base, p.b_base, f0);
+    multiply<T, M, 1>(f1, sa, sb, acc);
+    at = nat;
+  }
+}
+
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
+
+// The wave's rows of a tile, from its accumulators, to their places in out.
+template <class T, int M, bool kSwiglu, int kOut>
+__device__ __forceinline__ void store_tile(const MxGemmArgs& g, const int32_t* orow,
+                                           const float* rscale, int rows_valid, int col0, int wm,
+                                           int wn, int n32, int g2,
+                                           const f32x16 (&acc)[M][T::NT]) {
+  const int ncols = kSwiglu ? g.N >> 1 : g.N;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const int trow = (wm * T::MT + m) * 32 + n32;
+    if (trow >= rows_valid) continue;
+    const int64_t o = orow[trow];
+    if (o < 0 || o >= g.out_rows) continue;
+    const float rs = rscale[trow];
+    constexpr int NTO = kSwiglu ? T::NT / 2 : T::NT;
+#pragma unroll
+    for (int n = 0; n < NTO; ++n) {
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const int col = col0 + (wn * NTO + n) * 32 + 8 * jj + 4 * g2;
+        if (col >= ncols) continue;
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = 4 * jj + i;
+          if constexpr (kSwiglu) v[i] = silu_f(acc[m][n][j]) * acc[m][n + NTO][j] * rs;
+          else v[i] = acc[m][n][j] * rs;
+        }
+        store4<kOut>(g.out, o * ncols + col, v);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+template <class T, bool kSwiglu, int kOut, bool kSplit>
+__global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmArgs g, int n_tiles) {
+  __shared__ __attribute__((aligned(1024))) char ring[T::RING * (stage_bytes<T, kSplit>)];
+  __shared__ int32_t tiles[kMaxExperts + 1];
+  __shared__ int32_t wsum[T::WAVES];
+  __shared__ int32_t orow[2][T::BM];
+  __shared__ float rscale[2][T::BM];
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / T::WN, wn = wave % T::WN;
+  const int n32 = lane & 31, g2 = lane >> 5;
+  build_tile_table<T::THREADS, T::BM>(g.offsets, g.E, tiles, wsum, tid);
+
+  const int N = g.N, I = N >> 1, KB = g.K / 32;
+  const int nk = (KB + 3) / 4;
+  const uint32_t row_bytes = (uint32_t)KB * 16u;
+  Place<T> p;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) p.ro[h] = n32 * 64 + (((2 * h + g2) ^ ((n32 >> 2) & 3)) << 4);
+  p.a_base = (uint32_t)wm * T::MT * 2048;
+  p.b_base = (uint32_t)wn * T::NT * 2048;
+  p.a_row = wm * T::MT * 32 + n32;
+  p.b_row = T::BM + wn * T::NT * 32 + n32;
+  p.last_mask = KB % 4 ? (1u << (8 * (KB % 4))) - 1u : ~0u;
+  p.lane_shift = 8 * g2;
+  constexpr int kCols = kSwiglu ? T::BN / 2 : T::BN;  // output columns of a tile
+
+  // weight row of LDS row l, clamped to a valid one.  SwiGLU: of a wave's NT groups of 32 the
+  // first half are gate rows, the others the up rows of the same columns.
+  auto weight_row = [&](int l, int n_idx) -> int {
+    if constexpr (kSwiglu) {
+      constexpr int H = T::NT / 2;
+      const int w = l / (T::NT * 32), nt = (l >> 5) % T::NT, n = l & 31;
+      const int col = n_idx * kCols + (w * H + nt % H) * 32 + n;
+      return min(col, I - 1) + (nt >= H ? I : 0);
+    } else {
+      return min(n_idx * T::BN + l, N - 1);
+    }
+  };
+  // scales are read as aligned words: byte offsets from the array's start rounded down
+  auto scale_rsrc = [&](const uint8_t* p, int64_t bytes, uint32_t& skip) -> i32x4 {
+    skip = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3);
+    return make_rsrc(p - skip, ((uint32_t)bytes + skip + 3u) & ~3u);
+  };
+
+  Copies<T> c;
+  uint32_t a_skip, b_skip;
+  c.a_rsrc = make_rsrc(g.a, (uint32_t)g.a_rows * row_bytes);
+  c.sa_rsrc = scale_rsrc(g.a_scales, g.a_rows * KB, a_skip);
+  const int total_m = __builtin_amdgcn_readfirstlane(tiles[g.E]);
+  const int total = total_m * n_tiles;
+  const int G = gridDim.x;  // a multiple of 8
+  const int u = (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3);
+  const uint32_t ring_at = lds_addr(ring);
+  for (int r = 0;; ++r) {
+    const int tix = r * G + u;
+    if (tix >= total) break;
+    // groups of four row tiles, the row tile changing fastest
+    const int group = tix / (4 * n_tiles), in = tix - group * 4 * n_tiles;
+    const int gm = min(4, total_m - group * 4);
+    const int n_idx = in / gm, mt_global = group * 4 + (in - n_idx * gm);
+    int lo = 0, hi = g.E;  // tiles[lo] <= mt_global < tiles[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tiles[mid] <= mt_global) lo = mid; else hi = mid;
+    }
+    const int e = __builtin_amdgcn_readfirstlane(lo);
+    const int m_local = mt_global - __builtin_amdgcn_readfirstlane(tiles[e]);
+    const int row0 = __builtin_amdgcn_readfirstlane(g.offsets[e]) + m_local * T::BM;
+    const int end = min(__builtin_amdgcn_readfirstlane(g.offsets[e + 1]), (int)g.P);
+    const int rows_valid = min(T::BM, end - row0);
+    if (rows_valid <= 0) continue;  // behind P
+    const int mtv = max(0, min(T::MT, (rows_valid - wm * T::MT * 32 + 31) >> 5));
+
+    auto source = [&](int row) -> uint32_t {
+      const int idx = row0 + (row < rows_valid ? row : 0);
+      const int s = g.gather ? g.gather[idx] / g.gather_div : idx;
+      return (uint32_t)min(max(s, 0), (int)g.a_rows - 1);
+    };
+    const int64_t w_at = (int64_t)e * N;
+    c.b_rsrc = make_rsrc(g.blocks + w_at * row_bytes, (uint32_t)N * row_bytes);
+    c.sb_rsrc = scale_rsrc(g.scales + w_at * KB, (int64_t)N * KB, b_skip);
+#pragma unroll
+    for (int i = 0; i < T::A_DMA; ++i) {
+      const int row = (wave * T::A_DMA + i) * 16 + (lane >> 2);
+      c.a_off[i] = source(row) * row_bytes + (((lane & 3) ^ ((row >> 2) & 3)) << 4);
+    }
+#pragma unroll
+    for (int i = 0; i < T::B_DMA; ++i) {
+      const int l = (wave * T::B_DMA + i) * 16 + (lane >> 2);
+      c.b_off[i] = (uint32_t)weight_row(l, n_idx) * row_bytes +
+                   (((lane & 3) ^ ((l >> 2) & 3)) << 4);
+    }
+#pragma unroll
+    for (int i = 0; i < T::S_DMA; ++i) {
+      const int l = min(wave * T::S_DMA + i, T::S_GROUPS - 1) * 64 + lane;
+      c.s_off[i] = (l < T::BM ? source(l) * (uint32_t)KB + a_skip
+                              : (uint32_t)weight_row(l - T::BM, n_idx) * (uint32_t)KB + b_skip) & ~3u;
+    }
+    // where in its first word a row's scales begin; the same for all of a lane's weight rows
+    if constexpr (kSplit) {
+#pragma unroll
+      for (int m = 0; m < T::MT; ++m)
+        p.a_shift[m] = (source((wm * T::MT + m) * 32 + n32) * (uint32_t)KB + a_skip) & 3u;
+      p.b_shift = ((uint32_t)weight_row(wn * T::NT * 32 + n32, n_idx) * (uint32_t)KB + b_skip) & 3u;
+    }
+    const int par = r & 1;
+    for (int l = tid; l < T::BM; l += T::THREADS) {
+      const int row = row0 + (l < rows_valid ? l : 0);
+      orow[par][l] = g.scatter ? g.scatter[row] : row;
+      rscale[par][l] = g.row_scale ? g.row_scale[row] : 1.0f;
+    }
+
+    // every wave is done with the previous tile's ring
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < T::RING; ++i)
+      issue<T, kSplit>(c, min(i, nk - 1), ring_at + i * (stage_bytes<T, kSplit>), wave);
+    auto tile = [&](auto rows) {
+      constexpr int M = decltype(rows)::value;
+      f32x16 acc[M ? M : 1][T::NT];
+      kloop<T, M, kSplit>(c, p, nk, ring, ring_at, wave, acc);
+      if constexpr (M > 0)
+        store_tile<T, M, kSwiglu, kOut>(g, orow[par], rscale[par], rows_valid, n_idx * kCols, wm,
+                                        wn, n32, g2, acc);
+    };
+    if (mtv > T::MT / 2) tile(Const<T::MT>{});
+    else if (T::MT > 2 && mtv == 2) tile(Const<T::MT / 2>{});
+    else if (mtv == 1) tile(Const<1>{});
+    else tile(Const<0>{});
+  }
+  // no copy of the wave is left in flight when it ends
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
 namespace {
 
 template <bool kSwiglu>
@@ -129,9 +471,51 @@ void launch_small(const MxGemmArgs& g, dim3 grid, int n_tiles, hipStream_t s) {
     hipLaunchKernelGGL((mx_small_kernel<kSwiglu, kF16>), grid, dim3(kThreads), 0, s, g, n_tiles);
 }
 
+template <class T, bool kSwiglu, bool kSplit>
+void launch_tile(const MxGemmArgs& g, dim3 grid, int n_tiles, hipStream_t s) {
+  if (g.out_dtype == kF32)
+    hipLaunchKernelGGL((mx_tile_kernel<T, kSwiglu, kF32, kSplit>), grid, dim3(T::THREADS), 0, s, g, n_tiles);
+  else if (g.out_dtype == kBF16)
+    hipLaunchKernelGGL((mx_tile_kernel<T, kSwiglu, kBF16, kSplit>), grid, dim3(T::THREADS), 0, s, g, n_tiles);
+  else
+    hipLaunchKernelGGL((mx_tile_kernel<T, kSwiglu, kF16, kSplit>), grid, dim3(T::THREADS), 0, s, g, n_tiles);
+}
+
+template <class T>
+void launch_tiles(const MxGemmArgs& g, int num_cus, hipStream_t s) {
+  const int cols = g.swiglu ? T::BN / 2 : T::BN;
+  const int n_tiles = ((g.swiglu ? g.N / 2 : g.N) + cols - 1) / cols;
+  const int64_t tiles = ((g.P + T::BM - 1) / T::BM + std::min<int64_t>(g.E, g.P)) * n_tiles;
+  const dim3 grid((unsigned)((std::min<int64_t>(tiles, num_cus * T::PER_CU) + 7) / 8 * 8));
+  const bool split = g.K % 128 || (reinterpret_cast<uintptr_t>(g.a_scales) & 3) ||
+                     (reinterpret_cast<uintptr_t>(g.scales) & 3);
+  if (g.swiglu) {
+    if (split) launch_tile<T, true, true>(g, grid, n_tiles, s);
+    else launch_tile<T, true, false>(g, grid, n_tiles, s);
+  } else {
+    if (split) launch_tile<T, false, true>(g, grid, n_tiles, s);
+    else launch_tile<T, false, false>(g, grid, n_tiles, s);
+  }
+}
+
+#ifndef TILE_BIG
+#define TILE_BIG 4, 2, 2, 4, 4, 1
+#endif
+using Tile256 = Tile<TILE_BIG>;  // 256 x 256
+using Tile64 = Tile<1, 4, 2, 2, 3, 2>;   // 64 x 256
+
 }  // namespace
 
 hipError_t launch_mx_gemm(const MxGemmArgs& g, int num_cus, hipStream_t s) {
+  const int64_t rows = g.P / std::min<int64_t>(g.E, g.P);  // of an expert, at least
+  if (rows >= 128) {
+    launch_tiles<Tile256>(g, num_cus, s);
+    return hipGetLastError();
+  }
+  if (rows >= 24) {
+    launch_tiles<Tile64>(g, num_cus, s);
+    return hipGetLastError();
+  }
   const int n_tiles = g.swiglu ? (g.N / 2 + 15) / 16 : (g.N + 31) / 32;
   // an expert's rows begin a tile of their own: at most one more for each that has rows
   const int64_t tiles = ((g.P + 15) / 16 + std::min<int64_t>(g.E, g.P)) * n_tiles;
