@@ -141,23 +141,24 @@ namespace {
 
 // A tile: WM x WN waves, each MT x NT accumulator tiles of 32 x 32 (v_mfma_scale 32x32x64, the
 // weights first: a lane holds row lane & 31, columns 8 (j / 4) + 4 (lane / 32) + j % 4).
-template <int kWM, int kWN, int kMT, int kNT, int kRing, int kPerCu>
+#ifndef FENCE
+#define FENCE __builtin_amdgcn_sched_barrier(0)
+#endif
+template <int kWM, int kWN, int kMT, int kNT, int kPerCu>
 struct Tile {
   static constexpr int PER_CU = kPerCu;  // workgroups on a compute unit
-  static constexpr int WM = kWM, WN = kWN, MT = kMT, NT = kNT, RING = kRing;
+  static constexpr int WM = kWM, WN = kWN, MT = kMT, NT = kNT;
   static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
   static constexpr int BM = WM * MT * 32, BN = WN * NT * 32;
-  static_assert(BM % (16 * WAVES) == 0 && BN % (16 * WAVES) == 0, "whole copies a wave");
-  static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;   // 128 codes of a row
-  static constexpr int A_DMA = BM / 16 / WAVES, B_DMA = BN / 16 / WAVES;  // copies of 1 KB a wave
-  static constexpr int S_GROUPS = (BM + BN) / 64;  // of 64 rows' scale words, a copy each
+  static constexpr int A_DMA = BM / 8 / WAVES, B_DMA = BN / 8 / WAVES;  // copies of 8 rows a wave
+  static constexpr int S_GROUPS = (BM + BN) / 64;  // of 64 rows' scales, a copy each
   static constexpr int S_DMA = (S_GROUPS + WAVES - 1) / WAVES;  // a wave (the last group's twice)
-  static constexpr int SCALES = (BM + BN) * 4;
+  static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "whole copies a wave");
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;  // 256 codes of a row
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int WINDOW = (BM + BN) * 16;  // 16 scale bytes of a row
+  static constexpr int LDS = 2 * (STAGE + WINDOW);
 };
-
-// With kSplit a row's scale bytes lie in two words: a stage has both.
-template <class T, bool kSplit>
-constexpr int stage_bytes = T::A_BYTES + T::B_BYTES + (kSplit ? 2 : 1) * T::SCALES;
 
 template <class T>
 struct Copies {
@@ -165,39 +166,65 @@ struct Copies {
   uint32_t a_off[T::A_DMA], b_off[T::B_DMA], s_off[T::S_DMA];
 };
 
-// Step kb into the stage at LDS address st.  Scales: the aligned word that holds the step's first
-// byte, and with kSplit the next one too.
-template <class T, bool kSplit>
-__device__ __forceinline__ void issue(const Copies<T>& c, int kb, uint32_t st, int wave) {
-#pragma unroll
-  for (int i = 0; i < T::A_DMA; ++i)
-    dma16(c.a_rsrc, c.a_off[i], (uint32_t)kb * 64u, st + (wave * T::A_DMA + i) * 1024);
-#pragma unroll
-  for (int i = 0; i < T::B_DMA; ++i)
-    dma16(c.b_rsrc, c.b_off[i], (uint32_t)kb * 64u,
-          st + T::A_BYTES + (wave * T::B_DMA + i) * 1024);
+// dma16 for the lanes of `due`, all or none (every lane of the wave is at work here).
+__device__ __forceinline__ void dma16_if(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds,
+                                         uint32_t due) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\t"
+               "s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds\n\ts_mov_b64 exec, -1"
+               :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds), "s"(due) : "memory", "m0");
+}
+
+// Copy j of a wave's A_DMA + B_DMA of step kb, to the stage at LDS address st.
+template <class T>
+__device__ __forceinline__ void issue_one(const Copies<T>& c, int j, int kb, uint32_t st, int wave,
+                                          uint32_t due) {
+  if (j < T::A_DMA)
+    dma16_if(c.a_rsrc, c.a_off[j], (uint32_t)kb * 128u, st + (wave * T::A_DMA + j) * 1024,
+             due);
+  else
+    dma16_if(c.b_rsrc, c.b_off[j - T::A_DMA], (uint32_t)kb * 128u,
+          st + T::A_BYTES + (wave * T::B_DMA + j - T::A_DMA) * 1024, due);
+}
+
+// The scales of step kb on (kPerStep bytes of the row a step): 16 bytes from the aligned word
+// that holds the first.
+template <class T>
+__device__ __forceinline__ void issue_scales(const Copies<T>& c, int kb, uint32_t window, int wave,
+                                             uint32_t due) {
 #pragma unroll
   for (int i = 0; i < T::S_DMA; ++i) {
     // rows 64 g .. of the activations, then of the weights
     const int g = min(wave * T::S_DMA + i, T::S_GROUPS - 1);
-    const i32x4 rsrc = g * 64 < T::BM ? c.sa_rsrc : c.sb_rsrc;
-    const uint32_t at = st + T::A_BYTES + T::B_BYTES + g * 256;
-    dma4(rsrc, c.s_off[i], (uint32_t)kb * 4u, at);
-    if constexpr (kSplit) dma4(rsrc, c.s_off[i], (uint32_t)kb * 4u + 4u, at + T::SCALES);
+    dma16_if(g * 64 < T::BM ? c.sa_rsrc : c.sb_rsrc, c.s_off[i], (uint32_t)kb * 8u,
+             window + g * 1024, due);
   }
 }
 
-template <class T, bool kSplit>
-constexpr int copies_of_step = T::A_DMA + T::B_DMA + T::S_DMA * (kSplit ? 2 : 1);
+// Where a wave finds its operands in a stage, and its rows' scale bytes in their windows.
+template <class T>
+struct Place {
+  uint32_t ro[4], a_base, b_base;
+  int a_row, b_row;  // this lane's first row among the stage's rows
+  uint32_t a_shift[T::MT], b_shift;
+  uint32_t mask[2];  // of the last step's halves: scale bytes inside the row
+  uint32_t lane_shift;
+};
 
-// The four scale bytes of a row's step, the two of this lane's blocks at bytes 0 and 2.
+// The scale bytes of a row's step, four a half; the two of this lane's blocks at bytes 0 and 2.
 template <class T, bool kSplit>
-__device__ __forceinline__ int scale_word(const char* st, int row, uint32_t shift, uint32_t mask,
-                                          uint32_t lane_shift) {
-  const uint32_t* p = reinterpret_cast<const uint32_t*>(st + T::A_BYTES + T::B_BYTES) + row;
-  uint32_t v = p[0];
-  if constexpr (kSplit) v = __builtin_amdgcn_alignbyte(p[T::SCALES / 4], v, shift) & mask;
-  return (int)(v >> lane_shift);
+__device__ __forceinline__ void scale_words(const char* window, int row, int odd, uint32_t shift,
+                                            const uint32_t (&mask)[2], uint32_t lane_shift,
+                                            int (&v)[2]) {
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(window) + row * 4;
+  u32x2 w;
+  if constexpr (kSplit) {
+    const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+    w = u32x2{__builtin_amdgcn_alignbyte(x.y, x.x, shift), __builtin_amdgcn_alignbyte(x.z, x.y, shift)};
+  } else {
+    w = *reinterpret_cast<const u32x2*>(p + odd * 2);
+  }
+  v[0] = (int)((w.x & mask[0]) >> lane_shift);
+  v[1] = (int)((w.y & mask[1]) >> lane_shift);
 }
 
 template <class T>
@@ -206,79 +233,96 @@ struct Frags {
 };
 
 template <class T, int M>
-__device__ __forceinline__ void load_frags(const char* st, uint32_t ro, uint32_t a_base,
-                                           uint32_t b_base, Frags<T>& f) {
+__device__ __forceinline__ void load_frags(const char* st, uint32_t ro, const Place<T>& p,
+                                           Frags<T>& f) {
   if constexpr (M == 0) return;
 #pragma unroll
   for (int m = 0; m < M; ++m)
-    f.a[m] = *reinterpret_cast<const u32x4*>(st + a_base + m * 2048 + ro);
+    f.a[m] = *reinterpret_cast<const u32x4*>(st + p.a_base + m * 4096 + ro);
 #pragma unroll
   for (int n = 0; n < T::NT; ++n)
-    f.b[n] = *reinterpret_cast<const u32x4*>(st + T::A_BYTES + b_base + n * 2048 + ro);
+    f.b[n] = *reinterpret_cast<const u32x4*>(st + T::A_BYTES + p.b_base + n * 4096 + ro);
 }
 
-template <class T, int M, int kHalf>
-__device__ __forceinline__ void multiply(const Frags<T>& f, const int (&sa)[T::MT],
-                                         const int (&sb)[T::NT],
-                                         f32x16 (&acc)[M ? M : 1][T::NT]) {
+// A quarter of a step; `between(m)` runs after each row tile's instructions.
+template <class T, int M, int kQuarter, class F>
+__device__ __forceinline__ void multiply(const Frags<T>& f, const int (&sa)[T::MT][2],
+                                         const int (&sb)[T::NT][2],
+                                         f32x16 (&acc)[M ? M : 1][T::NT], F between) {
+  constexpr int kHalf = kQuarter / 2, kSel = kQuarter % 2 * 2;
 #pragma unroll
-  for (int m = 0; m < M; ++m)
+  for (int m = 0; m < T::MT; ++m) {
+    if constexpr (M > 0) {
+      if (m < M) {
 #pragma unroll
-    for (int n = 0; n < T::NT; ++n)
-      acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          codes8(f.b[n]), codes8(f.a[m]), acc[m][n], 4, 4, 2 * kHalf, sb[n], 2 * kHalf, sa[m]);
+        for (int n = 0; n < T::NT; ++n)
+          acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              codes8(f.b[n]), codes8(f.a[m]), acc[m][n], 4, 4, kSel, sb[n][kHalf], kSel,
+              sa[m][kHalf]);
+      }
+    }
+    between(m);
+  }
 }
 
-// Where a wave finds its operands in a stage, and its rows' scale bytes in their first words.
-template <class T>
-struct Place {
-  uint32_t ro[2], a_base, b_base;
-  int a_row, b_row;  // this lane's first row among the stage's scale words
-  uint32_t a_shift[T::MT], b_shift;
-  uint32_t last_mask, lane_shift;
-};
-
-// The k loop of a tile for a wave with M row tiles that hold rows.  Step kb goes to stage kb %
-// RING; the prologue issues RING steps.  The barrier of a step stands between its halves, where
-// every wave has read the stage: the copies of step kb + RING go there then, and the next
-// step's first half is read, which has to have landed.  Nothing past the last step is copied
-// (the prologue repeats the last where there are fewer).
+// The k loop of a tile for a wave with M row tiles that hold rows.  Step kb (256 of K: whole
+// 128-byte lines of the codes' rows) is in stage kb % 2, the scales of one step (kSplit) or two in
+// a window of their own.  The barrier of a step stands before its last quarter, where every wave
+// has read the stage: the copies of step kb + 2 go there then, among the quarter's products.  A
+// copy that is not due is issued for no lane: with a branch in its place the products of
+// the whole step were moved behind the barrier.
 template <class T, int M, bool kSplit>
 __device__ __forceinline__ void kloop(const Copies<T>& c, const Place<T>& p, int nk,
                                       const char* ring, uint32_t ring_at, int wave,
                                       f32x16 (&acc)[M ? M : 1][T::NT]) {
-  constexpr int kStep = copies_of_step<T, kSplit>;
 #pragma unroll
   for (int m = 0; m < M; ++m)
 #pragma unroll
     for (int n = 0; n < T::NT; ++n)
 #pragma unroll
       for (int j = 0; j < 16; ++j) acc[m][n][j] = 0.f;
-  wait_vm_barrier<(T::RING - 1) * kStep>();
+  wait_vm_barrier<T::A_DMA + T::B_DMA>();  // all but step 1's codes landed
   Frags<T> f0, f1;
-  load_frags<T, M>(ring, p.ro[0], p.a_base, p.b_base, f0);
-  int at = 0;
+  load_frags<T, M>(ring, p.ro[0], p, f0);
+  const auto nothing = [](int) {};
   for (int kb = 0; kb < nk; ++kb) {
-    const int nat = at == T::RING - 1 ? 0 : at + 1;
-    const char* st = ring + at * (stage_bytes<T, kSplit>);
-    const uint32_t mask = kSplit && kb == nk - 1 ? p.last_mask : ~0u;
-    int sa[T::MT], sb[T::NT];
+    const int odd = kb & 1;
+    const char* st = ring + odd * T::STAGE;
+    const int slot = kSplit ? odd : (kb >> 1) & 1;
+    const char* win = ring + 2 * T::STAGE + slot * T::WINDOW;
+    int sa[T::MT][2], sb[T::NT][2];
     if constexpr (M > 0) {
+      const uint32_t mask[2] = {kb == nk - 1 ? p.mask[0] : ~0u, kb == nk - 1 ? p.mask[1] : ~0u};
 #pragma unroll
       for (int m = 0; m < M; ++m)
-        sa[m] = scale_word<T, kSplit>(st, p.a_row + m * 32, p.a_shift[m], mask, p.lane_shift);
+        scale_words<T, kSplit>(win, p.a_row + m * 32, odd, p.a_shift[m], mask, p.lane_shift, sa[m]);
 #pragma unroll
       for (int n = 0; n < T::NT; ++n)
-        sb[n] = scale_word<T, kSplit>(st, p.b_row + n * 32, p.b_shift, mask, p.lane_shift);
+        scale_words<T, kSplit>(win, p.b_row + n * 32, odd, p.b_shift, mask, p.lane_shift, sb[n]);
     }
-    load_frags<T, M>(st, p.ro[1], p.a_base, p.b_base, f1);
-    multiply<T, M, 0>(f0, sa, sb, acc);
-    if (kb + T::RING - 1 < nk) wait_vm_barrier<(T::RING - 2) * kStep>();
-    else wait_vm_barrier<0>();
-    if (kb + T::RING < nk) issue<T, kSplit>(c, kb + T::RING, ring_at + at * (stage_bytes<T, kSplit>), wave);
-    load_frags<T, M>(ring + nat * (stage_bytes<T, kSplit>), p.ro[0], p.a_base, p.b_base, f0);
-    multiply<T, M, 1>(f1, sa, sb, acc);
-    at = nat;
+    load_frags<T, M>(st, p.ro[1], p, f1);
+    multiply<T, M, 0>(f0, sa, sb, acc, nothing);
+    FENCE;
+    load_frags<T, M>(st, p.ro[2], p, f0);
+    multiply<T, M, 1>(f1, sa, sb, acc, nothing);
+    FENCE;
+    load_frags<T, M>(st, p.ro[3], p, f1);
+    multiply<T, M, 2>(f0, sa, sb, acc, nothing);
+    FENCE;
+    wait_vm_barrier<0>();
+    FENCE;
+    load_frags<T, M>(ring + (odd ^ 1) * T::STAGE, p.ro[0], p, f0);
+    const int next = kb + 2;
+    const uint32_t due = __builtin_amdgcn_readfirstlane(next < nk ? ~0u : 0u);
+    issue_scales<T>(c, next, ring_at + 2 * T::STAGE + (kSplit ? slot : slot ^ 1) * T::WINDOW, wave,
+                    kSplit ? due : due & (uint32_t)(odd - 1));
+    multiply<T, M, 3>(f1, sa, sb, acc, [&](int m) {
+      constexpr int kAll = T::A_DMA + T::B_DMA, kPart = (kAll + T::MT - 1) / T::MT;
+#pragma unroll
+      for (int j = m * kPart; j < min((m + 1) * kPart, kAll); ++j)
+        issue_one<T>(c, j, next, ring_at + odd * T::STAGE, wave, due);
+    });
+    FENCE;
   }
 }
 
@@ -325,7 +369,7 @@ __device__ __forceinline__ void store_tile(const MxGemmArgs& g, const int32_t* o
 
 template <class T, bool kSwiglu, int kOut, bool kSplit>
 __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmArgs g, int n_tiles) {
-  __shared__ __attribute__((aligned(1024))) char ring[T::RING * (stage_bytes<T, kSplit>)];
+  __shared__ __attribute__((aligned(1024))) char ring[T::LDS];
   __shared__ int32_t tiles[kMaxExperts + 1];
   __shared__ int32_t wsum[T::WAVES];
   __shared__ int32_t orow[2][T::BM];
@@ -338,16 +382,20 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
   build_tile_table<T::THREADS, T::BM>(g.offsets, g.E, tiles, wsum, tid);
 
   const int N = g.N, I = N >> 1, KB = g.K / 32;
-  const int nk = (KB + 3) / 4;
+  const int nk = (KB + 7) / 8;
   const uint32_t row_bytes = (uint32_t)KB * 16u;
   Place<T> p;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) p.ro[h] = n32 * 64 + (((2 * h + g2) ^ ((n32 >> 2) & 3)) << 4);
-  p.a_base = (uint32_t)wm * T::MT * 2048;
-  p.b_base = (uint32_t)wn * T::NT * 2048;
+  for (int q = 0; q < 4; ++q) p.ro[q] = n32 * 128 + (((2 * q + g2) ^ (n32 & 7)) << 4);
+  p.a_base = (uint32_t)wm * T::MT * 4096;
+  p.b_base = (uint32_t)wn * T::NT * 4096;
   p.a_row = wm * T::MT * 32 + n32;
   p.b_row = T::BM + wn * T::NT * 32 + n32;
-  p.last_mask = KB % 4 ? (1u << (8 * (KB % 4))) - 1u : ~0u;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int inside = KB - (nk - 1) * 8 - 4 * h;  // scale bytes of the last step's half
+    p.mask[h] = inside >= 4 ? ~0u : inside > 0 ? (1u << (8 * inside)) - 1u : 0u;
+  }
   p.lane_shift = 8 * g2;
   constexpr int kCols = kSwiglu ? T::BN / 2 : T::BN;  // output columns of a tile
 
@@ -408,14 +456,13 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
     c.sb_rsrc = scale_rsrc(g.scales + w_at * KB, (int64_t)N * KB, b_skip);
 #pragma unroll
     for (int i = 0; i < T::A_DMA; ++i) {
-      const int row = (wave * T::A_DMA + i) * 16 + (lane >> 2);
-      c.a_off[i] = source(row) * row_bytes + (((lane & 3) ^ ((row >> 2) & 3)) << 4);
+      const int row = (wave * T::A_DMA + i) * 8 + (lane >> 3);
+      c.a_off[i] = source(row) * row_bytes + (((lane & 7) ^ (row & 7)) << 4);
     }
 #pragma unroll
     for (int i = 0; i < T::B_DMA; ++i) {
-      const int l = (wave * T::B_DMA + i) * 16 + (lane >> 2);
-      c.b_off[i] = (uint32_t)weight_row(l, n_idx) * row_bytes +
-                   (((lane & 3) ^ ((l >> 2) & 3)) << 4);
+      const int l = (wave * T::B_DMA + i) * 8 + (lane >> 3);
+      c.b_off[i] = (uint32_t)weight_row(l, n_idx) * row_bytes + (((lane & 7) ^ (l & 7)) << 4);
     }
 #pragma unroll
     for (int i = 0; i < T::S_DMA; ++i) {
@@ -439,9 +486,13 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
 
     // every wave is done with the previous tile's ring
     lds_barrier();
+    issue_scales<T>(c, 0, ring_at + 2 * T::STAGE, wave, ~0u);
+    if (kSplit) issue_scales<T>(c, min(1, nk - 1), ring_at + 2 * T::STAGE + T::WINDOW, wave, ~0u);
 #pragma unroll
-    for (int i = 0; i < T::RING; ++i)
-      issue<T, kSplit>(c, min(i, nk - 1), ring_at + i * (stage_bytes<T, kSplit>), wave);
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < T::A_DMA + T::B_DMA; ++j)
+        issue_one<T>(c, j, min(i, nk - 1), ring_at + i * T::STAGE, wave, ~0u);
     auto tile = [&](auto rows) {
       constexpr int M = decltype(rows)::value;
       f32x16 acc[M ? M : 1][T::NT];
@@ -499,10 +550,13 @@ void launch_tiles(const MxGemmArgs& g, int num_cus, hipStream_t s) {
 }
 
 #ifndef TILE_BIG
-#define TILE_BIG 4, 2, 2, 4, 4, 1
+#define TILE_BIG 4, 2, 2, 4, 1
 #endif
 using Tile256 = Tile<TILE_BIG>;  // 256 x 256
-using Tile64 = Tile<1, 4, 2, 2, 3, 2>;   // 64 x 256
+#ifndef TILE_SMALL
+#define TILE_SMALL 2, 2, 1, 2, 2
+#endif
+using Tile64 = Tile<TILE_SMALL>;
 
 }  // namespace
 
