@@ -1714,11 +1714,13 @@ int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_
   if (!is_float_dtype(out_dtype)) return fail(NF4MOE_EDTYPE, "out_dtype=%d is unknown", out_dtype);
   if (gather != nullptr && gather_div < 1)
     return fail(NF4MOE_EINVAL, "gather_div must be >= 1");
-  if (P >= INT32_MAX || a_rows >= INT32_MAX || out_rows >= INT32_MAX || N > INT32_MAX / 2 ||
+  if (P >= (1 << 30) || a_rows >= INT32_MAX || out_rows >= INT32_MAX || N > INT32_MAX / 2 ||
       K > INT32_MAX / 2)
     return fail(NF4MOE_EOVERFLOW, "P, a_rows, out_rows, N or K too large for 32-bit indexing");
-  // the kernel addresses activations and one expert's weights with 32-bit byte offsets
-  if (a_rows > (int64_t)UINT32_MAX / (K / 2) || N > (int64_t)UINT32_MAX / (K / 2))
+  // the kernel addresses activations and one expert's weights with 32-bit byte offsets, up to a
+  // tile's rows behind the end
+  if (a_rows + kMxTileRows > (int64_t)UINT32_MAX / (K / 2) ||
+      N + kMxTileRows > (int64_t)UINT32_MAX / (K / 2))
     return fail(NF4MOE_EOVERFLOW, "the activations' codes or one expert's exceed 4 GiB");
   if (P == 0) return ok();
   if (a == nullptr || blocks == nullptr || scales == nullptr || expert_offsets == nullptr ||

@@ -21,6 +21,11 @@ namespace nf4moe {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+#ifndef FENCE
+#define FENCE __builtin_amdgcn_sched_barrier(0)
+#endif
 
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
@@ -37,14 +42,39 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   else return pack_half2((_Float16)a, (_Float16)b);
 }
 
-template <int kOut>
-__device__ __forceinline__ void store4(void* out, int64_t idx, const float (&v)[4]) {
-  if constexpr (kOut == kF32) {
-    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(out) + idx) = f32x4{v[0], v[1], v[2], v[3]};
-  } else {
-    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(out) + idx) =
-        u32x2{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3])};
+// build_tile_table with the rows at and beyond P left out.
+template <int kThreads, int kBM>
+__device__ __forceinline__ void build_tiles(const int32_t* __restrict__ offsets, int E, int P,
+                                            int32_t* tiles, int32_t* wsum, int tid) {
+  constexpr int kPer = kMaxExperts / kThreads;
+  const int lane = tid & 63, wave = tid >> 6;
+  int32_t cnt[kPer];
+  int32_t local = 0;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int ex = tid * kPer + u;
+    cnt[u] = 0;
+    if (ex < E) cnt[u] = max(0, min(offsets[ex + 1], P) - min(offsets[ex], P) + kBM - 1) / kBM;
+    local += cnt[u];
   }
+  int32_t incl = local;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int32_t v = __shfl_up(incl, off, 64);
+    if (lane >= off) incl += v;
+  }
+  if (lane == 63) wsum[wave] = incl;
+  __syncthreads();
+  int32_t run = incl - local;
+  for (int w = 0; w < wave; ++w) run += wsum[w];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int ex = tid * kPer + u;
+    if (ex < E) tiles[ex] = run;
+    run += cnt[u];
+  }
+  if (tid == kThreads - 1) tiles[E] = run;
+  __syncthreads();
 }
 
 __device__ __forceinline__ i32x8 codes8(u32x4 v) {
@@ -59,7 +89,7 @@ template <bool kSwiglu, int kOut>
 __global__ __launch_bounds__(kThreads) void mx_small_kernel(MxGemmArgs g, int n_tiles) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r16 = lane & 15, q = lane >> 4;
-  build_tile_table<kThreads, 16>(g.offsets, g.E, s_tiles, s_wsum, tid);
+  build_tiles<kThreads, 16>(g.offsets, g.E, (int)g.P, s_tiles, s_wsum, tid);
   const int N = g.N, I = N >> 1, KB = g.K / 32;
   const int total = s_tiles[g.E] * n_tiles;
   for (int tix = blockIdx.x; tix < total; tix += gridDim.x) {
@@ -72,7 +102,6 @@ __global__ __launch_bounds__(kThreads) void mx_small_kernel(MxGemmArgs g, int n_
     const int e = lo;
     const int row0 = g.offsets[e] + (mt - s_tiles[e]) * 16;
     const int rows = min(16, min(g.offsets[e + 1], (int)g.P) - row0);
-    if (rows <= 0) continue;  // behind P
     const int row = row0 + (r16 < rows ? r16 : 0);
     int64_t src = g.gather ? g.gather[row] / g.gather_div : row;
     src = src < 0 ? 0 : src >= g.a_rows ? g.a_rows - 1 : src;
@@ -139,11 +168,9 @@ __global__ __launch_bounds__(kThreads) void mx_small_kernel(MxGemmArgs g, int n_
 
 namespace {
 
-// A tile: WM x WN waves, each MT x NT accumulator tiles of 32 x 32 (v_mfma_scale 32x32x64, the
-// weights first: a lane holds row lane & 31, columns 8 (j / 4) + 4 (lane / 32) + j % 4).
-#ifndef FENCE
-#define FENCE __builtin_amdgcn_sched_barrier(0)
-#endif
+// A tile: WM x WN waves, each MT x NT accumulator tiles of 32 x 32 (v_mfma_scale 32x32x64: a lane
+// holds column lane & 31 of rows 8 (j / 4) + 4 (lane / 32) + j % 4).  The weight rows are laid out
+// so that a lane's NT columns are neighbours: a row's results leave as whole lines.
 template <int kWM, int kWN, int kMT, int kNT, int kPerCu>
 struct Tile {
   static constexpr int PER_CU = kPerCu;  // workgroups on a compute unit
@@ -153,49 +180,66 @@ struct Tile {
   static constexpr int A_DMA = BM / 8 / WAVES, B_DMA = BN / 8 / WAVES;  // copies of 8 rows a wave
   static constexpr int S_GROUPS = (BM + BN) / 64;  // of 64 rows' scales, a copy each
   static constexpr int S_DMA = (S_GROUPS + WAVES - 1) / WAVES;  // a wave (the last group's twice)
-  static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "whole copies a wave");
+  static_assert(BM % (8 * WAVES) == 0 && BM % 64 == 0, "whole copies a wave");
+  static_assert(32 % (B_DMA * 8) == 0, "a wave copies rows of one group of 32 weight rows");
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;  // 256 codes of a row
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int WINDOW = (BM + BN) * 16;  // 16 scale bytes of a row
   static constexpr int LDS = 2 * (STAGE + WINDOW);
 };
 
+constexpr int kDescs = 64;  // tiles of a workgroup that are looked up at a time
+
+// Which rows and columns a tile has.
+struct TileDesc {
+  int e, row0, rows, n_idx;
+};
+
+// What a wave copies: offsets of its lanes in the arrays at step 0 of a tile.
 template <class T>
 struct Copies {
   i32x4 a_rsrc, b_rsrc, sa_rsrc, sb_rsrc;
-  uint32_t a_off[T::A_DMA], b_off[T::B_DMA], s_off[T::S_DMA];
+  uint32_t a_off[T::A_DMA], b_off, s_off[T::S_DMA];
 };
 
-// dma16 for the lanes of `due`, all or none (every lane of the wave is at work here).
-__device__ __forceinline__ void dma16_if(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds,
-                                         uint32_t due) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\t"
-               "s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds\n\ts_mov_b64 exec, -1"
-               :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds), "s"(due) : "memory", "m0");
+// The value of every lane, for a scalar register.
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ i32x4 scalar(i32x4 v) {
+  return i32x4{scalar(v.x), scalar(v.y), scalar(v.z), scalar(v.w)};
 }
 
-// Copy j of a wave's A_DMA + B_DMA of step kb, to the stage at LDS address st.
+// dma16 for the lanes of `due`, all or none (every lane of the wave is at work here).  Bounds are
+// checked on voff alone, so it is the whole offset.
+__device__ __forceinline__ void dma16_if(i32x4 rsrc, uint32_t voff, uint32_t lds, uint32_t due) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\t"
+               "s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds\n\ts_mov_b64 exec, -1"
+               :: "v"(voff), "s"(rsrc), "s"(lds), "s"(scalar((int)due))
+               : "memory", "m0");
+}
+
+// Copy j of a wave's A_DMA + B_DMA of step kb, to the stage at LDS address st; a lane's weight rows
+// are b_step bytes apart.
 template <class T>
-__device__ __forceinline__ void issue_one(const Copies<T>& c, int j, int kb, uint32_t st, int wave,
-                                          uint32_t due) {
+__device__ __forceinline__ void issue_one(const Copies<T>& c, i32x4 b_rsrc, int j, int kb,
+                                          uint32_t b_step, uint32_t st, int wave, uint32_t due) {
+  const uint32_t k = (uint32_t)kb * 128u;
   if (j < T::A_DMA)
-    dma16_if(c.a_rsrc, c.a_off[j], (uint32_t)kb * 128u, st + (wave * T::A_DMA + j) * 1024,
-             due);
+    dma16_if(c.a_rsrc, c.a_off[j] + k, st + (wave * T::A_DMA + j) * 1024, due);
   else
-    dma16_if(c.b_rsrc, c.b_off[j - T::A_DMA], (uint32_t)kb * 128u,
-          st + T::A_BYTES + (wave * T::B_DMA + j - T::A_DMA) * 1024, due);
+    dma16_if(b_rsrc, c.b_off + ((uint32_t)(j - T::A_DMA) * b_step + k),
+             st + T::A_BYTES + (wave * T::B_DMA + j - T::A_DMA) * 1024, due);
 }
 
-// The scales of step kb on (kPerStep bytes of the row a step): 16 bytes from the aligned word
-// that holds the first.
+// The scales of step kb on (eight bytes of the row a step): 16 bytes from the aligned word that
+// holds the first.
 template <class T>
-__device__ __forceinline__ void issue_scales(const Copies<T>& c, int kb, uint32_t window, int wave,
+__device__ __forceinline__ void issue_scales(const Copies<T>& c, i32x4 sb_rsrc, int kb, uint32_t window, int wave,
                                              uint32_t due) {
 #pragma unroll
   for (int i = 0; i < T::S_DMA; ++i) {
     // rows 64 g .. of the activations, then of the weights
     const int g = min(wave * T::S_DMA + i, T::S_GROUPS - 1);
-    dma16_if(g * 64 < T::BM ? c.sa_rsrc : c.sb_rsrc, c.s_off[i], (uint32_t)kb * 8u,
+    dma16_if(g * 64 < T::BM ? c.sa_rsrc : sb_rsrc, c.s_off[i] + (uint32_t)kb * 8u,
              window + g * 1024, due);
   }
 }
@@ -205,8 +249,9 @@ template <class T>
 struct Place {
   uint32_t ro[4], a_base, b_base;
   int a_row, b_row;  // this lane's first row among the stage's rows
-  uint32_t a_shift[T::MT], b_shift;
+  uint32_t a_shift[T::MT], b_shift[T::NT];
   uint32_t mask[2];  // of the last step's halves: scale bytes inside the row
+  int last;          // that step
   uint32_t lane_shift;
 };
 
@@ -257,8 +302,8 @@ __device__ __forceinline__ void multiply(const Frags<T>& f, const int (&sa)[T::M
 #pragma unroll
         for (int n = 0; n < T::NT; ++n)
           acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              codes8(f.b[n]), codes8(f.a[m]), acc[m][n], 4, 4, kSel, sb[n][kHalf], kSel,
-              sa[m][kHalf]);
+              codes8(f.a[m]), codes8(f.b[n]), acc[m][n], 4, 4, kSel, sa[m][kHalf], kSel,
+              sb[n][kHalf]);
       }
     }
     between(m);
@@ -266,14 +311,16 @@ __device__ __forceinline__ void multiply(const Frags<T>& f, const int (&sa)[T::M
 }
 
 // The k loop of a tile for a wave with M row tiles that hold rows.  Step kb (256 of K: whole
-// 128-byte lines of the codes' rows) is in stage kb % 2, the scales of one step (kSplit) or two in
-// a window of their own.  The barrier of a step stands before its last quarter, where every wave
-// has read the stage: the copies of step kb + 2 go there then, among the quarter's products.  A
-// copy that is not due is issued for no lane: with a branch in its place the products of
-// the whole step were moved behind the barrier.
-template <class T, int M, bool kSplit>
-__device__ __forceinline__ void kloop(const Copies<T>& c, const Place<T>& p, int nk,
-                                      const char* ring, uint32_t ring_at, int wave,
+// 128-byte lines of the codes' rows) is in the stage of its parity, counted on over the tiles, the
+// scales of one step (kSplit) or two in a window of their own.  The barrier of a step stands before
+// its last quarter, where every wave has read the stage: the copies of the step after next go
+// there then, among the quarter's products -- of the next tile's first steps at the end of a
+// tile, for which `next_copies` changes c.  A copy that is not due is issued for no lane: with a
+// branch in its place the products of the whole step were moved behind the barrier.
+template <class T, int M, bool kSplit, class F>
+__device__ __forceinline__ void kloop(Copies<T>& c, const Place<T>& p, int nk, uint32_t b_step,
+                                      const char* ring, uint32_t ring_at, int wave, int& stage_,
+                                      int& window_, bool more, F next_copies,
                                       f32x16 (&acc)[M ? M : 1][T::NT]) {
 #pragma unroll
   for (int m = 0; m < M; ++m)
@@ -281,24 +328,26 @@ __device__ __forceinline__ void kloop(const Copies<T>& c, const Place<T>& p, int
     for (int n = 0; n < T::NT; ++n)
 #pragma unroll
       for (int j = 0; j < 16; ++j) acc[m][n][j] = 0.f;
-  wait_vm_barrier<T::A_DMA + T::B_DMA>();  // all but step 1's codes landed
   Frags<T> f0, f1;
-  load_frags<T, M>(ring, p.ro[0], p, f0);
+  load_frags<T, M>(ring + scalar(stage_) * T::STAGE, p.ro[0], p, f0);
   const auto nothing = [](int) {};
   for (int kb = 0; kb < nk; ++kb) {
-    const int odd = kb & 1;
-    const char* st = ring + odd * T::STAGE;
-    const int slot = kSplit ? odd : (kb >> 1) & 1;
-    const char* win = ring + 2 * T::STAGE + slot * T::WINDOW;
+    if (kb == nk - 2) next_copies();
+    const int stage = scalar(stage_), window = scalar(window_);
+    const i32x4 b_rsrc = scalar(c.b_rsrc), sb_rsrc = scalar(c.sb_rsrc);
+    const char* st = ring + stage * T::STAGE;
+    const char* win = ring + 2 * T::STAGE + window * T::WINDOW;
     int sa[T::MT][2], sb[T::NT][2];
     if constexpr (M > 0) {
-      const uint32_t mask[2] = {kb == nk - 1 ? p.mask[0] : ~0u, kb == nk - 1 ? p.mask[1] : ~0u};
+      const int left = p.last - kb;  // a step behind the last has no scales
+      const uint32_t mask[2] = {left > 0 ? ~0u : left ? 0u : p.mask[0],
+                                left > 0 ? ~0u : left ? 0u : p.mask[1]};
 #pragma unroll
       for (int m = 0; m < M; ++m)
-        scale_words<T, kSplit>(win, p.a_row + m * 32, odd, p.a_shift[m], mask, p.lane_shift, sa[m]);
+        scale_words<T, kSplit>(win, p.a_row + m * 32, kb & 1, p.a_shift[m], mask, p.lane_shift, sa[m]);
 #pragma unroll
       for (int n = 0; n < T::NT; ++n)
-        scale_words<T, kSplit>(win, p.b_row + n * 32, odd, p.b_shift, mask, p.lane_shift, sb[n]);
+        scale_words<T, kSplit>(win, p.b_row + n * 32, kb & 1, p.b_shift[n], mask, p.lane_shift, sb[n]);
     }
     load_frags<T, M>(st, p.ro[1], p, f1);
     multiply<T, M, 0>(f0, sa, sb, acc, nothing);
@@ -311,18 +360,23 @@ __device__ __forceinline__ void kloop(const Copies<T>& c, const Place<T>& p, int
     FENCE;
     wait_vm_barrier<0>();
     FENCE;
-    load_frags<T, M>(ring + (odd ^ 1) * T::STAGE, p.ro[0], p, f0);
-    const int next = kb + 2;
-    const uint32_t due = __builtin_amdgcn_readfirstlane(next < nk ? ~0u : 0u);
-    issue_scales<T>(c, next, ring_at + 2 * T::STAGE + (kSplit ? slot : slot ^ 1) * T::WINDOW, wave,
-                    kSplit ? due : due & (uint32_t)(odd - 1));
+    load_frags<T, M>(ring + (stage ^ 1) * T::STAGE, p.ro[0], p, f0);
+    const int ahead = kb + 2 < nk ? kb + 2 : kb + 2 - nk;
+    const uint32_t due = kb + 2 < nk || more ? ~0u : 0u;
+    // a window read for the last time gives its place (an odd step); at an even one the other
+    // window's is free
+    const int slot = kSplit || (kb & 1) ? window : window ^ 1;
+    issue_scales<T>(c, sb_rsrc, ahead, ring_at + 2 * T::STAGE + slot * T::WINDOW, wave,
+                    kSplit || !(ahead & 1) ? due : 0u);
     multiply<T, M, 3>(f1, sa, sb, acc, [&](int m) {
       constexpr int kAll = T::A_DMA + T::B_DMA, kPart = (kAll + T::MT - 1) / T::MT;
 #pragma unroll
       for (int j = m * kPart; j < min((m + 1) * kPart, kAll); ++j)
-        issue_one<T>(c, j, next, ring_at + odd * T::STAGE, wave, due);
+        issue_one<T>(c, b_rsrc, j, ahead, b_step, ring_at + stage * T::STAGE, wave, due);
     });
     FENCE;
+    stage_ = stage ^ 1;
+    window_ = kSplit || (kb & 1) || kb == nk - 1 ? window ^ 1 : window;
   }
 }
 
@@ -331,35 +385,53 @@ struct Const {
   static constexpr int value = V;
 };
 
+// N neighbouring values.
+template <int kOut, int N>
+__device__ __forceinline__ void store_run(void* out, int64_t at, const float (&v)[N]) {
+  if constexpr (kOut == kF32) {
+    float* p = reinterpret_cast<float*>(out) + at;
+    if constexpr (N == 4) *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    else if constexpr (N == 2) *reinterpret_cast<f32x2*>(p) = f32x2{v[0], v[1]};
+    else p[0] = v[0];
+  } else {
+    uint16_t* p = reinterpret_cast<uint16_t*>(out) + at;
+    if constexpr (N == 4)
+      *reinterpret_cast<u32x2*>(p) = u32x2{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3])};
+    else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = pack2<kOut>(v[0], v[1]);
+    else p[0] = (uint16_t)pack2<kOut>(v[0], 0.f);
+  }
+}
+
 // The wave's rows of a tile, from its accumulators, to their places in out.
 template <class T, int M, bool kSwiglu, int kOut>
-__device__ __forceinline__ void store_tile(const MxGemmArgs& g, const int32_t* orow,
-                                           const float* rscale, int rows_valid, int col0, int wm,
+__device__ __forceinline__ void store_tile(const MxGemmArgs& g, const TileDesc& d,
+                                           const int32_t* orow, const float* rscale, int wm,
                                            int wn, int n32, int g2,
                                            const f32x16 (&acc)[M][T::NT]) {
+  constexpr int C = kSwiglu ? T::NT / 2 : T::NT;  // columns of a lane
   const int ncols = kSwiglu ? g.N >> 1 : g.N;
+  const int col = (d.n_idx * T::WN + wn) * 32 * C + n32 * C;
+  if (col >= ncols) return;  // ncols is a multiple of 16: all of a lane's columns or none
 #pragma unroll
   for (int m = 0; m < M; ++m) {
-    const int trow = (wm * T::MT + m) * 32 + n32;
-    if (trow >= rows_valid) continue;
-    const int64_t o = orow[trow];
-    if (o < 0 || o >= g.out_rows) continue;
-    const float rs = rscale[trow];
-    constexpr int NTO = kSwiglu ? T::NT / 2 : T::NT;
 #pragma unroll
-    for (int n = 0; n < NTO; ++n) {
+    for (int q = 0; q < 4; ++q) {
+      const int trow = (wm * T::MT + m) * 32 + 8 * q + 4 * g2;
+      i32x4 o = i32x4{0, 1, 2, 3} + (d.row0 + trow);
+      f32x4 rs = {1.f, 1.f, 1.f, 1.f};
+      if (g.scatter) o = *reinterpret_cast<const i32x4*>(orow + trow);
+      if (g.row_scale) rs = *reinterpret_cast<const f32x4*>(rscale + trow);
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        const int col = col0 + (wn * NTO + n) * 32 + 8 * jj + 4 * g2;
-        if (col >= ncols) continue;
-        float v[4];
+      for (int i = 0; i < 4; ++i) {
+        if (trow + i >= d.rows || o[i] < 0 || o[i] >= g.out_rows) continue;
+        float v[C];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = 4 * jj + i;
-          if constexpr (kSwiglu) v[i] = silu_f(acc[m][n][j]) * acc[m][n + NTO][j] * rs;
-          else v[i] = acc[m][n][j] * rs;
+        for (int n = 0; n < C; ++n) {
+          const int j = 4 * q + i;
+          if constexpr (kSwiglu) v[n] = silu_f(acc[m][n][j]) * acc[m][n + C][j] * rs[i];
+          else v[n] = acc[m][n][j] * rs[i];
         }
-        store4<kOut>(g.out, o * ncols + col, v);
+        store_run<kOut, C>(g.out, (int64_t)o[i] * ncols + col, v);
       }
     }
   }
@@ -370,20 +442,24 @@ __device__ __forceinline__ void store_tile(const MxGemmArgs& g, const int32_t* o
 template <class T, bool kSwiglu, int kOut, bool kSplit>
 __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmArgs g, int n_tiles) {
   __shared__ __attribute__((aligned(1024))) char ring[T::LDS];
+  __shared__ __attribute__((aligned(16))) int32_t srow[2][T::BM];   // gather entry of each row
+  __shared__ __attribute__((aligned(16))) int32_t orow[2][T::BM];   // and its scatter entry
+  __shared__ __attribute__((aligned(16))) float rscale[2][T::BM];   // and row scale
+  __shared__ TileDesc descs[kDescs];
   __shared__ int32_t tiles[kMaxExperts + 1];
   __shared__ int32_t wsum[T::WAVES];
-  __shared__ int32_t orow[2][T::BM];
-  __shared__ float rscale[2][T::BM];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / T::WN, wn = wave % T::WN;
   const int n32 = lane & 31, g2 = lane >> 5;
-  build_tile_table<T::THREADS, T::BM>(g.offsets, g.E, tiles, wsum, tid);
+  build_tiles<T::THREADS, T::BM>(g.offsets, g.E, (int)g.P, tiles, wsum, tid);
 
   const int N = g.N, I = N >> 1, KB = g.K / 32;
-  const int nk = (KB + 7) / 8;
+  const int nk = max(2, (KB + 7) / 8);
   const uint32_t row_bytes = (uint32_t)KB * 16u;
+  constexpr int C = kSwiglu ? T::NT / 2 : T::NT;  // neighbouring columns of a lane
+  const uint32_t b_step = 8u * C * row_bytes;
   Place<T> p;
 #pragma unroll
   for (int q = 0; q < 4; ++q) p.ro[q] = n32 * 128 + (((2 * q + g2) ^ (n32 & 7)) << 4);
@@ -391,120 +467,151 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
   p.b_base = (uint32_t)wn * T::NT * 4096;
   p.a_row = wm * T::MT * 32 + n32;
   p.b_row = T::BM + wn * T::NT * 32 + n32;
+  p.last = (KB + 7) / 8 - 1;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int inside = KB - (nk - 1) * 8 - 4 * h;  // scale bytes of the last step's half
+    const int inside = KB - p.last * 8 - 4 * h;  // scale bytes of the last step's half
     p.mask[h] = inside >= 4 ? ~0u : inside > 0 ? (1u << (8 * inside)) - 1u : 0u;
   }
   p.lane_shift = 8 * g2;
-  constexpr int kCols = kSwiglu ? T::BN / 2 : T::BN;  // output columns of a tile
 
-  // weight row of LDS row l, clamped to a valid one.  SwiGLU: of a wave's NT groups of 32 the
-  // first half are gate rows, the others the up rows of the same columns.
+  // The weight row of LDS row l = (wave column, group of 32, i): columns C i .. of a wave column
+  // go to its first C groups; SwiGLU: their up rows to the others.  Rows behind the
+  // matrix are read as zeros, gate rows behind I are up rows; neither's results are stored.
   auto weight_row = [&](int l, int n_idx) -> int {
-    if constexpr (kSwiglu) {
-      constexpr int H = T::NT / 2;
-      const int w = l / (T::NT * 32), nt = (l >> 5) % T::NT, n = l & 31;
-      const int col = n_idx * kCols + (w * H + nt % H) * 32 + n;
-      return min(col, I - 1) + (nt >= H ? I : 0);
-    } else {
-      return min(n_idx * T::BN + l, N - 1);
-    }
+    const int w = l / (T::NT * 32), nt = (l >> 5) % T::NT, i = l & 31;
+    return ((n_idx * T::WN + w) * 32 + i) * C + nt % C + (nt >= C ? I : 0);
   };
   // scales are read as aligned words: byte offsets from the array's start rounded down
-  auto scale_rsrc = [&](const uint8_t* p, int64_t bytes, uint32_t& skip) -> i32x4 {
-    skip = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3);
-    return make_rsrc(p - skip, ((uint32_t)bytes + skip + 3u) & ~3u);
+  auto scale_rsrc = [&](const uint8_t* at, int64_t bytes, uint32_t& skip) -> i32x4 {
+    skip = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 3);
+    return make_rsrc(at - skip, ((uint32_t)bytes + skip + 3u) & ~3u);
   };
-
-  Copies<T> c;
-  uint32_t a_skip, b_skip;
-  c.a_rsrc = make_rsrc(g.a, (uint32_t)g.a_rows * row_bytes);
-  c.sa_rsrc = scale_rsrc(g.a_scales, g.a_rows * KB, a_skip);
   const int total_m = __builtin_amdgcn_readfirstlane(tiles[g.E]);
   const int total = total_m * n_tiles;
   const int G = gridDim.x;  // a multiple of 8
   const int u = (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3);
-  const uint32_t ring_at = lds_addr(ring);
-  for (int r = 0;; ++r) {
-    const int tix = r * G + u;
-    if (tix >= total) break;
-    // groups of four row tiles, the row tile changing fastest
-    const int group = tix / (4 * n_tiles), in = tix - group * 4 * n_tiles;
-    const int gm = min(4, total_m - group * 4);
-    const int n_idx = in / gm, mt_global = group * 4 + (in - n_idx * gm);
-    int lo = 0, hi = g.E;  // tiles[lo] <= mt_global < tiles[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (tiles[mid] <= mt_global) lo = mid; else hi = mid;
+  if (u >= total) return;
+  // Tiles r .. r + 63 of this workgroup: groups of four row tiles, the row tile changing fastest.
+  auto look_up = [&](int r) {
+    const int64_t t = (int64_t)(r + tid) * G + u;
+    if (tid < kDescs && t < total) {
+      const int tix = (int)t;
+      const int group = tix / (4 * n_tiles), in = tix - group * 4 * n_tiles;
+      const int gm = min(4, total_m - group * 4);
+      const int n_idx = in / gm, mt = group * 4 + (in - n_idx * gm);
+      int lo = 0, hi = g.E;  // tiles[lo] <= mt < tiles[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tiles[mid] <= mt) lo = mid; else hi = mid;
+      }
+      const int row0 = g.offsets[lo] + (mt - tiles[lo]) * T::BM;
+      const int end = min(g.offsets[lo + 1], (int)g.P);
+      descs[tid] = TileDesc{lo, row0, min(T::BM, end - row0), n_idx};
     }
-    const int e = __builtin_amdgcn_readfirstlane(lo);
-    const int m_local = mt_global - __builtin_amdgcn_readfirstlane(tiles[e]);
-    const int row0 = __builtin_amdgcn_readfirstlane(g.offsets[e]) + m_local * T::BM;
-    const int end = min(__builtin_amdgcn_readfirstlane(g.offsets[e + 1]), (int)g.P);
-    const int rows_valid = min(T::BM, end - row0);
-    if (rows_valid <= 0) continue;  // behind P
-    const int mtv = max(0, min(T::MT, (rows_valid - wm * T::MT * 32 + 31) >> 5));
-
-    auto source = [&](int row) -> uint32_t {
-      const int idx = row0 + (row < rows_valid ? row : 0);
-      const int s = g.gather ? g.gather[idx] / g.gather_div : idx;
-      return (uint32_t)min(max(s, 0), (int)g.a_rows - 1);
-    };
-    const int64_t w_at = (int64_t)e * N;
+  };
+  auto desc = [&](int r) -> TileDesc {
+    const TileDesc d = descs[r & (kDescs - 1)];
+    return TileDesc{__builtin_amdgcn_readfirstlane(d.e), __builtin_amdgcn_readfirstlane(d.row0),
+                    __builtin_amdgcn_readfirstlane(d.rows), __builtin_amdgcn_readfirstlane(d.n_idx)};
+  };
+  const i32x4 ga_rsrc = make_rsrc(g.gather, g.gather ? (uint32_t)g.P * 4u : 0u);
+  const i32x4 sc_rsrc = make_rsrc(g.scatter, g.scatter ? (uint32_t)g.P * 4u : 0u);
+  const i32x4 rs_rsrc = make_rsrc(g.row_scale, g.row_scale ? (uint32_t)g.P * 4u : 0u);
+  // The index arrays' entries of a tile's rows (the last row's for the rows behind it).
+  auto copy_indices = [&](const TileDesc& d, int par) {
+    for (int grp = wave; grp < T::BM / 64; grp += T::WAVES) {
+      const uint32_t at = (uint32_t)(d.row0 + min(grp * 64 + lane, d.rows - 1)) * 4u;
+      if (g.gather) dma4(ga_rsrc, at, 0, lds_addr(&srow[par][grp * 64]));
+      if (g.scatter) dma4(sc_rsrc, at, 0, lds_addr(&orow[par][grp * 64]));
+      if (g.row_scale) dma4(rs_rsrc, at, 0, lds_addr(&rscale[par][grp * 64]));
+    }
+  };
+  auto source = [&](const TileDesc& d, int par, int row) -> uint32_t {
+    const int s = g.gather ? srow[par][row] / g.gather_div : d.row0 + min(row, d.rows - 1);
+    return (uint32_t)min(max(s, 0), (int)g.a_rows - 1);
+  };
+  Copies<T> c;
+  uint32_t a_skip, b_skip = 0;
+  c.a_rsrc = make_rsrc(g.a, (uint32_t)g.a_rows * row_bytes);
+  c.sa_rsrc = scale_rsrc(g.a_scales, g.a_rows * KB, a_skip);
+  auto copies_of = [&](const TileDesc& d, int par) {
+    const int64_t w_at = (int64_t)d.e * N;
     c.b_rsrc = make_rsrc(g.blocks + w_at * row_bytes, (uint32_t)N * row_bytes);
     c.sb_rsrc = scale_rsrc(g.scales + w_at * KB, (int64_t)N * KB, b_skip);
 #pragma unroll
     for (int i = 0; i < T::A_DMA; ++i) {
       const int row = (wave * T::A_DMA + i) * 8 + (lane >> 3);
-      c.a_off[i] = source(row) * row_bytes + (((lane & 7) ^ (row & 7)) << 4);
+      c.a_off[i] = source(d, par, row) * row_bytes + (((lane & 7) ^ (row & 7)) << 4);
     }
-#pragma unroll
-    for (int i = 0; i < T::B_DMA; ++i) {
-      const int l = (wave * T::B_DMA + i) * 8 + (lane >> 3);
-      c.b_off[i] = (uint32_t)weight_row(l, n_idx) * row_bytes + (((lane & 7) ^ (l & 7)) << 4);
-    }
+    const int l0 = wave * T::B_DMA * 8 + (lane >> 3);
+    c.b_off = (uint32_t)weight_row(l0, d.n_idx) * row_bytes + (((lane & 7) ^ (l0 & 7)) << 4);
 #pragma unroll
     for (int i = 0; i < T::S_DMA; ++i) {
       const int l = min(wave * T::S_DMA + i, T::S_GROUPS - 1) * 64 + lane;
-      c.s_off[i] = (l < T::BM ? source(l) * (uint32_t)KB + a_skip
-                              : (uint32_t)weight_row(l - T::BM, n_idx) * (uint32_t)KB + b_skip) & ~3u;
+      c.s_off[i] = (l < T::BM ? source(d, par, l) * (uint32_t)KB + a_skip
+                              : (uint32_t)weight_row(l - T::BM, d.n_idx) * (uint32_t)KB + b_skip) & ~3u;
     }
-    // where in its first word a row's scales begin; the same for all of a lane's weight rows
+  };
+
+  const uint32_t ring_at = lds_addr(ring);
+  look_up(0);
+  __syncthreads();
+  TileDesc cur = desc(0);
+  copy_indices(cur, 0);
+  wait_vm_barrier<0>();
+  copies_of(cur, 0);
+  issue_scales<T>(c, c.sb_rsrc, 0, ring_at + 2 * T::STAGE, wave, ~0u);
+  if (kSplit) issue_scales<T>(c, c.sb_rsrc, 1, ring_at + 2 * T::STAGE + T::WINDOW, wave, ~0u);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < T::A_DMA + T::B_DMA; ++j)
+      issue_one<T>(c, c.b_rsrc, j, i, b_step, ring_at + i * T::STAGE, wave, ~0u);
+  wait_vm_barrier<T::A_DMA + T::B_DMA>();  // all but step 1's codes landed
+  int stage = 0, window = 0;
+  for (int r = 0;; ++r) {
+    const int par = r & 1;
+    const bool more = (int64_t)(r + 1) * G + u < total;
+    TileDesc next = cur;
+    if (more) {
+      if (((r + 1) & (kDescs - 1)) == 0) {
+        __syncthreads();
+        look_up(r + 1);
+        __syncthreads();
+      }
+      next = desc(r + 1);
+      copy_indices(next, par ^ 1);
+      // they are read two steps before the tile's end, behind a step's barrier
+      if (nk < 3) wait_vm_barrier<0>();
+    }
+    // where in its first word a row's scales begin
     if constexpr (kSplit) {
 #pragma unroll
       for (int m = 0; m < T::MT; ++m)
-        p.a_shift[m] = (source((wm * T::MT + m) * 32 + n32) * (uint32_t)KB + a_skip) & 3u;
-      p.b_shift = ((uint32_t)weight_row(wn * T::NT * 32 + n32, n_idx) * (uint32_t)KB + b_skip) & 3u;
-    }
-    const int par = r & 1;
-    for (int l = tid; l < T::BM; l += T::THREADS) {
-      const int row = row0 + (l < rows_valid ? l : 0);
-      orow[par][l] = g.scatter ? g.scatter[row] : row;
-      rscale[par][l] = g.row_scale ? g.row_scale[row] : 1.0f;
-    }
-
-    // every wave is done with the previous tile's ring
-    lds_barrier();
-    issue_scales<T>(c, 0, ring_at + 2 * T::STAGE, wave, ~0u);
-    if (kSplit) issue_scales<T>(c, min(1, nk - 1), ring_at + 2 * T::STAGE + T::WINDOW, wave, ~0u);
+        p.a_shift[m] = (source(cur, par, (wm * T::MT + m) * 32 + n32) * (uint32_t)KB + a_skip) & 3u;
+      const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>(g.scales + (int64_t)cur.e * N * KB);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < T::A_DMA + T::B_DMA; ++j)
-        issue_one<T>(c, j, min(i, nk - 1), ring_at + i * T::STAGE, wave, ~0u);
+      for (int n = 0; n < T::NT; ++n)
+        p.b_shift[n] = (at + (uint32_t)weight_row((wn * T::NT + n) * 32 + n32, cur.n_idx) * KB) & 3u;
+    }
+    const int mtv = max(0, min(T::MT, (cur.rows - wm * T::MT * 32 + 31) >> 5));
     auto tile = [&](auto rows) {
       constexpr int M = decltype(rows)::value;
       f32x16 acc[M ? M : 1][T::NT];
-      kloop<T, M, kSplit>(c, p, nk, ring, ring_at, wave, acc);
+      kloop<T, M, kSplit>(c, p, nk, b_step, ring, ring_at, wave, stage, window, more,
+                          [&] { copies_of(next, par ^ 1); }, acc);
       if constexpr (M > 0)
-        store_tile<T, M, kSwiglu, kOut>(g, orow[par], rscale[par], rows_valid, n_idx * kCols, wm,
-                                        wn, n32, g2, acc);
+        store_tile<T, M, kSwiglu, kOut>(g, cur, orow[par], rscale[par], wm, wn, n32, g2, acc);
     };
     if (mtv > T::MT / 2) tile(Const<T::MT>{});
     else if (T::MT > 2 && mtv == 2) tile(Const<T::MT / 2>{});
     else if (mtv == 1) tile(Const<1>{});
     else tile(Const<0>{});
+    if (!more) break;
+    cur = next;
+    // every wave has read this tile's indices, whose place the next but one's take
+    lds_barrier();
   }
   // no copy of the wave is left in flight when it ends
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
