@@ -1686,7 +1686,7 @@ static size_t mx_codes_bytes(int64_t rows, int64_t K) {
 
 size_t grouped_mx4_gemm_workspace(int64_t a_rows, int64_t K, int a_dtype) {
   if (a_rows < 1 || K < 32 || K % 32 || !is_float_dtype(a_dtype) ||
-      a_rows > (int64_t)UINT32_MAX / (K / 2))
+      a_rows > kMxMaxBytes / (K / 2))
     return 0;
   return mx_codes_bytes(a_rows, K) + align_up((size_t)a_rows * (size_t)(K / 32), 256);
 }
@@ -1719,9 +1719,8 @@ int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_
     return fail(NF4MOE_EOVERFLOW, "P, a_rows, out_rows, N or K too large for 32-bit indexing");
   // the kernel addresses activations and one expert's weights with 32-bit byte offsets, up to a
   // tile's rows behind the end
-  if (a_rows + kMxTileRows > (int64_t)UINT32_MAX / (K / 2) ||
-      N + kMxTileRows > (int64_t)UINT32_MAX / (K / 2))
-    return fail(NF4MOE_EOVERFLOW, "the activations' codes or one expert's exceed 4 GiB");
+  if (a_rows + kMxTileRows > kMxMaxBytes / (K / 2) || N + kMxTileRows > kMxMaxBytes / (K / 2))
+    return fail(NF4MOE_EOVERFLOW, "the activations' codes or one expert's exceed 3.5 GiB");
   if (P == 0) return ok();
   if (a == nullptr || blocks == nullptr || scales == nullptr || expert_offsets == nullptr ||
       out == nullptr || a_rows == 0 || out_rows == 0)

@@ -243,7 +243,8 @@ hipError_t launch_mx_quantize(const void* x, int x_dtype, int64_t E, int64_t R, 
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, void* out,
                                 int out_dtype, hipStream_t s);
 
-constexpr int64_t kMxTileRows = 512;  // rows behind a matrix's end whose places are computed
+constexpr int64_t kMxMaxBytes = 0xe0000000;  // of the activations' codes and of one expert's
+constexpr int64_t kMxTileRows = 512;         // rows behind a matrix's end whose places are computed
 struct MxGemmArgs {
   const uint8_t* a;         // [a_rows, K / 2] codes
   const uint8_t* a_scales;  // [a_rows, K / 32]

@@ -199,7 +199,7 @@ struct TileDesc {
 template <class T>
 struct Copies {
   i32x4 a_rsrc, b_rsrc, sa_rsrc, sb_rsrc;
-  uint32_t a_off[T::A_DMA], b_off, s_off[T::S_DMA];
+  uint32_t a_off[T::A_DMA], b_off[2], s_off[T::S_DMA];  // b_off: even and odd copies
 };
 
 // The value of every lane, for a scalar register.
@@ -208,39 +208,42 @@ __device__ __forceinline__ i32x4 scalar(i32x4 v) {
   return i32x4{scalar(v.x), scalar(v.y), scalar(v.z), scalar(v.w)};
 }
 
-// dma16 for the lanes of `due`, all or none (every lane of the wave is at work here).  Bounds are
-// checked on voff alone, so it is the whole offset.
-__device__ __forceinline__ void dma16_if(i32x4 rsrc, uint32_t voff, uint32_t lds, uint32_t due) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\t"
-               "s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds\n\ts_mov_b64 exec, -1"
-               :: "v"(voff), "s"(rsrc), "s"(lds), "s"(scalar((int)due))
-               : "memory", "m0");
-}
+// The weight copies of a step that are issued in the next one's first half.
+struct Pending {
+  i32x4 rsrc;
+  uint32_t off[2], where;
+  int kb;
+};
 
-// Copy j of a wave's A_DMA + B_DMA of step kb, to the stage at LDS address st; a lane's weight rows
+// An offset that no array has: a copy from there writes zeros and reads no memory.
+constexpr uint32_t kNowhere = 0xf0000000u;
+
+// Copy j of a wave's A_DMA and of its B_DMA, to the stage at LDS address st.  Bounds are checked on
+// the lane's offset alone, so it is the whole one; `where` is 0 or kNowhere.  A lane's weight rows
 // are b_step bytes apart.
 template <class T>
-__device__ __forceinline__ void issue_one(const Copies<T>& c, i32x4 b_rsrc, int j, int kb,
-                                          uint32_t b_step, uint32_t st, int wave, uint32_t due) {
-  const uint32_t k = (uint32_t)kb * 128u;
-  if (j < T::A_DMA)
-    dma16_if(c.a_rsrc, c.a_off[j] + k, st + (wave * T::A_DMA + j) * 1024, due);
-  else
-    dma16_if(b_rsrc, c.b_off + ((uint32_t)(j - T::A_DMA) * b_step + k),
-             st + T::A_BYTES + (wave * T::B_DMA + j - T::A_DMA) * 1024, due);
+__device__ __forceinline__ void issue_a(const Copies<T>& c, int j, int kb, uint32_t st, int wave,
+                                        uint32_t where) {
+  dma16(c.a_rsrc, (c.a_off[j] + (uint32_t)kb * 128u) | where, 0, st + (wave * T::A_DMA + j) * 1024);
+}
+template <class T>
+__device__ __forceinline__ void issue_b(const Pending& d, int j, uint32_t b_step, uint32_t st,
+                                        int wave) {
+  dma16(d.rsrc, (d.off[j & 1] + ((uint32_t)j * b_step + (uint32_t)d.kb * 128u)) | d.where, 0,
+        st + T::A_BYTES + (wave * T::B_DMA + j) * 1024);
 }
 
 // The scales of step kb on (eight bytes of the row a step): 16 bytes from the aligned word that
 // holds the first.
 template <class T>
 __device__ __forceinline__ void issue_scales(const Copies<T>& c, i32x4 sb_rsrc, int kb, uint32_t window, int wave,
-                                             uint32_t due) {
+                                             uint32_t trash, uint32_t where) {
 #pragma unroll
   for (int i = 0; i < T::S_DMA; ++i) {
     // rows 64 g .. of the activations, then of the weights
     const int g = min(wave * T::S_DMA + i, T::S_GROUPS - 1);
-    dma16_if(g * 64 < T::BM ? c.sa_rsrc : sb_rsrc, c.s_off[i] + (uint32_t)kb * 8u,
-             window + g * 1024, due);
+    dma16(g * 64 < T::BM ? c.sa_rsrc : sb_rsrc, (c.s_off[i] + (uint32_t)kb * 8u) | where, 0,
+          where ? trash : window + g * 1024);
   }
 }
 
@@ -314,11 +317,14 @@ __device__ __forceinline__ void multiply(const Frags<T>& f, const int (&sa)[T::M
 // 128-byte lines of the codes' rows) is in the stage of its parity, counted on over the tiles, the
 // scales of one step (kSplit) or two in a window of their own.  The barrier of a step stands before
 // its last quarter, where every wave has read the stage: the copies of the step after next go
-// there then, among the quarter's products -- of the next tile's first steps at the end of a
-// tile, for which `next_copies` changes c.  A copy that is not due is issued for no lane: with a
-// branch in its place the products of the whole step were moved behind the barrier.
+// there then, the activations' among the quarter's products, the weights' among those of the next
+// step's first half (all in one quarter kept the waves from their products: the copies' addresses
+// take the compute unit 16 cycles each).  At the end of a tile they are those of the next
+// tile's first steps, for which `next_copies` changes c.  A copy that is not due comes from nowhere:
+// with a branch in its place the products of the whole step were moved behind the barrier.
 template <class T, int M, bool kSplit, class F>
-__device__ __forceinline__ void kloop(Copies<T>& c, const Place<T>& p, int nk, uint32_t b_step,
+__device__ __forceinline__ void kloop(Copies<T>& c, Pending& d, const Place<T>& p, int nk,
+                                      uint32_t b_step,
                                       const char* ring, uint32_t ring_at, int wave, int& stage_,
                                       int& window_, bool more, F next_copies,
                                       f32x16 (&acc)[M ? M : 1][T::NT]) {
@@ -331,10 +337,14 @@ __device__ __forceinline__ void kloop(Copies<T>& c, const Place<T>& p, int nk, u
   Frags<T> f0, f1;
   load_frags<T, M>(ring + scalar(stage_) * T::STAGE, p.ro[0], p, f0);
   const auto nothing = [](int) {};
+  const auto part = [](int m, int n) { return n * m / T::MT; };
   for (int kb = 0; kb < nk; ++kb) {
     if (kb == nk - 2) next_copies();
     const int stage = scalar(stage_), window = scalar(window_);
-    const i32x4 b_rsrc = scalar(c.b_rsrc), sb_rsrc = scalar(c.sb_rsrc);
+    const i32x4 sb_rsrc = scalar(c.sb_rsrc);
+    d.rsrc = scalar(d.rsrc);
+    d.where = scalar((int)d.where);
+    d.kb = scalar(d.kb);
     const char* st = ring + stage * T::STAGE;
     const char* win = ring + 2 * T::STAGE + window * T::WINDOW;
     int sa[T::MT][2], sb[T::NT][2];
@@ -349,11 +359,20 @@ __device__ __forceinline__ void kloop(Copies<T>& c, const Place<T>& p, int nk, u
       for (int n = 0; n < T::NT; ++n)
         scale_words<T, kSplit>(win, p.b_row + n * 32, kb & 1, p.b_shift[n], mask, p.lane_shift, sb[n]);
     }
+    const uint32_t other = ring_at + (stage ^ 1) * T::STAGE;
     load_frags<T, M>(st, p.ro[1], p, f1);
-    multiply<T, M, 0>(f0, sa, sb, acc, nothing);
+    multiply<T, M, 0>(f0, sa, sb, acc, [&](int m) {
+#pragma unroll
+      for (int j = part(m, T::B_DMA / 2); j < part(m + 1, T::B_DMA / 2); ++j)
+        issue_b<T>(d, j, b_step, other, wave);
+    });
     FENCE;
     load_frags<T, M>(st, p.ro[2], p, f0);
-    multiply<T, M, 1>(f1, sa, sb, acc, nothing);
+    multiply<T, M, 1>(f1, sa, sb, acc, [&](int m) {
+#pragma unroll
+      for (int j = part(m, T::B_DMA - T::B_DMA / 2); j < part(m + 1, T::B_DMA - T::B_DMA / 2); ++j)
+        issue_b<T>(d, j + T::B_DMA / 2, b_step, other, wave);
+    });
     FENCE;
     load_frags<T, M>(st, p.ro[3], p, f1);
     multiply<T, M, 2>(f0, sa, sb, acc, nothing);
@@ -362,18 +381,18 @@ __device__ __forceinline__ void kloop(Copies<T>& c, const Place<T>& p, int nk, u
     FENCE;
     load_frags<T, M>(ring + (stage ^ 1) * T::STAGE, p.ro[0], p, f0);
     const int ahead = kb + 2 < nk ? kb + 2 : kb + 2 - nk;
-    const uint32_t due = kb + 2 < nk || more ? ~0u : 0u;
+    const uint32_t where = scalar(kb + 2 < nk || more ? 0 : (int)kNowhere);
     // a window read for the last time gives its place (an odd step); at an even one the other
     // window's is free
     const int slot = kSplit || (kb & 1) ? window : window ^ 1;
     issue_scales<T>(c, sb_rsrc, ahead, ring_at + 2 * T::STAGE + slot * T::WINDOW, wave,
-                    kSplit || !(ahead & 1) ? due : 0u);
+                    ring_at + T::LDS, kSplit || !(ahead & 1) ? where : kNowhere);
     multiply<T, M, 3>(f1, sa, sb, acc, [&](int m) {
-      constexpr int kAll = T::A_DMA + T::B_DMA, kPart = (kAll + T::MT - 1) / T::MT;
 #pragma unroll
-      for (int j = m * kPart; j < min((m + 1) * kPart, kAll); ++j)
-        issue_one<T>(c, b_rsrc, j, ahead, b_step, ring_at + stage * T::STAGE, wave, due);
+      for (int j = part(m, T::A_DMA); j < part(m + 1, T::A_DMA); ++j)
+        issue_a<T>(c, j, ahead, ring_at + stage * T::STAGE, wave, where);
     });
+    d = Pending{c.b_rsrc, {c.b_off[0], c.b_off[1]}, where, ahead};
     FENCE;
     stage_ = stage ^ 1;
     window_ = kSplit || (kb & 1) || kb == nk - 1 ? window ^ 1 : window;
@@ -441,7 +460,7 @@ __device__ __forceinline__ void store_tile(const MxGemmArgs& g, const TileDesc& 
 
 template <class T, bool kSwiglu, int kOut, bool kSplit>
 __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmArgs g, int n_tiles) {
-  __shared__ __attribute__((aligned(1024))) char ring[T::LDS];
+  __shared__ __attribute__((aligned(1024))) char ring[T::LDS + 1024];  // with a place for copies of nothing
   __shared__ __attribute__((aligned(16))) int32_t srow[2][T::BM];   // gather entry of each row
   __shared__ __attribute__((aligned(16))) int32_t orow[2][T::BM];   // and its scatter entry
   __shared__ __attribute__((aligned(16))) float rscale[2][T::BM];   // and row scale
@@ -462,7 +481,7 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
   const uint32_t b_step = 8u * C * row_bytes;
   Place<T> p;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) p.ro[q] = n32 * 128 + (((2 * q + g2) ^ (n32 & 7)) << 4);
+  for (int q = 0; q < 4; ++q) p.ro[q] = n32 * 128 + (((2 * q + g2) ^ ((n32 >> 1) & 7)) << 4);
   p.a_base = (uint32_t)wm * T::MT * 4096;
   p.b_base = (uint32_t)wn * T::NT * 4096;
   p.a_row = wm * T::MT * 32 + n32;
@@ -542,10 +561,14 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
 #pragma unroll
     for (int i = 0; i < T::A_DMA; ++i) {
       const int row = (wave * T::A_DMA + i) * 8 + (lane >> 3);
-      c.a_off[i] = source(d, par, row) * row_bytes + (((lane & 7) ^ (row & 7)) << 4);
+      c.a_off[i] = row < d.rows ? source(d, par, row) * row_bytes + (((lane & 7) ^ ((row >> 1) & 7)) << 4)
+                                : kNowhere;
     }
     const int l0 = wave * T::B_DMA * 8 + (lane >> 3);
-    c.b_off = (uint32_t)weight_row(l0, d.n_idx) * row_bytes + (((lane & 7) ^ (l0 & 7)) << 4);
+    // chunks are exchanged by the row's second to fourth bit: eight rows on, by four more
+    const uint32_t chunk = (lane & 7) ^ ((l0 >> 1) & 7);
+    c.b_off[0] = (uint32_t)weight_row(l0, d.n_idx) * row_bytes + (chunk << 4);
+    c.b_off[1] = (uint32_t)weight_row(l0, d.n_idx) * row_bytes + ((chunk ^ 4) << 4);
 #pragma unroll
     for (int i = 0; i < T::S_DMA; ++i) {
       const int l = min(wave * T::S_DMA + i, T::S_GROUPS - 1) * 64 + lane;
@@ -561,14 +584,17 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
   copy_indices(cur, 0);
   wait_vm_barrier<0>();
   copies_of(cur, 0);
-  issue_scales<T>(c, c.sb_rsrc, 0, ring_at + 2 * T::STAGE, wave, ~0u);
-  if (kSplit) issue_scales<T>(c, c.sb_rsrc, 1, ring_at + 2 * T::STAGE + T::WINDOW, wave, ~0u);
+  issue_scales<T>(c, c.sb_rsrc, 0, ring_at + 2 * T::STAGE, wave, 0, 0);
+  if (kSplit) issue_scales<T>(c, c.sb_rsrc, 1, ring_at + 2 * T::STAGE + T::WINDOW, wave, 0, 0);
+  Pending d{c.b_rsrc, {c.b_off[0], c.b_off[1]}, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int j = 0; j < T::A_DMA; ++j) issue_a<T>(c, j, 0, ring_at, wave, 0);
 #pragma unroll
-    for (int j = 0; j < T::A_DMA + T::B_DMA; ++j)
-      issue_one<T>(c, c.b_rsrc, j, i, b_step, ring_at + i * T::STAGE, wave, ~0u);
-  wait_vm_barrier<T::A_DMA + T::B_DMA>();  // all but step 1's codes landed
+  for (int j = 0; j < T::B_DMA; ++j) issue_b<T>(d, j, b_step, ring_at, wave);
+#pragma unroll
+  for (int j = 0; j < T::A_DMA; ++j) issue_a<T>(c, j, 1, ring_at + T::STAGE, wave, 0);
+  d.kb = 1;
+  wait_vm_barrier<T::A_DMA>();  // step 0 landed
   int stage = 0, window = 0;
   for (int r = 0;; ++r) {
     const int par = r & 1;
@@ -599,7 +625,7 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
     auto tile = [&](auto rows) {
       constexpr int M = decltype(rows)::value;
       f32x16 acc[M ? M : 1][T::NT];
-      kloop<T, M, kSplit>(c, p, nk, b_step, ring, ring_at, wave, stage, window, more,
+      kloop<T, M, kSplit>(c, d, p, nk, b_step, ring, ring_at, wave, stage, window, more,
                           [&] { copies_of(next, par ^ 1); }, acc);
       if constexpr (M > 0)
         store_tile<T, M, kSwiglu, kOut>(g, cur, orow[par], rscale[par], wm, wn, n32, g2, acc);

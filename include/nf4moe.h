@@ -713,7 +713,7 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t R, int
  * expert's rows.  The order of the sums depends on the sizes only: results are the same from
  * call to call.  P = 0 does nothing.  Alignment (else EINVAL): a, blocks and out 16 bytes,
  * scales 1, the others 4.  P below 2^30; the codes of a, and of one expert, with 512 rows more
- * at most 4 GiB (EOVERFLOW).
+ * at most 3.5 GiB (EOVERFLOW).
  * grouped_mx4_gemm_workspace returns 0 for MXFP4 and for invalid arguments. */
 #define NF4MOE_MXFP4 3 /* a_dtype of grouped_mx4_gemm only */
 size_t grouped_mx4_gemm_workspace(int64_t a_rows, int64_t K, int a_dtype);
