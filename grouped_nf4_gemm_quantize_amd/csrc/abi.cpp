@@ -1752,15 +1752,7 @@ int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_
   int cus = 0;
   const int st = cu_count(&cus);
   if (st != NF4MOE_OK) return st;
-  if (a_dtype != NF4MOE_MXFP4) {
-    uint8_t* codes = (uint8_t*)workspace;
-    uint8_t* sc = codes + mx_codes_bytes(a_rows, K);
-    hipError_t err = launch_mx_quantize(a, a_dtype, 1, a_rows, K, false, codes, sc,
-                                        (hipStream_t)stream);
-    if (err != hipSuccess) return hip_fail(err, "mxfp4 quantize launch");
-    g.a = codes;
-    g.a_scales = sc;
-  }
+  g.a_dtype = a_dtype;
   g.a_rows = a_rows;
   g.gather = gather;
   g.gather_div = gather_div;
@@ -1777,6 +1769,16 @@ int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_
   g.out_rows = out_rows;
   g.out = out;
   g.out_dtype = out_dtype;
+  if (a_dtype != NF4MOE_MXFP4 && !mx_gemm_quantises(g)) {
+    uint8_t* codes = (uint8_t*)workspace;
+    uint8_t* sc = codes + mx_codes_bytes(a_rows, K);
+    hipError_t err = launch_mx_quantize(a, a_dtype, 1, a_rows, K, false, codes, sc,
+                                        (hipStream_t)stream);
+    if (err != hipSuccess) return hip_fail(err, "mxfp4 quantize launch");
+    g.a = codes;
+    g.a_scales = sc;
+    g.a_dtype = NF4MOE_MXFP4;
+  }
   hipError_t err = launch_mx_gemm(g, cus, (hipStream_t)stream);
   if (err != hipSuccess) return hip_fail(err, "mxfp4 product launch");
   return ok();

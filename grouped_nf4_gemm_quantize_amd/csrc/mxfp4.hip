@@ -11,96 +11,15 @@
 #include "common.h"
 #include "launch.h"
 #include "mfma_common.h"
+#include "mx_common.h"
 
 namespace nf4moe {
 
 namespace {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// The scale byte of a block whose largest magnitude has these fp32 bits (infinity
-// or NaN: 255), and the power of two the conversion divides by.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
-  const uint32_t e = top >> 23;
-  return top >= 0x7f800000u ? 255u : e > 2u ? e - 2u : 0u;
-}
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-  return __uint_as_float(byte == 0u ? 0x400000u : byte == 255u ? 0x3f800000u : byte << 23);
-}
-
-// fp32 bits of the magnitude of the larger element of a 16-bit pair's magnitudes.
-template <int kT>
-__device__ __forceinline__ uint32_t wide_bits(uint32_t mag16) {
-  if constexpr (kT == kBF16) return mag16 << 16;
-  else return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)mag16));
-}
-
-__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
-  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
-                                                                __builtin_bit_cast(u16x2, b)));
-}
-
-// Two elements (one 16-bit word pair) to the codes of byte kSel of `old`.
-template <int kT, int kSel>
-__device__ __forceinline__ uint32_t cvt_pair(uint32_t old, uint32_t pair, float scale) {
-  if constexpr (kT == kBF16)
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2, pair), scale,
-                                                     kSel);
-  else
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, u32_as_half2(pair), scale, kSel);
-}
-
 template <int kCtrl>
 __device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
   return (uint32_t)dpp_i<kCtrl>((int)v);
-}
-
-// Eight consecutive values of a lane, four lanes a block.
-template <int kT>
-struct Eight {
-  u32x4 v[kT == kF32 ? 2 : 1];
-};
-
-template <int kT>
-__device__ __forceinline__ void load_eight(const void* x, int64_t i, Eight<kT>& o) {
-  const u32x4* p = reinterpret_cast<const u32x4*>(x) + i * (kT == kF32 ? 2 : 1);
-#pragma unroll
-  for (int j = 0; j < (kT == kF32 ? 2 : 1); ++j) o.v[j] = p[j];
-}
-
-template <int kT>
-__device__ __forceinline__ uint32_t eight_codes(const Eight<kT>& x, uint32_t& byte) {
-  uint32_t top;
-  if constexpr (kT == kF32) {
-    top = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, x.v[j >> 2][j & 3] & 0x7fffffffu);
-  } else {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = pk_max_u16(m, x.v[0][j] & 0x7fff7fffu);
-    top = max(m & 0xffffu, m >> 16);
-  }
-  top = max(top, dpp_u<kDppXor1>(top));
-  top = max(top, dpp_u<kDppXor2>(top));
-  if constexpr (kT != kF32) top = wide_bits<kT>(top);
-  byte = scale_byte(top);
-  const float s = scale_value(byte);
-  uint32_t c = 0;
-  if constexpr (kT == kF32) {
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(x.v[0][0]), __uint_as_float(x.v[0][1]), s, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(x.v[0][2]), __uint_as_float(x.v[0][3]), s, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(x.v[1][0]), __uint_as_float(x.v[1][1]), s, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(x.v[1][2]), __uint_as_float(x.v[1][3]), s, 3);
-  } else {
-    c = cvt_pair<kT, 0>(c, x.v[0][0], s);
-    c = cvt_pair<kT, 1>(c, x.v[0][1], s);
-    c = cvt_pair<kT, 2>(c, x.v[0][2], s);
-    c = cvt_pair<kT, 3>(c, x.v[0][3], s);
-  }
-  return byte == 255u ? 0u : c;
 }
 
 // Blocks along the rows: the matrix is a flat run of blocks, eight values a lane.
@@ -112,9 +31,13 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* x, int64_t
   if (i >= n8) return;
   Eight<kT> v;
   load_eight<kT>(x, i, v);
-  uint32_t byte;
-  const uint32_t c = eight_codes<kT>(v, byte);
-  codes[i] = c;
+  uint32_t top = eight_top<kT>(v);  // of the four lanes of a block
+  top = max(top, dpp_u<kDppXor1>(top));
+  top = max(top, dpp_u<kDppXor2>(top));
+  if constexpr (kT != kF32) top = wide_bits<kT>(top);
+  const uint32_t byte = scale_byte(top);
+  const uint32_t c = eight_codes<kT>(v, scale_value(byte));
+  codes[i] = byte == 255u ? 0u : c;
   if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
 }
 
@@ -144,10 +67,10 @@ __global__ __launch_bounds__(256) void mx_quantize_cols_kernel(const void* x, in
   for (int q = 0; q < 4; ++q) {
     uint32_t w = 0;
     if constexpr (kT == kF32) {
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, __uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1]), s, 0);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, __uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3]), s, 1);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, __uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5]), s, 2);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, __uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7]), s, 3);
+      w = cvt_two<0>(w, v[8 * q], v[8 * q + 1], s);
+      w = cvt_two<1>(w, v[8 * q + 2], v[8 * q + 3], s);
+      w = cvt_two<2>(w, v[8 * q + 4], v[8 * q + 5], s);
+      w = cvt_two<3>(w, v[8 * q + 6], v[8 * q + 7], s);
     } else {
       w = cvt_pair<kT, 0>(w, v[8 * q] | v[8 * q + 1] << 16, s);
       w = cvt_pair<kT, 1>(w, v[8 * q + 2] | v[8 * q + 3] << 16, s);

@@ -15,13 +15,13 @@
 #include "common.h"
 #include "launch.h"
 #include "mfma_common.h"
+#include "mx_common.h"
 
 namespace nf4moe {
 
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 #ifndef FENCE
 #define FENCE __builtin_amdgcn_sched_barrier(0)
@@ -30,22 +30,17 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
 
-__shared__ int32_t s_tiles[kMaxExperts + 1];
-__shared__ int32_t s_wsum[kWaves];
-__shared__ float s_part[kWaves][2][16][17];
-
 // Two values rounded to the nearest 16-bit ones.
 template <int kOut>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   if constexpr (kOut == kBF16) return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
   else return pack_half2((_Float16)a, (_Float16)b);
 }
 
-// build_tile_table with the rows at and beyond P left out.
+// build_tile_table with the rows at and beyond P left out; rows[e] is expert e's first row.
 template <int kThreads, int kBM>
 __device__ __forceinline__ void build_tiles(const int32_t* __restrict__ offsets, int E, int P,
-                                            int32_t* tiles, int32_t* wsum, int tid) {
+                                            int32_t* tiles, int32_t* rows, int32_t* wsum, int tid) {
   constexpr int kPer = kMaxExperts / kThreads;
   const int lane = tid & 63, wave = tid >> 6;
   int32_t cnt[kPer];
@@ -54,7 +49,12 @@ __device__ __forceinline__ void build_tiles(const int32_t* __restrict__ offsets,
   for (int u = 0; u < kPer; ++u) {
     const int ex = tid * kPer + u;
     cnt[u] = 0;
-    if (ex < E) cnt[u] = max(0, min(offsets[ex + 1], P) - min(offsets[ex], P) + kBM - 1) / kBM;
+    if (ex < E) {
+      const int from = min(offsets[ex], P), to = min(offsets[ex + 1], P);
+      cnt[u] = max(0, to - from + kBM - 1) / kBM;
+      rows[ex] = from;
+      if (ex == E - 1) rows[E] = to;
+    }
     local += cnt[u];
   }
   int32_t incl = local;
@@ -84,12 +84,60 @@ __device__ __forceinline__ i32x8 codes8(u32x4 v) {
 }  // namespace
 
 // 16 rows of one expert by 32 weight rows (SwiGLU: 16 gate and their 16 up rows) a
-// workgroup; its waves take every fourth 128 of K and join in LDS.
-template <bool kSwiglu, int kOut>
+// workgroup; its waves take every fourth 128 of K, four at a time with their reads in flight
+// together, and join in LDS.  kA: the activations' type, or kCodes for blocks made before; else a
+// lane makes the block it multiplies (32 values of its row) itself, which costs one launch less.
+constexpr int kCodes = 3;
+
+template <int kA>
+struct ABlock {
+  Eight<kA> v[4];
+};
+template <>
+struct ABlock<kCodes> {
+  u32x4 c;
+  uint8_t s;
+};
+
+template <int kA>
+__device__ __forceinline__ void load_block(const MxGemmArgs& g, int64_t block, ABlock<kA>& o) {
+  if constexpr (kA == kCodes) {
+    o.c = reinterpret_cast<const u32x4*>(g.a)[block];
+    o.s = g.a_scales[block];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_eight<kA>(g.a, block * 4 + i, o.v[i]);
+  }
+}
+
+template <int kA>
+__device__ __forceinline__ u32x4 block_codes(const ABlock<kA>& x, int& scale) {
+  if constexpr (kA == kCodes) {
+    scale = x.s;
+    return x.c;
+  } else {
+    uint32_t top = max(max(eight_top<kA>(x.v[0]), eight_top<kA>(x.v[1])),
+                       max(eight_top<kA>(x.v[2]), eight_top<kA>(x.v[3])));
+    if constexpr (kA != kF32) top = wide_bits<kA>(top);
+    const uint32_t byte = scale_byte(top);
+    const float s = scale_value(byte);
+    scale = (int)byte;
+    u32x4 c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = byte == 255u ? 0u : eight_codes<kA>(x.v[i], s);
+    return c;
+  }
+}
+
+template <bool kSwiglu, int kOut, int kA>
 __global__ __launch_bounds__(kThreads) void mx_small_kernel(MxGemmArgs g, int n_tiles) {
+  __shared__ int32_t s_tiles[kMaxExperts + 1];
+  __shared__ int32_t s_first[kMaxExperts + 1];
+  __shared__ int32_t s_wsum[kWaves];
+  __shared__ float s_part[kWaves][2][16][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r16 = lane & 15, q = lane >> 4;
-  build_tiles<kThreads, 16>(g.offsets, g.E, (int)g.P, s_tiles, s_wsum, tid);
+  build_tiles<kThreads, 16>(g.offsets, g.E, (int)g.P, s_tiles, s_first, s_wsum, tid);
   const int N = g.N, I = N >> 1, KB = g.K / 32;
   const int total = s_tiles[g.E] * n_tiles;
   for (int tix = blockIdx.x; tix < total; tix += gridDim.x) {
@@ -100,36 +148,45 @@ __global__ __launch_bounds__(kThreads) void mx_small_kernel(MxGemmArgs g, int n_
       if (s_tiles[mid] <= mt) lo = mid; else hi = mid;
     }
     const int e = lo;
-    const int row0 = g.offsets[e] + (mt - s_tiles[e]) * 16;
-    const int rows = min(16, min(g.offsets[e + 1], (int)g.P) - row0);
+    const int row0 = s_first[e] + (mt - s_tiles[e]) * 16;
+    const int rows = min(16, s_first[e + 1] - row0);
     const int row = row0 + (r16 < rows ? r16 : 0);
     int64_t src = g.gather ? g.gather[row] / g.gather_div : row;
     src = src < 0 ? 0 : src >= g.a_rows ? g.a_rows - 1 : src;
-    const uint8_t* ac = g.a + src * KB * 16;
-    const uint8_t* as = g.a_scales + src * KB;
     // weight rows of the tile's two halves, clamped to valid ones
-    const uint8_t* wc[2];
-    const uint8_t* ws[2];
+    int64_t w_block[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      int n = kSwiglu ? min(nt * 16 + r16, I - 1) + h * I : min(nt * 32 + h * 16 + r16, N - 1);
-      const int64_t at = (int64_t)e * N + n;
-      wc[h] = g.blocks + at * KB * 16;
-      ws[h] = g.scales + at * KB;
+      const int n = kSwiglu ? min(nt * 16 + r16, I - 1) + h * I : min(nt * 32 + h * 16 + r16, N - 1);
+      w_block[h] = ((int64_t)e * N + n) * KB;
     }
     f32x4 acc[2] = {};
-    for (int b0 = wave * 4; b0 < KB; b0 += kWaves * 4) {
-      const int b = min(b0 + q, KB - 1);
-      const bool in = b0 + q < KB;
-      const u32x4 av = *reinterpret_cast<const u32x4*>(ac + (int64_t)b * 16);
-      const int sa = in ? as[b] : 0;
+    constexpr int kRound = kA == kF32 ? 2 : 4;
+    for (int b0 = wave * 4; b0 < KB; b0 += kWaves * 4 * kRound) {
+      ABlock<kA> a[kRound];
+      u32x4 w[kRound][2];
+      uint8_t sw[kRound][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4 wv = *reinterpret_cast<const u32x4*>(wc[h] + (int64_t)b * 16);
-        const int sw = in ? ws[h][b] : 0;
+      for (int i = 0; i < kRound; ++i) {
+        const int b = min(b0 + i * kWaves * 4 + q, KB - 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          w[i][h] = reinterpret_cast<const u32x4*>(g.blocks)[w_block[h] + b];
+          sw[i][h] = g.scales[w_block[h] + b];
+        }
+        load_block<kA>(g, src * KB + b, a[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kRound; ++i) {
+        const bool in = b0 + i * kWaves * 4 + q < KB;  // no scales behind the row's end
+        int sa;
+        const u32x4 av = block_codes<kA>(a[i], sa);
+        sa = in ? sa : 0;
         // the weights first: a lane's four sums are consecutive output columns
-        acc[h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes8(wv), codes8(av), acc[h],
-                                                                  4, 4, 0, sw, 0, sa);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          acc[h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              codes8(w[i][h]), codes8(av), acc[h], 4, 4, 0, in ? sw[i][h] : 0, 0, sa);
       }
     }
     __syncthreads();  // the last tile's sums are read
@@ -188,7 +245,7 @@ struct Tile {
   static constexpr int LDS = 2 * (STAGE + WINDOW);
 };
 
-constexpr int kDescs = 64;  // tiles of a workgroup that are looked up at a time
+constexpr int kDescs = 32;  // tiles of a workgroup that are looked up at a time
 
 // Which rows and columns a tile has.
 struct TileDesc {
@@ -202,18 +259,26 @@ struct Copies {
   uint32_t a_off[T::A_DMA], b_off[2], s_off[T::S_DMA];  // b_off: even and odd copies
 };
 
-// The value of every lane, for a scalar register.
-__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ i32x4 scalar(i32x4 v) {
-  return i32x4{scalar(v.x), scalar(v.y), scalar(v.z), scalar(v.w)};
-}
-
 // The weight copies of a step that are issued in the next one's first half.
 struct Pending {
   i32x4 rsrc;
   uint32_t off[2], where;
   int kb;
 };
+
+// The value of every lane, for a scalar register.
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ i32x4 scalar(i32x4 v) {
+  return i32x4{scalar(v.x), scalar(v.y), scalar(v.z), scalar(v.w)};
+}
+
+// dma16 and dma4 with the resource and the place in scalar registers, wherever they are.
+__device__ __forceinline__ void copy16(i32x4 rsrc, uint32_t voff, uint32_t lds) {
+  dma16(scalar(rsrc), voff, 0, (uint32_t)scalar((int)lds));
+}
+__device__ __forceinline__ void copy4(i32x4 rsrc, uint32_t voff, uint32_t lds) {
+  dma4(scalar(rsrc), voff, 0, (uint32_t)scalar((int)lds));
+}
 
 // An offset that no array has: a copy from there writes zeros and reads no memory.
 constexpr uint32_t kNowhere = 0xf0000000u;
@@ -224,25 +289,25 @@ constexpr uint32_t kNowhere = 0xf0000000u;
 template <class T>
 __device__ __forceinline__ void issue_a(const Copies<T>& c, int j, int kb, uint32_t st, int wave,
                                         uint32_t where) {
-  dma16(c.a_rsrc, (c.a_off[j] + (uint32_t)kb * 128u) | where, 0, st + (wave * T::A_DMA + j) * 1024);
+  copy16(c.a_rsrc, (c.a_off[j] + (uint32_t)kb * 128u) | where, st + (wave * T::A_DMA + j) * 1024);
 }
 template <class T>
 __device__ __forceinline__ void issue_b(const Pending& d, int j, uint32_t b_step, uint32_t st,
                                         int wave) {
-  dma16(d.rsrc, (d.off[j & 1] + ((uint32_t)j * b_step + (uint32_t)d.kb * 128u)) | d.where, 0,
+  copy16(d.rsrc, (d.off[j & 1] + ((uint32_t)j * b_step + (uint32_t)d.kb * 128u)) | d.where,
         st + T::A_BYTES + (wave * T::B_DMA + j) * 1024);
 }
 
 // The scales of step kb on (eight bytes of the row a step): 16 bytes from the aligned word that
 // holds the first.
 template <class T>
-__device__ __forceinline__ void issue_scales(const Copies<T>& c, i32x4 sb_rsrc, int kb, uint32_t window, int wave,
+__device__ __forceinline__ void issue_scales(const Copies<T>& c, int kb, uint32_t window, int wave,
                                              uint32_t trash, uint32_t where) {
 #pragma unroll
   for (int i = 0; i < T::S_DMA; ++i) {
     // rows 64 g .. of the activations, then of the weights
     const int g = min(wave * T::S_DMA + i, T::S_GROUPS - 1);
-    dma16(g * 64 < T::BM ? c.sa_rsrc : sb_rsrc, (c.s_off[i] + (uint32_t)kb * 8u) | where, 0,
+    copy16(g * 64 < T::BM ? c.sa_rsrc : c.sb_rsrc, (c.s_off[i] + (uint32_t)kb * 8u) | where,
           where ? trash : window + g * 1024);
   }
 }
@@ -341,10 +406,6 @@ __device__ __forceinline__ void kloop(Copies<T>& c, Pending& d, const Place<T>& 
   for (int kb = 0; kb < nk; ++kb) {
     if (kb == nk - 2) next_copies();
     const int stage = scalar(stage_), window = scalar(window_);
-    const i32x4 sb_rsrc = scalar(c.sb_rsrc);
-    d.rsrc = scalar(d.rsrc);
-    d.where = scalar((int)d.where);
-    d.kb = scalar(d.kb);
     const char* st = ring + stage * T::STAGE;
     const char* win = ring + 2 * T::STAGE + window * T::WINDOW;
     int sa[T::MT][2], sb[T::NT][2];
@@ -385,7 +446,7 @@ __device__ __forceinline__ void kloop(Copies<T>& c, Pending& d, const Place<T>& 
     // a window read for the last time gives its place (an odd step); at an even one the other
     // window's is free
     const int slot = kSplit || (kb & 1) ? window : window ^ 1;
-    issue_scales<T>(c, sb_rsrc, ahead, ring_at + 2 * T::STAGE + slot * T::WINDOW, wave,
+    issue_scales<T>(c, ahead, ring_at + 2 * T::STAGE + slot * T::WINDOW, wave,
                     ring_at + T::LDS, kSplit || !(ahead & 1) ? where : kNowhere);
     multiply<T, M, 3>(f1, sa, sb, acc, [&](int m) {
 #pragma unroll
@@ -421,6 +482,16 @@ __device__ __forceinline__ void store_run(void* out, int64_t at, const float (&v
   }
 }
 
+// The results of row j of row tile m: its C columns.
+template <class T, int M, bool kSwiglu, int C>
+__device__ __forceinline__ void row_of(const f32x16 (&acc)[M][T::NT], int m, int j, float (&v)[C]) {
+#pragma unroll
+  for (int n = 0; n < C; ++n) {
+    if constexpr (kSwiglu) v[n] = silu_f(acc[m][n][j]) * acc[m][n + C][j];
+    else v[n] = acc[m][n][j];
+  }
+}
+
 // The wave's rows of a tile, from its accumulators, to their places in out.
 template <class T, int M, bool kSwiglu, int kOut>
 __device__ __forceinline__ void store_tile(const MxGemmArgs& g, const TileDesc& d,
@@ -429,13 +500,30 @@ __device__ __forceinline__ void store_tile(const MxGemmArgs& g, const TileDesc& 
                                            const f32x16 (&acc)[M][T::NT]) {
   constexpr int C = kSwiglu ? T::NT / 2 : T::NT;  // columns of a lane
   const int ncols = kSwiglu ? g.N >> 1 : g.N;
-  const int col = (d.n_idx * T::WN + wn) * 32 * C + n32 * C;
+  const int col0 = (d.n_idx * T::WN + wn) * 32 * C, row0 = wm * T::MT * 32;
+  if (!g.scatter && !g.row_scale && row0 + M * 32 <= d.rows && col0 + 32 * C <= ncols &&
+      d.row0 + d.rows <= g.out_rows) {
+    // whole and in order: the rows' places follow from a scalar, the lane's part is the same
+    constexpr int kSize = kOut == kF32 ? 4 : 2;
+    const uint32_t lane_at = (uint32_t)(4 * g2 * ncols + n32 * C) * kSize;
+    char* at = reinterpret_cast<char*>(g.out) + ((int64_t)(d.row0 + row0) * ncols + col0) * kSize;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float v[C];
+        row_of<T, M, kSwiglu, C>(acc, m, j, v);
+        store_run<kOut, C>(at + (int64_t)(m * 32 + 8 * (j / 4) + j % 4) * ncols * kSize + lane_at, 0, v);
+      }
+    return;
+  }
+  const int col = col0 + n32 * C;
   if (col >= ncols) return;  // ncols is a multiple of 16: all of a lane's columns or none
 #pragma unroll
   for (int m = 0; m < M; ++m) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int trow = (wm * T::MT + m) * 32 + 8 * q + 4 * g2;
+      const int trow = row0 + m * 32 + 8 * q + 4 * g2;
       i32x4 o = i32x4{0, 1, 2, 3} + (d.row0 + trow);
       f32x4 rs = {1.f, 1.f, 1.f, 1.f};
       if (g.scatter) o = *reinterpret_cast<const i32x4*>(orow + trow);
@@ -444,12 +532,9 @@ __device__ __forceinline__ void store_tile(const MxGemmArgs& g, const TileDesc& 
       for (int i = 0; i < 4; ++i) {
         if (trow + i >= d.rows || o[i] < 0 || o[i] >= g.out_rows) continue;
         float v[C];
+        row_of<T, M, kSwiglu, C>(acc, m, 4 * q + i, v);
 #pragma unroll
-        for (int n = 0; n < C; ++n) {
-          const int j = 4 * q + i;
-          if constexpr (kSwiglu) v[n] = silu_f(acc[m][n][j]) * acc[m][n + C][j] * rs[i];
-          else v[n] = acc[m][n][j] * rs[i];
-        }
+        for (int n = 0; n < C; ++n) v[n] *= rs[i];
         store_run<kOut, C>(g.out, (int64_t)o[i] * ncols + col, v);
       }
     }
@@ -466,13 +551,14 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
   __shared__ __attribute__((aligned(16))) float rscale[2][T::BM];   // and row scale
   __shared__ TileDesc descs[kDescs];
   __shared__ int32_t tiles[kMaxExperts + 1];
+  __shared__ int32_t first[kMaxExperts + 1];
   __shared__ int32_t wsum[T::WAVES];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / T::WN, wn = wave % T::WN;
   const int n32 = lane & 31, g2 = lane >> 5;
-  build_tiles<T::THREADS, T::BM>(g.offsets, g.E, (int)g.P, tiles, wsum, tid);
+  build_tiles<T::THREADS, T::BM>(g.offsets, g.E, (int)g.P, tiles, first, wsum, tid);
 
   const int N = g.N, I = N >> 1, KB = g.K / 32;
   const int nk = max(2, (KB + 7) / 8);
@@ -524,9 +610,8 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
         const int mid = (lo + hi) >> 1;
         if (tiles[mid] <= mt) lo = mid; else hi = mid;
       }
-      const int row0 = g.offsets[lo] + (mt - tiles[lo]) * T::BM;
-      const int end = min(g.offsets[lo + 1], (int)g.P);
-      descs[tid] = TileDesc{lo, row0, min(T::BM, end - row0), n_idx};
+      const int row0 = first[lo] + (mt - tiles[lo]) * T::BM;
+      descs[tid] = TileDesc{lo, row0, min(T::BM, first[lo + 1] - row0), n_idx};
     }
   };
   auto desc = [&](int r) -> TileDesc {
@@ -541,9 +626,9 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
   auto copy_indices = [&](const TileDesc& d, int par) {
     for (int grp = wave; grp < T::BM / 64; grp += T::WAVES) {
       const uint32_t at = (uint32_t)(d.row0 + min(grp * 64 + lane, d.rows - 1)) * 4u;
-      if (g.gather) dma4(ga_rsrc, at, 0, lds_addr(&srow[par][grp * 64]));
-      if (g.scatter) dma4(sc_rsrc, at, 0, lds_addr(&orow[par][grp * 64]));
-      if (g.row_scale) dma4(rs_rsrc, at, 0, lds_addr(&rscale[par][grp * 64]));
+      if (g.gather) copy4(ga_rsrc, at, lds_addr(&srow[par][grp * 64]));
+      if (g.scatter) copy4(sc_rsrc, at, lds_addr(&orow[par][grp * 64]));
+      if (g.row_scale) copy4(rs_rsrc, at, lds_addr(&rscale[par][grp * 64]));
     }
   };
   auto source = [&](const TileDesc& d, int par, int row) -> uint32_t {
@@ -584,8 +669,8 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
   copy_indices(cur, 0);
   wait_vm_barrier<0>();
   copies_of(cur, 0);
-  issue_scales<T>(c, c.sb_rsrc, 0, ring_at + 2 * T::STAGE, wave, 0, 0);
-  if (kSplit) issue_scales<T>(c, c.sb_rsrc, 1, ring_at + 2 * T::STAGE + T::WINDOW, wave, 0, 0);
+  issue_scales<T>(c, 0, ring_at + 2 * T::STAGE, wave, 0, 0);
+  if (kSplit) issue_scales<T>(c, 1, ring_at + 2 * T::STAGE + T::WINDOW, wave, 0, 0);
   Pending d{c.b_rsrc, {c.b_off[0], c.b_off[1]}, 0, 0};
 #pragma unroll
   for (int j = 0; j < T::A_DMA; ++j) issue_a<T>(c, j, 0, ring_at, wave, 0);
@@ -645,14 +730,22 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
 
 namespace {
 
-template <bool kSwiglu>
+template <bool kSwiglu, int kA>
 void launch_small(const MxGemmArgs& g, dim3 grid, int n_tiles, hipStream_t s) {
   if (g.out_dtype == kF32)
-    hipLaunchKernelGGL((mx_small_kernel<kSwiglu, kF32>), grid, dim3(kThreads), 0, s, g, n_tiles);
+    hipLaunchKernelGGL((mx_small_kernel<kSwiglu, kF32, kA>), grid, dim3(kThreads), 0, s, g, n_tiles);
   else if (g.out_dtype == kBF16)
-    hipLaunchKernelGGL((mx_small_kernel<kSwiglu, kBF16>), grid, dim3(kThreads), 0, s, g, n_tiles);
+    hipLaunchKernelGGL((mx_small_kernel<kSwiglu, kBF16, kA>), grid, dim3(kThreads), 0, s, g, n_tiles);
   else
-    hipLaunchKernelGGL((mx_small_kernel<kSwiglu, kF16>), grid, dim3(kThreads), 0, s, g, n_tiles);
+    hipLaunchKernelGGL((mx_small_kernel<kSwiglu, kF16, kA>), grid, dim3(kThreads), 0, s, g, n_tiles);
+}
+
+template <bool kSwiglu>
+void launch_small(const MxGemmArgs& g, dim3 grid, int n_tiles, hipStream_t s) {
+  if (g.a_dtype == kF32) launch_small<kSwiglu, kF32>(g, grid, n_tiles, s);
+  else if (g.a_dtype == kBF16) launch_small<kSwiglu, kBF16>(g, grid, n_tiles, s);
+  else if (g.a_dtype == kF16) launch_small<kSwiglu, kF16>(g, grid, n_tiles, s);
+  else launch_small<kSwiglu, kCodes>(g, grid, n_tiles, s);
 }
 
 template <class T, bool kSwiglu, bool kSplit>
@@ -690,25 +783,29 @@ using Tile256 = Tile<TILE_BIG>;  // 256 x 256
 #define TILE_SMALL 2, 2, 1, 2, 2
 #endif
 using Tile64 = Tile<TILE_SMALL>;
+#ifndef SMALL_P
+#define SMALL_P 32
+#endif
+bool use_small(const MxGemmArgs& g) { return g.P <= SMALL_P; }
+
 
 }  // namespace
 
+bool mx_gemm_quantises(const MxGemmArgs& g) { return use_small(g); }
+
 hipError_t launch_mx_gemm(const MxGemmArgs& g, int num_cus, hipStream_t s) {
-  const int64_t rows = g.P / std::min<int64_t>(g.E, g.P);  // of an expert, at least
-  if (rows >= 128) {
+  if (use_small(g)) {
+    const int n_tiles = g.swiglu ? (g.N / 2 + 15) / 16 : (g.N + 31) / 32;
+    // an expert's rows begin a tile of their own: at most one more for each that has rows
+    const int64_t tiles = ((g.P + 15) / 16 + std::min<int64_t>(g.E, g.P)) * n_tiles;
+    const dim3 grid((unsigned)std::min<int64_t>(tiles, num_cus * 8));
+    if (g.swiglu) launch_small<true>(g, grid, n_tiles, s);
+    else launch_small<false>(g, grid, n_tiles, s);
+  } else if (g.P / std::min<int64_t>(g.E, g.P) >= 80) {
     launch_tiles<Tile256>(g, num_cus, s);
-    return hipGetLastError();
-  }
-  if (rows >= 24) {
+  } else {
     launch_tiles<Tile64>(g, num_cus, s);
-    return hipGetLastError();
   }
-  const int n_tiles = g.swiglu ? (g.N / 2 + 15) / 16 : (g.N + 31) / 32;
-  // an expert's rows begin a tile of their own: at most one more for each that has rows
-  const int64_t tiles = ((g.P + 15) / 16 + std::min<int64_t>(g.E, g.P)) * n_tiles;
-  const dim3 grid((unsigned)std::min<int64_t>(tiles, num_cus * 8));
-  if (g.swiglu) launch_small<true>(g, grid, n_tiles, s);
-  else launch_small<false>(g, grid, n_tiles, s);
   return hipGetLastError();
 }
 
