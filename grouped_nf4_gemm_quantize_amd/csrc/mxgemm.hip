@@ -83,11 +83,16 @@ __device__ __forceinline__ i32x8 codes8(u32x4 v) {
 
 }  // namespace
 
-// 16 rows of one expert by 32 weight rows (SwiGLU: 16 gate and their 16 up rows) a
-// workgroup; its waves take every fourth 128 of K, four at a time with their reads in flight
-// together, and join in LDS.  kA: the activations' type, or kCodes for blocks made before; else a
-// lane makes the block it multiplies (32 values of its row) itself, which costs one launch less.
+// 16 rows of one expert by 32 weight rows (SwiGLU: 16 gate and their 16 up rows) a workgroup.  Of
+// every 4096 of K a wave takes four runs of 256 (whole lines of the codes, eight scale bytes at
+// a time), whose reads are all in flight while the workgroup lays the rows' blocks into LDS; the
+// waves join in LDS.  kA: the activations' type, or kCodes for blocks made before: making them
+// here costs one launch less.
 constexpr int kCodes = 3;
+constexpr int kSmallRows = 32;  // P of a call, at most
+constexpr int kChunk = 128;     // blocks of K at a time
+constexpr int kRuns = kChunk / 8 / kWaves;
+constexpr int kRowBytes = kChunk * 16 + 16;  // of a row's codes in LDS: 16 rows on 16 bank groups
 
 template <int kA>
 struct ABlock {
@@ -129,30 +134,70 @@ __device__ __forceinline__ u32x4 block_codes(const ABlock<kA>& x, int& scale) {
   }
 }
 
+// The expert, first row and rows of 16-row tile mt, by one wave: 64 experts at a time, a lane's tiles
+// counted over the lanes below it by ballots (an expert has at most kSmallRows / 16).  False
+// behind the last tile.
+__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int E, int P, int mt,
+                                          int lane, int& e, int& row0, int& rows) {
+  int before = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int ex = e0 + lane;
+    const int from = min(ex < E ? offsets[ex] : P, P);
+    const int to = max(from, min(ex < E ? offsets[ex + 1] : P, P));
+    const int n = (to - from + 15) / 16;
+    int below = before, all = 0;
+#pragma unroll
+    for (int k = 1; k <= kSmallRows / 16; ++k) {
+      const uint64_t has = __ballot(n >= k);
+      below += __builtin_amdgcn_mbcnt_hi((uint32_t)(has >> 32),
+                                         __builtin_amdgcn_mbcnt_lo((uint32_t)has, 0));
+      all += __popcll(has);
+    }
+    if (mt < before + all) {
+      const uint64_t mine = __ballot(mt >= below && mt < below + n);
+      const int l = __ffsll((unsigned long long)mine) - 1;
+      e = e0 + l;
+      row0 = __builtin_amdgcn_readlane(from, l) + (mt - __builtin_amdgcn_readlane(below, l)) * 16;
+      rows = min(16, __builtin_amdgcn_readlane(to, l) - row0);
+      return true;
+    }
+    before += all;
+  }
+  return false;
+}
+
+// The scale bytes of blocks b0 .. b0 + 7 of a row of KB; 0 behind the row's end.
+__device__ __forceinline__ uint64_t run_scales(const uint8_t* row, int b0, int KB) {
+  uint64_t v = 0;
+  if (KB >= 8) {
+    // eight bytes at any place, none behind the row
+    const int from = min(b0, KB - 8);
+    __builtin_memcpy(&v, row + from, 8);
+    return v >> (8 * (b0 - from));
+  }
+  for (int i = 0; i < KB; ++i) v |= (uint64_t)row[i] << (8 * i);
+  return v;
+}
+
 template <bool kSwiglu, int kOut, int kA>
 __global__ __launch_bounds__(kThreads) void mx_small_kernel(MxGemmArgs g, int n_tiles) {
-  __shared__ int32_t s_tiles[kMaxExperts + 1];
-  __shared__ int32_t s_first[kMaxExperts + 1];
-  __shared__ int32_t s_wsum[kWaves];
+  __shared__ __attribute__((aligned(16))) char s_codes[16 * kRowBytes];
+  __shared__ uint8_t s_scales[16 * kChunk];
+  __shared__ int32_t s_src[16];
   __shared__ float s_part[kWaves][2][16][17];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q = lane >> 4;
-  build_tiles<kThreads, 16>(g.offsets, g.E, (int)g.P, s_tiles, s_first, s_wsum, tid);
   const int N = g.N, I = N >> 1, KB = g.K / 32;
-  const int total = s_tiles[g.E] * n_tiles;
-  for (int tix = blockIdx.x; tix < total; tix += gridDim.x) {
+  for (int tix = blockIdx.x;; tix += gridDim.x) {
     const int mt = tix / n_tiles, nt = tix - mt * n_tiles;
-    int lo = 0, hi = g.E;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_tiles[mid] <= mt) lo = mid; else hi = mid;
+    int e, row0, rows;
+    if (!find_tile(g.offsets, g.E, (int)g.P, mt, lane, e, row0, rows)) break;
+    if (tid < 16) {
+      const int row = row0 + min(tid, rows - 1);
+      const int s = g.gather ? g.gather[row] / g.gather_div : row;
+      s_src[tid] = min(max(s, 0), (int)g.a_rows - 1);
     }
-    const int e = lo;
-    const int row0 = s_first[e] + (mt - s_tiles[e]) * 16;
-    const int rows = min(16, s_first[e + 1] - row0);
-    const int row = row0 + (r16 < rows ? r16 : 0);
-    int64_t src = g.gather ? g.gather[row] / g.gather_div : row;
-    src = src < 0 ? 0 : src >= g.a_rows ? g.a_rows - 1 : src;
     // weight rows of the tile's two halves, clamped to valid ones
     int64_t w_block[2];
 #pragma unroll
@@ -161,32 +206,49 @@ __global__ __launch_bounds__(kThreads) void mx_small_kernel(MxGemmArgs g, int n_
       w_block[h] = ((int64_t)e * N + n) * KB;
     }
     f32x4 acc[2] = {};
-    constexpr int kRound = kA == kF32 ? 2 : 4;
-    for (int b0 = wave * 4; b0 < KB; b0 += kWaves * 4 * kRound) {
-      ABlock<kA> a[kRound];
-      u32x4 w[kRound][2];
-      uint8_t sw[kRound][2];
+    for (int c0 = 0; c0 < KB; c0 += kChunk) {
+      u32x4 w[kRuns][2][2];
+      uint64_t sw[kRuns][2];
 #pragma unroll
-      for (int i = 0; i < kRound; ++i) {
-        const int b = min(b0 + i * kWaves * 4 + q, KB - 1);
+      for (int i = 0; i < kRuns; ++i) {
+        const int b0 = c0 + (i * kWaves + wave) * 8;
+        if (b0 >= KB) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          w[i][h] = reinterpret_cast<const u32x4*>(g.blocks)[w_block[h] + b];
-          sw[i][h] = g.scales[w_block[h] + b];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            w[i][h][j] = reinterpret_cast<const u32x4*>(g.blocks)[w_block[h] + min(b0 + 4 * j + q, KB - 1)];
+          sw[i][h] = run_scales(g.scales + w_block[h], b0, KB);
         }
-        load_block<kA>(g, src * KB + b, a[i]);
       }
+      __syncthreads();  // s_src is there, the last chunk is read
+      const int here = min(kChunk, KB - c0);
+      for (int x = tid; x < rows * here; x += kThreads) {
+        const int r = x / here, b = x - r * here;
+        ABlock<kA> v;
+        load_block<kA>(g, (int64_t)s_src[r] * KB + c0 + b, v);
+        int scale;
+        *reinterpret_cast<u32x4*>(s_codes + r * kRowBytes + b * 16) = block_codes<kA>(v, scale);
+        s_scales[r * kChunk + b] = (uint8_t)scale;
+      }
+      __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kRound; ++i) {
-        const bool in = b0 + i * kWaves * 4 + q < KB;  // no scales behind the row's end
-        int sa;
-        const u32x4 av = block_codes<kA>(a[i], sa);
-        sa = in ? sa : 0;
-        // the weights first: a lane's four sums are consecutive output columns
+      for (int i = 0; i < kRuns; ++i) {
+        const int b0 = c0 + (i * kWaves + wave) * 8;
+        if (b0 >= KB) break;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          acc[h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              codes8(w[i][h]), codes8(av), acc[h], 4, 4, 0, in ? sw[i][h] : 0, 0, sa);
+        for (int j = 0; j < 2; ++j) {
+          // rows behind the last multiply what lies in LDS; their results are not stored
+          const int b = b0 + 4 * j + q;
+          const u32x4 av = *reinterpret_cast<const u32x4*>(s_codes + r16 * kRowBytes + (b - c0) * 16);
+          const int sa = b < KB ? s_scales[r16 * kChunk + b - c0] : 0;
+          // the weights first: a lane's four sums are consecutive output columns
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            acc[h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                codes8(w[i][h][j]), codes8(av), acc[h], 4, 4, 0,
+                (int)(sw[i][h] >> (8 * (4 * j + q))) & 255, 0, sa);
+        }
       }
     }
     __syncthreads();  // the last tile's sums are read
@@ -197,11 +259,13 @@ __global__ __launch_bounds__(kThreads) void mx_small_kernel(MxGemmArgs g, int n_
     __syncthreads();
     // 16 rows x 32 columns (SwiGLU: 16), two (one) a thread
     const int c = tid & 15, r = tid >> 4;
-    float v[2];
+    if (r >= rows) continue;
+    float v[2] = {0.f, 0.f};
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      v[h] = (s_part[0][h][r][c] + s_part[1][h][r][c]) + (s_part[2][h][r][c] + s_part[3][h][r][c]);
-    if (r < rows) {
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) v[h] += s_part[w][h][r][c];
+    {
       const int i = row0 + r;
       const int64_t o = g.scatter ? g.scatter[i] : i;
       if (o >= 0 && o < g.out_rows) {
@@ -784,7 +848,7 @@ using Tile256 = Tile<TILE_BIG>;  // 256 x 256
 #endif
 using Tile64 = Tile<TILE_SMALL>;
 #ifndef SMALL_P
-#define SMALL_P 32
+#define SMALL_P kSmallRows
 #endif
 bool use_small(const MxGemmArgs& g) { return g.P <= SMALL_P; }
 
