@@ -1769,7 +1769,7 @@ int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_
   g.out_rows = out_rows;
   g.out = out;
   g.out_dtype = out_dtype;
-  if (a_dtype != NF4MOE_MXFP4 && !mx_gemm_quantises(g)) {
+  if (a_dtype != NF4MOE_MXFP4 && !mx_gemm_quantises(g, cus)) {
     uint8_t* codes = (uint8_t*)workspace;
     uint8_t* sc = codes + mx_codes_bytes(a_rows, K);
     hipError_t err = launch_mx_quantize(a, a_dtype, 1, a_rows, K, false, codes, sc,

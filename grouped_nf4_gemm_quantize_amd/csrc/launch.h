@@ -266,7 +266,7 @@ struct MxGemmArgs {
   int out_dtype;
 };
 // Whether the product takes values and makes their codes itself.
-bool mx_gemm_quantises(const MxGemmArgs& g);
+bool mx_gemm_quantises(const MxGemmArgs& g, int num_cus);
 hipError_t launch_mx_gemm(const MxGemmArgs& g, int num_cus, hipStream_t s);
 
 // ---- token rows into expert rows and back (dispatch.hip) ----------------------

@@ -41,47 +41,64 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* x, int64_t
   if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
 }
 
-// Blocks along the columns of [R, K]: a lane takes 32 rows of one column.
-template <int kT>
-__global__ __launch_bounds__(256) void mx_quantize_cols_kernel(const void* x, int64_t R, int64_t K,
-                                                               uint8_t* codes, uint8_t* scales) {
-  const int64_t col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
-  const int64_t rb = ((int64_t)blockIdx.y * 4 + (threadIdx.x >> 6)), blocks = R / 32;
+// Blocks along the columns of [R, K]: a lane takes 32 rows of one column, or of two neighbours as
+// they lie in a word (16-bit values, K even).  A workgroup's eight waves have row blocks beside each
+// other, so that the L2 collects whole lines of a column's codes.
+constexpr int kColWaves = 8;
+
+template <int kT, int kCols>
+__global__ __launch_bounds__(kColWaves * 64) void mx_quantize_cols_kernel(const void* x, int64_t R,
+                                                                          int64_t K, uint8_t* codes,
+                                                                          uint8_t* scales) {
+  const int64_t col = ((int64_t)blockIdx.x * 64 + (threadIdx.x & 63)) * kCols;
+  const int64_t rb = (int64_t)blockIdx.y * kColWaves + (threadIdx.x >> 6), blocks = R / 32;
   if (col >= K || rb >= blocks) return;
   const int64_t e = blockIdx.z;
   const int64_t at = (e * R + rb * 32) * K + col;
   uint32_t v[32];
-  uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     if constexpr (kT == kF32) v[j] = reinterpret_cast<const uint32_t*>(x)[at + j * K];
+    else if constexpr (kCols == 2)
+      v[j] = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(x) + at + j * K);
     else v[j] = reinterpret_cast<const uint16_t*>(x)[at + j * K];
   }
+  uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) top = max(top, v[j] & (kT == kF32 ? 0x7fffffffu : 0x7fffu));
-  if constexpr (kT != kF32) top = wide_bits<kT>(top);
-  const uint32_t byte = scale_byte(top);
-  const float s = scale_value(byte);
-  u32x4 c;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t w = 0;
-    if constexpr (kT == kF32) {
-      w = cvt_two<0>(w, v[8 * q], v[8 * q + 1], s);
-      w = cvt_two<1>(w, v[8 * q + 2], v[8 * q + 3], s);
-      w = cvt_two<2>(w, v[8 * q + 4], v[8 * q + 5], s);
-      w = cvt_two<3>(w, v[8 * q + 6], v[8 * q + 7], s);
-    } else {
-      w = cvt_pair<kT, 0>(w, v[8 * q] | v[8 * q + 1] << 16, s);
-      w = cvt_pair<kT, 1>(w, v[8 * q + 2] | v[8 * q + 3] << 16, s);
-      w = cvt_pair<kT, 2>(w, v[8 * q + 4] | v[8 * q + 5] << 16, s);
-      w = cvt_pair<kT, 3>(w, v[8 * q + 6] | v[8 * q + 7] << 16, s);
-    }
-    c[q] = byte == 255u ? 0u : w;
+  for (int j = 0; j < 32; ++j) {
+    if constexpr (kT == kF32) m = max(m, v[j] & 0x7fffffffu);
+    else m = pk_max_u16(m, v[j] & 0x7fff7fffu);
   }
-  const int64_t ob = (e * K + col) * blocks + rb;
-  reinterpret_cast<u32x4*>(codes)[ob] = c;
-  scales[ob] = (uint8_t)byte;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    uint32_t top = m;
+    if constexpr (kT != kF32) top = wide_bits<kT>(c ? m >> 16 : m & 0xffffu);
+    const uint32_t byte = scale_byte(top);
+    const float s = scale_value(byte);
+    u32x4 o;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t w = 0;
+      if constexpr (kT == kF32) {
+        w = cvt_two<0>(w, v[8 * q], v[8 * q + 1], s);
+        w = cvt_two<1>(w, v[8 * q + 2], v[8 * q + 3], s);
+        w = cvt_two<2>(w, v[8 * q + 4], v[8 * q + 5], s);
+        w = cvt_two<3>(w, v[8 * q + 6], v[8 * q + 7], s);
+      } else {
+        // this column's half of two rows' words
+        constexpr uint32_t kLow = 0x05040100u, kHigh = 0x07060302u;
+        const uint32_t sel = c ? kHigh : kLow;
+        w = cvt_pair<kT, 0>(w, __builtin_amdgcn_perm(v[8 * q + 1], v[8 * q], sel), s);
+        w = cvt_pair<kT, 1>(w, __builtin_amdgcn_perm(v[8 * q + 3], v[8 * q + 2], sel), s);
+        w = cvt_pair<kT, 2>(w, __builtin_amdgcn_perm(v[8 * q + 5], v[8 * q + 4], sel), s);
+        w = cvt_pair<kT, 3>(w, __builtin_amdgcn_perm(v[8 * q + 7], v[8 * q + 6], sel), s);
+      }
+      o[q] = byte == 255u ? 0u : w;
+    }
+    const int64_t ob = (e * K + col + c) * blocks + rb;
+    reinterpret_cast<u32x4*>(codes)[ob] = o;
+    scales[ob] = (uint8_t)byte;
+  }
 }
 
 template <int kSel>
@@ -128,13 +145,21 @@ hipError_t launch_mx_quantize(const void* x, int x_dtype, int64_t E, int64_t R, 
       hipLaunchKernelGGL(mx_quantize_kernel<kF16>, grid, dim3(256), 0, s, x, n8, c, scales);
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)((K + 63) / 64), (unsigned)((R / 32 + 3) / 4), (unsigned)E);
+  const bool pairs = x_dtype != kF32 && K % 2 == 0 && (reinterpret_cast<uintptr_t>(x) & 3) == 0;
+  const int64_t width = pairs ? 128 : 64;
+  const dim3 grid((unsigned)((K + width - 1) / width), (unsigned)((R / 32 + kColWaves - 1) / kColWaves),
+                  (unsigned)E);
+  const dim3 block(kColWaves * 64);
   if (x_dtype == kF32)
-    hipLaunchKernelGGL(mx_quantize_cols_kernel<kF32>, grid, dim3(256), 0, s, x, R, K, codes, scales);
+    hipLaunchKernelGGL((mx_quantize_cols_kernel<kF32, 1>), grid, block, 0, s, x, R, K, codes, scales);
+  else if (x_dtype == kBF16 && pairs)
+    hipLaunchKernelGGL((mx_quantize_cols_kernel<kBF16, 2>), grid, block, 0, s, x, R, K, codes, scales);
   else if (x_dtype == kBF16)
-    hipLaunchKernelGGL(mx_quantize_cols_kernel<kBF16>, grid, dim3(256), 0, s, x, R, K, codes, scales);
+    hipLaunchKernelGGL((mx_quantize_cols_kernel<kBF16, 1>), grid, block, 0, s, x, R, K, codes, scales);
+  else if (pairs)
+    hipLaunchKernelGGL((mx_quantize_cols_kernel<kF16, 2>), grid, block, 0, s, x, R, K, codes, scales);
   else
-    hipLaunchKernelGGL(mx_quantize_cols_kernel<kF16>, grid, dim3(256), 0, s, x, R, K, codes, scales);
+    hipLaunchKernelGGL((mx_quantize_cols_kernel<kF16, 1>), grid, block, 0, s, x, R, K, codes, scales);
   return hipGetLastError();
 }
 

@@ -23,9 +23,6 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-#ifndef FENCE
-#define FENCE __builtin_amdgcn_sched_barrier(0)
-#endif
 
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
@@ -491,19 +488,19 @@ __device__ __forceinline__ void kloop(Copies<T>& c, Pending& d, const Place<T>& 
       for (int j = part(m, T::B_DMA / 2); j < part(m + 1, T::B_DMA / 2); ++j)
         issue_b<T>(d, j, b_step, other, wave);
     });
-    FENCE;
+    __builtin_amdgcn_sched_barrier(0);
     load_frags<T, M>(st, p.ro[2], p, f0);
     multiply<T, M, 1>(f1, sa, sb, acc, [&](int m) {
 #pragma unroll
       for (int j = part(m, T::B_DMA - T::B_DMA / 2); j < part(m + 1, T::B_DMA - T::B_DMA / 2); ++j)
         issue_b<T>(d, j + T::B_DMA / 2, b_step, other, wave);
     });
-    FENCE;
+    __builtin_amdgcn_sched_barrier(0);
     load_frags<T, M>(st, p.ro[3], p, f1);
     multiply<T, M, 2>(f0, sa, sb, acc, nothing);
-    FENCE;
+    __builtin_amdgcn_sched_barrier(0);
     wait_vm_barrier<0>();
-    FENCE;
+    __builtin_amdgcn_sched_barrier(0);
     load_frags<T, M>(ring + (stage ^ 1) * T::STAGE, p.ro[0], p, f0);
     const int ahead = kb + 2 < nk ? kb + 2 : kb + 2 - nk;
     const uint32_t where = scalar(kb + 2 < nk || more ? 0 : (int)kNowhere);
@@ -518,7 +515,7 @@ __device__ __forceinline__ void kloop(Copies<T>& c, Pending& d, const Place<T>& 
         issue_a<T>(c, j, ahead, ring_at + stage * T::STAGE, wave, where);
     });
     d = Pending{c.b_rsrc, {c.b_off[0], c.b_off[1]}, where, ahead};
-    FENCE;
+    __builtin_amdgcn_sched_barrier(0);
     stage_ = stage ^ 1;
     window_ = kSplit || (kb & 1) || kb == nk - 1 ? window ^ 1 : window;
   }
@@ -839,30 +836,30 @@ void launch_tiles(const MxGemmArgs& g, int num_cus, hipStream_t s) {
   }
 }
 
-#ifndef TILE_BIG
-#define TILE_BIG 4, 2, 2, 4, 1
-#endif
-using Tile256 = Tile<TILE_BIG>;  // 256 x 256
-#ifndef TILE_SMALL
-#define TILE_SMALL 2, 2, 1, 2, 2
-#endif
-using Tile64 = Tile<TILE_SMALL>;
-#ifndef SMALL_P
-#define SMALL_P kSmallRows
-#endif
-bool use_small(const MxGemmArgs& g) { return g.P <= SMALL_P; }
+using Tile256 = Tile<4, 2, 2, 4, 1>;  // 256 x 256
+using Tile64 = Tile<2, 2, 1, 2, 2>;   // 64 x 128
+// 16-row tiles of a call, at most: an expert's rows begin one of their own.
+int64_t small_tiles(const MxGemmArgs& g) {
+  const int64_t hit = std::min<int64_t>(g.E, g.P);
+  return (hit + (g.P - hit) / 16) * (g.swiglu ? (g.N / 2 + 15) / 16 : (g.N + 31) / 32);
+}
 
+// One launch of 16-row tiles while they are few, each reading its weights for itself.  Measured,
+// small against quantising and 64-row tiles (us, in a graph): 16 pairs on 64 experts of 2048 x 2048
+// (1024 tiles) 14.1 against 15.9, 24 pairs (1536) 16.9 and 17.3, 32 pairs (2048) 21.9 and 19.4;
+// 32 rows of one 4096 x 4096 (256) 12.1 and 16.6; 24 rows of 28672 x 2048 (1792) 24.2 and 17.6.
+bool use_small(const MxGemmArgs& g, int num_cus) {
+  return g.P <= kSmallRows && small_tiles(g) <= 6 * num_cus;
+}
 
 }  // namespace
 
-bool mx_gemm_quantises(const MxGemmArgs& g) { return use_small(g); }
+bool mx_gemm_quantises(const MxGemmArgs& g, int num_cus) { return use_small(g, num_cus); }
 
 hipError_t launch_mx_gemm(const MxGemmArgs& g, int num_cus, hipStream_t s) {
-  if (use_small(g)) {
+  if (use_small(g, num_cus)) {
     const int n_tiles = g.swiglu ? (g.N / 2 + 15) / 16 : (g.N + 31) / 32;
-    // an expert's rows begin a tile of their own: at most one more for each that has rows
-    const int64_t tiles = ((g.P + 15) / 16 + std::min<int64_t>(g.E, g.P)) * n_tiles;
-    const dim3 grid((unsigned)std::min<int64_t>(tiles, num_cus * 8));
+    const dim3 grid((unsigned)small_tiles(g));
     if (g.swiglu) launch_small<true>(g, grid, n_tiles, s);
     else launch_small<false>(g, grid, n_tiles, s);
   } else if (g.P / std::min<int64_t>(g.E, g.P) >= 80) {
