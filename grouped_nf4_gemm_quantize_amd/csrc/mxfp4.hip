@@ -43,18 +43,25 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* x, int64_t
 
 // Blocks along the columns of [R, K]: a lane takes 32 rows of one column, or of two neighbours as
 // they lie in a word (16-bit values, K even).  A workgroup's eight waves have row blocks beside each
-// other, so that the L2 collects whole lines of a column's codes.
+// other: their codes, 128 bytes of a column, and scales go through LDS and leave as whole
+// lines (16 x 2048 x 2048 bf16: 31.5 us; 46.5 us with a lane's 16 bytes and scale byte stored as they are).
 constexpr int kColWaves = 8;
 
 template <int kT, int kCols>
 __global__ __launch_bounds__(kColWaves * 64) void mx_quantize_cols_kernel(const void* x, int64_t R,
                                                                           int64_t K, uint8_t* codes,
                                                                           uint8_t* scales) {
-  const int64_t col = ((int64_t)blockIdx.x * 64 + (threadIdx.x & 63)) * kCols;
-  const int64_t rb = (int64_t)blockIdx.y * kColWaves + (threadIdx.x >> 6), blocks = R / 32;
-  if (col >= K || rb >= blocks) return;
-  const int64_t e = blockIdx.z;
-  const int64_t at = (e * R + rb * 32) * K + col;
+  constexpr int kStride = kColWaves * 16 + 16;  // of a column's codes in LDS
+  __shared__ __attribute__((aligned(16))) char s_codes[64 * kCols * kStride];
+  __shared__ __attribute__((aligned(8))) uint8_t s_scales[64 * kCols * kColWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col0 = (int64_t)blockIdx.x * 64 * kCols, blocks = R / 32;
+  const int64_t rb0 = (int64_t)blockIdx.y * kColWaves, e = blockIdx.z;
+  const int cols = (int)min((int64_t)64 * kCols, K - col0);
+  const int rbs = (int)min((int64_t)kColWaves, blocks - rb0);
+  // lanes behind the last column or row block read its values again
+  const int c0 = min(lane * kCols, cols - kCols), rb = min(wave, rbs - 1);
+  const int64_t at = (e * R + (rb0 + rb) * 32) * K + col0 + c0;
   uint32_t v[32];
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
@@ -95,9 +102,22 @@ __global__ __launch_bounds__(kColWaves * 64) void mx_quantize_cols_kernel(const 
       }
       o[q] = byte == 255u ? 0u : w;
     }
-    const int64_t ob = (e * K + col + c) * blocks + rb;
-    reinterpret_cast<u32x4*>(codes)[ob] = o;
-    scales[ob] = (uint8_t)byte;
+    *reinterpret_cast<u32x4*>(s_codes + (c0 + c) * kStride + rb * 16) = o;
+    s_scales[(c0 + c) * kColWaves + rb] = (uint8_t)byte;
+  }
+  __syncthreads();
+  // eight threads a column; K and the row blocks set how many columns and blocks there are
+  for (int i = threadIdx.x; i < cols * kColWaves; i += kColWaves * 64) {
+    const int c = i / kColWaves, b = i % kColWaves;
+    if (b >= rbs) continue;
+    const int64_t ob = (e * K + col0 + c) * blocks + rb0 + b;
+    reinterpret_cast<u32x4*>(codes)[ob] = *reinterpret_cast<const u32x4*>(s_codes + c * kStride + b * 16);
+    if (blocks % kColWaves == 0 && (reinterpret_cast<uintptr_t>(scales) & 7) == 0) {
+      if (b == 0)
+        *reinterpret_cast<uint64_t*>(scales + ob) = *reinterpret_cast<const uint64_t*>(s_scales + c * kColWaves);
+    } else {
+      scales[ob] = s_scales[c * kColWaves + b];
+    }
   }
 }
 
