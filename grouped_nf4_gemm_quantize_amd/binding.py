@@ -138,7 +138,8 @@ _SIGNATURES = {
     "mxfp4_quantize": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp,
                                 _c_vp]),
     "mxfp4_dequantize": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_int, _c_vp]),
-    "grouped_mx4_gemm_workspace": (_c_size, [_c_i64, _c_i64, _c_int]),
+    "grouped_mx4_gemm_workspace": (_c_size, [_c_i64, _c_int, _c_int, _c_i64, _c_i64, _c_i64,
+                                             _c_int]),
     "grouped_mx4_gemm": (_c_int, [_c_vp, _c_int, _c_vp, _c_i64, _c_vp, _c_int, _c_vp, _c_vp,
                                   _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp,
                                   _c_vp, _c_int, _c_i64, _c_vp, _c_size, _c_vp]),
@@ -860,7 +861,9 @@ def grouped_gemm_mx4(a, a_scales, blocks, scales, offsets, P: int, gather=None,
     if a_scales is None:
         code = _dtype_code(a.dtype)
         ap = _need(a, "a", dev, (rows, K))
-        ws = _workspace(workspace, lib.grouped_mx4_gemm_workspace(rows, K, code), dev)
+        epi = EPI_SWIGLU if swiglu else EPI_NONE
+        ws = _workspace(workspace,
+                        lib.grouped_mx4_gemm_workspace(rows, code, E, P, N, K, epi), dev)
     else:
         code, ws = MXFP4, None
         ap = _need(a, "a", dev, (rows, K2), torch.uint8)

@@ -1684,9 +1684,10 @@ static size_t mx_codes_bytes(int64_t rows, int64_t K) {
   return align_up((size_t)rows * (size_t)(K / 2), 256);
 }
 
-size_t grouped_mx4_gemm_workspace(int64_t a_rows, int64_t K, int a_dtype) {
-  if (a_rows < 1 || K < 32 || K % 32 || !is_float_dtype(a_dtype) ||
-      a_rows > kMxMaxBytes / (K / 2))
+size_t grouped_mx4_gemm_workspace(int64_t a_rows, int a_dtype, int E, int64_t P, int64_t N,
+                                  int64_t K, int epilogue) {
+  if (a_rows < 1 || K < 32 || K % 32 || !is_float_dtype(a_dtype) || a_rows > kMxMaxBytes / (K / 2) ||
+      E < 1 || P < 1 || N < 16 || mx_gemm_small(E, P, N, epilogue == NF4MOE_EPI_SWIGLU))
     return 0;
   return mx_codes_bytes(a_rows, K) + align_up((size_t)a_rows * (size_t)(K / 32), 256);
 }
@@ -1739,8 +1740,8 @@ int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_
   MxGemmArgs g{};
   g.a = (const uint8_t*)a;
   g.a_scales = a_scales;
-  if (a_dtype != NF4MOE_MXFP4) {
-    const size_t need = grouped_mx4_gemm_workspace(a_rows, K, a_dtype);
+  const size_t need = grouped_mx4_gemm_workspace(a_rows, a_dtype, E, P, N, K, epilogue);
+  if (need > 0) {
     if (workspace == nullptr || ws_bytes < need)
       return fail(NF4MOE_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                   workspace ? ws_bytes : (size_t)0);
@@ -1769,7 +1770,7 @@ int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_
   g.out_rows = out_rows;
   g.out = out;
   g.out_dtype = out_dtype;
-  if (a_dtype != NF4MOE_MXFP4 && !mx_gemm_quantises(g, cus)) {
+  if (need > 0) {
     uint8_t* codes = (uint8_t*)workspace;
     uint8_t* sc = codes + mx_codes_bytes(a_rows, K);
     hipError_t err = launch_mx_quantize(a, a_dtype, 1, a_rows, K, false, codes, sc,

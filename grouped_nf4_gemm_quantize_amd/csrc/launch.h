@@ -246,7 +246,7 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 constexpr int64_t kMxMaxBytes = 0xe0000000;  // of the activations' codes and of one expert's
 constexpr int64_t kMxTileRows = 512;         // rows behind a matrix's end whose places are computed
 struct MxGemmArgs {
-  const uint8_t* a;         // [a_rows, K / 2] codes, or values where mx_gemm_quantises
+  const uint8_t* a;         // [a_rows, K / 2] codes, or values where mx_gemm_small
   const uint8_t* a_scales;  // [a_rows, K / 32], null for values
   int a_dtype;              // kF32, kBF16, kF16, or 3 for codes
   int64_t a_rows;
@@ -265,8 +265,8 @@ struct MxGemmArgs {
   void* out;
   int out_dtype;
 };
-// Whether the product takes values and makes their codes itself.
-bool mx_gemm_quantises(const MxGemmArgs& g, int num_cus);
+// Whether a call has few enough rows for the kernel that takes values too and makes their codes.
+bool mx_gemm_small(int E, int64_t P, int64_t N, bool swiglu);
 hipError_t launch_mx_gemm(const MxGemmArgs& g, int num_cus, hipStream_t s);
 
 // ---- token rows into expert rows and back (dispatch.hip) ----------------------

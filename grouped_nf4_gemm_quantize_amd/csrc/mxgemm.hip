@@ -838,28 +838,30 @@ void launch_tiles(const MxGemmArgs& g, int num_cus, hipStream_t s) {
 
 using Tile256 = Tile<4, 2, 2, 4, 1>;  // 256 x 256
 using Tile64 = Tile<2, 2, 1, 2, 2>;   // 64 x 128
-// 16-row tiles of a call, at most: an expert's rows begin one of their own.
-int64_t small_tiles(const MxGemmArgs& g) {
-  const int64_t hit = std::min<int64_t>(g.E, g.P);
-  return (hit + (g.P - hit) / 16) * (g.swiglu ? (g.N / 2 + 15) / 16 : (g.N + 31) / 32);
+// Columns of a 16-row tile's workgroup, and the tiles of a call, at most: an expert's rows begin one
+// of their own.
+int small_n_tiles(int64_t N, bool swiglu) { return (int)(swiglu ? (N / 2 + 15) / 16 : (N + 31) / 32); }
+int64_t small_tiles(int E, int64_t P, int64_t N, bool swiglu) {
+  const int64_t hit = std::min<int64_t>(E, P);
+  return (hit + (P - hit) / 16) * small_n_tiles(N, swiglu);
 }
+
+}  // namespace
 
 // One launch of 16-row tiles while they are few, each reading its weights for itself.  Measured,
 // small against quantising and 64-row tiles (us, in a graph): 16 pairs on 64 experts of 2048 x 2048
 // (1024 tiles) 14.1 against 15.9, 24 pairs (1536) 16.9 and 17.3, 32 pairs (2048) 21.9 and 19.4;
 // 32 rows of one 4096 x 4096 (256) 12.1 and 16.6; 24 rows of 28672 x 2048 (1792) 24.2 and 17.6.
-bool use_small(const MxGemmArgs& g, int num_cus) {
-  return g.P <= kSmallRows && small_tiles(g) <= 6 * num_cus;
+bool mx_gemm_small(int E, int64_t P, int64_t N, bool swiglu) {
+  return P <= kSmallRows && small_tiles(E, P, N, swiglu) <= 1536;
 }
 
-}  // namespace
-
-bool mx_gemm_quantises(const MxGemmArgs& g, int num_cus) { return use_small(g, num_cus); }
-
+// 256-row tiles from 80 rows an expert on.  Measured, 64 against 256 (us, 64 experts of 2048 x 2048):
+// 32 rows each 28.6 and 33.2, 64 rows 32.3 and 40.7, 96 rows 43.8 and 36.6, 128 rows 46.6 and 37.6.
 hipError_t launch_mx_gemm(const MxGemmArgs& g, int num_cus, hipStream_t s) {
-  if (use_small(g, num_cus)) {
-    const int n_tiles = g.swiglu ? (g.N / 2 + 15) / 16 : (g.N + 31) / 32;
-    const dim3 grid((unsigned)small_tiles(g));
+  if (mx_gemm_small(g.E, g.P, g.N, g.swiglu)) {
+    const int n_tiles = small_n_tiles(g.N, g.swiglu);
+    const dim3 grid((unsigned)small_tiles(g.E, g.P, g.N, g.swiglu));
     if (g.swiglu) launch_small<true>(g, grid, n_tiles, s);
     else launch_small<false>(g, grid, n_tiles, s);
   } else if (g.P / std::min<int64_t>(g.E, g.P) >= 80) {

@@ -707,16 +707,19 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t R, int
  *                 [0, out_rows) are not written (as without scatter), two rows to one place give
  *                 one or a mix of them;
  *   out           [out_rows, N or I] F32, BF16 or F16; no input of the call (EINVAL);
- *   workspace     grouped_mx4_gemm_workspace(a_rows, K, a_dtype) bytes, 256-byte aligned (NULL
- *                 for MXFP4 activations).  Two calls must not share it while both run.
+ *   workspace     grouped_mx4_gemm_workspace(a_rows, a_dtype, E, P, N, K, epilogue) bytes,
+ *                 256-byte aligned (NULL for 0, as for MXFP4 activations and for few rows, whose
+ *                 blocks are made in the product's launch).  Two calls must not share it while
+ *                 both run.
  * Scale byte 255 on either side makes what it multiplies NaN: its row, or its column for the
  * expert's rows.  The order of the sums depends on the sizes only: results are the same from
  * call to call.  P = 0 does nothing.  Alignment (else EINVAL): a, blocks and out 16 bytes,
  * scales 1, the others 4.  P below 2^30; the codes of a, and of one expert, with 512 rows more
  * at most 3.5 GiB (EOVERFLOW).
- * grouped_mx4_gemm_workspace returns 0 for MXFP4 and for invalid arguments. */
+ * The query gives 0 for invalid arguments too. */
 #define NF4MOE_MXFP4 3 /* a_dtype of grouped_mx4_gemm only */
-size_t grouped_mx4_gemm_workspace(int64_t a_rows, int64_t K, int a_dtype);
+size_t grouped_mx4_gemm_workspace(int64_t a_rows, int a_dtype, int E, int64_t P, int64_t N,
+                                  int64_t K, int epilogue);
 int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_t a_rows,
                      const int32_t* gather, int gather_div, const uint8_t* blocks,
                      const uint8_t* scales, const int32_t* expert_offsets, int E, int64_t P,

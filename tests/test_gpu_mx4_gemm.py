@@ -356,6 +356,6 @@ def test_refusals_of_the_binding(gpu_lib):
     with pytest.raises(gpu_lib.Nf4MoeError):
         f(a, sa, w, sw, off, 9)  # a has 8 rows
     with pytest.raises(gpu_lib.Nf4MoeError):
-        f(torch.randn(8, 64, device=DEV), None, w, sw, off, 8,
+        f(torch.randn(64, 64, device=DEV), None, w, sw, off, 64,
           workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     assert f(a[:0], sa[:0], w, sw, off, 0).shape == (0, 32)

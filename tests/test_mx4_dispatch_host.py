@@ -53,7 +53,7 @@ def test_dequantize_refuses(lib, status, changes):
 GEMM = dict(a=at(0), ad=3, sa=at(1), rows=8, gather=at(2), div=2, blocks=at(3), scales=at(4),
             off=at(5), E=4, P=16, N=64, K=96, epi=0, rs=at(6), scatter=at(7), out=at(8), od=1,
             out_rows=16, ws=None, wsb=0, stream=None)
-WIDE = dict(ad=1, sa=None, ws=at(9), wsb=1 << 16)
+WIDE = dict(ad=1, sa=None, P=256, out_rows=256, ws=at(9), wsb=1 << 16)
 
 
 @pytest.mark.parametrize("status,changes", [
@@ -88,11 +88,14 @@ def test_product_of_no_rows(lib):
 
 
 def test_product_workspace(lib):
-    f = lib.grouped_mx4_gemm_workspace
-    assert f(8, 96, 3) == 0 and f(0, 96, 1) == 0 and f(8, 80, 1) == 0 and f(8, 0, 1) == 0
-    assert f(-1, 96, 1) == 0 and f(8, 96, 7) == 0
-    assert f(8, 96, 1) >= 8 * 48 + 8 * 3
-    assert f(1 << 20, 4096, 0) >= (1 << 20) * (2048 + 128)
+    args = dict(rows=64, ad=1, E=4, P=256, N=64, K=96, epi=0)
+    f = lambda **kw: lib.grouped_mx4_gemm_workspace(*dict(args, **kw).values())  # noqa: E731
+    assert f() >= 64 * 48 + 64 * 3 and f(ad=0, rows=1 << 20, K=4096) >= (1 << 20) * (2048 + 128)
+    assert f(P=8) == 0  # few rows: made in the product's launch
+    assert f(P=32, N=1 << 20) > 0
+    for bad in (dict(ad=3), dict(rows=0), dict(K=80), dict(K=0), dict(rows=-1), dict(ad=7),
+                dict(P=0), dict(E=0), dict(N=0), dict(rows=1 << 40)):
+        assert f(**bad) == 0, bad
 
 
 DISP = dict(x=at(0), xd=1, pos=at(1), w=at(2), T=4, k=2, R=8, H=64, rows=at(3), rd=2, stream=None)
