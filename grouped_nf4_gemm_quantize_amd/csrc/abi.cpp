@@ -1648,8 +1648,8 @@ int mxfp4_quantize(const void* x, int x_dtype, int64_t E, int64_t R, int64_t K, 
                 (long long)(transpose ? R : K));
   if (E > kMxMaxElems || R > kMxMaxElems / E || K > kMxMaxElems / E / R)
     return fail(NF4MOE_EOVERFLOW, "E*R*K is too large");
-  if (transpose && (E > 65535 || K > ((int64_t)1 << 31) || R > ((int64_t)1 << 22)))
-    return fail(NF4MOE_EOVERFLOW, "transposed: E up to 65535, R up to 2^22, K up to 2^31");
+  if (transpose && (E > 65535 || K > ((int64_t)1 << 28) || R > ((int64_t)1 << 23)))
+    return fail(NF4MOE_EOVERFLOW, "transposed: E up to 65535, R up to 2^23, K up to 2^28");
   if (is_any(codes, {x, scales}) || scales == x)
     return fail(NF4MOE_EINVAL, "codes and scales must not be x or each other");
   if (!aligned(x, transpose ? dtype_bytes(x_dtype) : 16) || !aligned(codes, 16))

@@ -11,6 +11,8 @@
 // All go by token, so that a token's row is read (or written) once for its k pairs.
 // Bound by memory.
 
+#include <algorithm>
+
 #include "common.h"
 #include "launch.h"
 #include "mfma_common.h"
@@ -47,20 +49,21 @@ template <int kX, int kRows>
 __global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs g, int c8, int toks) {
   const int tl = c8 < 256 ? threadIdx.x / c8 : 0;
   const int c0 = threadIdx.x - tl * c8;
-  const int64_t t = (int64_t)blockIdx.x * toks + tl;
-  if (tl >= toks || t >= g.T) return;
-  const int32_t* pos = g.pos + t * g.k;
-  for (int c = c0; c < c8; c += 256) {
-    float v[8];
-    load8<kX>(g.x, t * g.H + c * 8, v);
-    for (int j = 0; j < g.k; ++j) {
-      const int32_t at = pos[j];
-      if (!has_row(at, g.R)) continue;
-      float o[8];
-      const float w = g.w ? g.w[t * g.k + j] : 1.f;
+  if (tl >= toks) return;
+  for (int64_t t = (int64_t)blockIdx.x * toks + tl; t < g.T; t += (int64_t)gridDim.x * toks) {
+    const int32_t* pos = g.pos + t * g.k;
+    for (int c = c0; c < c8; c += 256) {
+      float v[8];
+      load8<kX>(g.x, t * g.H + c * 8, v);
+      for (int j = 0; j < g.k; ++j) {
+        const int32_t at = pos[j];
+        if (!has_row(at, g.R)) continue;
+        float o[8];
+        const float w = g.w ? g.w[t * g.k + j] : 1.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = g.w ? w * v[i] : v[i];
-      store8<kRows>(g.out, (int64_t)at * g.H + c * 8, o);
+        for (int i = 0; i < 8; ++i) o[i] = g.w ? w * v[i] : v[i];
+        store8<kRows>(g.out, (int64_t)at * g.H + c * 8, o);
+      }
     }
   }
 }
@@ -69,21 +72,22 @@ template <int kRows, int kY>
 __global__ __launch_bounds__(256) void combine_rows_kernel(DispatchArgs g, int c8, int toks) {
   const int tl = c8 < 256 ? threadIdx.x / c8 : 0;
   const int c0 = threadIdx.x - tl * c8;
-  const int64_t t = (int64_t)blockIdx.x * toks + tl;
-  if (tl >= toks || t >= g.T) return;
-  const int32_t* pos = g.pos + t * g.k;
-  for (int c = c0; c < c8; c += 256) {
-    float y[8] = {};
-    for (int j = 0; j < g.k; ++j) {
-      const int32_t at = pos[j];
-      if (!has_row(at, g.R)) continue;
-      float v[8];
-      load8<kRows>(g.x, (int64_t)at * g.H + c * 8, v);
-      const float w = g.w ? g.w[t * g.k + j] : 1.f;
+  if (tl >= toks) return;
+  for (int64_t t = (int64_t)blockIdx.x * toks + tl; t < g.T; t += (int64_t)gridDim.x * toks) {
+    const int32_t* pos = g.pos + t * g.k;
+    for (int c = c0; c < c8; c += 256) {
+      float y[8] = {};
+      for (int j = 0; j < g.k; ++j) {
+        const int32_t at = pos[j];
+        if (!has_row(at, g.R)) continue;
+        float v[8];
+        load8<kRows>(g.x, (int64_t)at * g.H + c * 8, v);
+        const float w = g.w ? g.w[t * g.k + j] : 1.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] += w * v[i];
+        for (int i = 0; i < 8; ++i) y[i] += w * v[i];
+      }
+      store8<kY>(g.out, t * g.H + c * 8, y);
     }
-    store8<kY>(g.out, t * g.H + c * 8, y);
   }
 }
 
@@ -91,43 +95,44 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(DispatchArgs g, int c
 template <int kDy, int kRows, int kD>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(DispatchArgs g, int c8) {
   __shared__ float s_sum[4][8];
-  const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int32_t* pos = g.pos + t * g.k;
-  for (int j0 = 0; j0 < g.k; j0 += 8) {
-    float sum[8] = {};
-    for (int c = threadIdx.x; c < c8; c += 256) {
-      float dy[8];
-      load8<kDy>(g.x, t * g.H + c * 8, dy);
+  for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
+    const int32_t* pos = g.pos + t * g.k;
+    for (int j0 = 0; j0 < g.k; j0 += 8) {
+      float sum[8] = {};
+      for (int c = threadIdx.x; c < c8; c += 256) {
+        float dy[8];
+        load8<kDy>(g.x, t * g.H + c * 8, dy);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int32_t at = j0 + j < g.k ? pos[j0 + j] : -1;
-        if (!has_row(at, g.R)) continue;
-        const int64_t i0 = (int64_t)at * g.H + c * 8;
-        float v[8];
-        load8<kRows>(g.rows, i0, v);
+        for (int j = 0; j < 8; ++j) {
+          const int32_t at = j0 + j < g.k ? pos[j0 + j] : -1;
+          if (!has_row(at, g.R)) continue;
+          const int64_t i0 = (int64_t)at * g.H + c * 8;
+          float v[8];
+          load8<kRows>(g.rows, i0, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[j] += dy[i] * v[i];
-        if (g.out) {
-          const float w = g.w ? g.w[t * g.k + j0 + j] : 1.f;
-          float o[8];
+          for (int i = 0; i < 8; ++i) sum[j] += dy[i] * v[i];
+          if (g.out) {
+            const float w = g.w ? g.w[t * g.k + j0 + j] : 1.f;
+            float o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = w * dy[i];
-          store8<kD>(g.out, i0, o);
+            for (int i = 0; i < 8; ++i) o[i] = w * dy[i];
+            store8<kD>(g.out, i0, o);
+          }
         }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float s = wave_sum(sum[j]);
-      if (lane == 0) s_sum[wave][j] = s;
+      for (int j = 0; j < 8; ++j) {
+        const float s = wave_sum(sum[j]);
+        if (lane == 0) s_sum[wave][j] = s;
+      }
+      __syncthreads();
+      if (threadIdx.x < 8 && j0 + (int)threadIdx.x < g.k) {
+        const int j = threadIdx.x;
+        g.dw[t * g.k + j0 + j] = (s_sum[0][j] + s_sum[1][j]) + (s_sum[2][j] + s_sum[3][j]);
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (threadIdx.x < 8 && j0 + (int)threadIdx.x < g.k) {
-      const int j = threadIdx.x;
-      g.dw[t * g.k + j0 + j] = (s_sum[0][j] + s_sum[1][j]) + (s_sum[2][j] + s_sum[3][j]);
-    }
-    __syncthreads();
   }
 }
 
@@ -135,42 +140,42 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(DispatchArgs g, int c8
 template <bool kRenorm>
 __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs g) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= g.T) return;
-  const float* l = g.logits + t * g.E;
-  int id = -1;
-  float dw = 0.f;
-  if (lane < g.k) {
-    id = g.ids[t * g.k + lane];
-    if (id < 0 || id >= g.E) id = -1;
-    if (id >= 0) dw = g.dw[t * g.k + lane];
-  }
-  const float mine = id >= 0 ? l[id] : -INFINITY;
-  float top = mine, all = 0.f;
-  if constexpr (!kRenorm) {
-    for (int e = lane; e < g.E; e += 64) top = fmaxf(top, l[e]);
-  }
-  top = wave_max(top);
-  const float ex = id >= 0 ? __expf(mine - top) : 0.f;
-  if constexpr (kRenorm) {
-    all = wave_sum(ex);
-  } else {
-    for (int e = lane; e < g.E; e += 64) all += __expf(l[e] - top);
-    all = wave_sum(all);
-  }
-  const float w = id >= 0 ? ex / all : 0.f;
-  const float mean = wave_sum(w * dw);
-  const float mine_g = kRenorm ? w * (dw - mean) : dw;
-  for (int e = lane; e - lane < g.E; e += 64) {
-    float v = 0.f;
-    for (int j = 0; j < g.k; ++j) {
-      const int ij = __builtin_amdgcn_readlane(id, j);
-      const float gj = lane_f(mine_g, j);
-      if (ij == e) v += gj;
+  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < g.T; t += (int64_t)gridDim.x * 4) {
+    const float* l = g.logits + t * g.E;
+    int id = -1;
+    float dw = 0.f;
+    if (lane < g.k) {
+      id = g.ids[t * g.k + lane];
+      if (id < 0 || id >= g.E) id = -1;
+      if (id >= 0) dw = g.dw[t * g.k + lane];
     }
-    if (e < g.E) {
-      if constexpr (!kRenorm) v = __expf(l[e] - top) / all * (v - mean);
-      g.dlogits[t * g.E + e] = v;
+    const float mine = id >= 0 ? l[id] : -INFINITY;
+    float top = mine, all = 0.f;
+    if constexpr (!kRenorm) {
+      for (int e = lane; e < g.E; e += 64) top = fmaxf(top, l[e]);
+    }
+    top = wave_max(top);
+    const float ex = id >= 0 ? expf(mine - top) : 0.f;
+    if constexpr (kRenorm) {
+      all = wave_sum(ex);
+    } else {
+      for (int e = lane; e < g.E; e += 64) all += expf(l[e] - top);
+      all = wave_sum(all);
+    }
+    const float w = id >= 0 ? ex / all : 0.f;
+    const float mean = wave_sum(w * dw);
+    const float mine_g = kRenorm ? w * (dw - mean) : dw;
+    for (int e = lane; e - lane < g.E; e += 64) {
+      float v = 0.f;
+      for (int j = 0; j < g.k; ++j) {
+        const int ij = __builtin_amdgcn_readlane(id, j);
+        const float gj = lane_f(mine_g, j);
+        if (ij == e) v += gj;
+      }
+      if (e < g.E) {
+        if constexpr (!kRenorm) v = expf(l[e] - top) / all * (v - mean);
+        g.dlogits[t * g.E + e] = v;
+      }
     }
   }
 }
@@ -189,11 +194,14 @@ namespace {
     __VA_ARGS__;                               \
   }
 
+// Workgroups of 256; a grid's threads are counted in 32 bits.
+unsigned groups(int64_t n) { return (unsigned)std::min<int64_t>(n, 1 << 22); }
+
 }  // namespace
 
 hipError_t launch_dispatch(const DispatchArgs& g, hipStream_t s) {
   const int c8 = g.H / 8, toks = c8 < 256 ? 256 / c8 : 1;
-  const dim3 grid((unsigned)((g.T + toks - 1) / toks));
+  const dim3 grid(groups((g.T + toks - 1) / toks));
   NF4MOE_BY_TYPE(g.x_dtype, kX, NF4MOE_BY_TYPE(g.out_dtype, kO,
       hipLaunchKernelGGL((dispatch_kernel<kX, kO>), grid, dim3(256), 0, s, g, c8, toks)))
   return hipGetLastError();
@@ -201,21 +209,21 @@ hipError_t launch_dispatch(const DispatchArgs& g, hipStream_t s) {
 
 hipError_t launch_combine_rows(const DispatchArgs& g, hipStream_t s) {
   const int c8 = g.H / 8, toks = c8 < 256 ? 256 / c8 : 1;
-  const dim3 grid((unsigned)((g.T + toks - 1) / toks));
+  const dim3 grid(groups((g.T + toks - 1) / toks));
   NF4MOE_BY_TYPE(g.x_dtype, kX, NF4MOE_BY_TYPE(g.out_dtype, kO,
       hipLaunchKernelGGL((combine_rows_kernel<kX, kO>), grid, dim3(256), 0, s, g, c8, toks)))
   return hipGetLastError();
 }
 
 hipError_t launch_combine_bwd(const DispatchArgs& g, hipStream_t s) {
-  const dim3 grid((unsigned)g.T);
+  const dim3 grid(groups(g.T));
   NF4MOE_BY_TYPE(g.x_dtype, kX, NF4MOE_BY_TYPE(g.rows_dtype, kR, NF4MOE_BY_TYPE(g.out_dtype, kO,
       hipLaunchKernelGGL((combine_bwd_kernel<kX, kR, kO>), grid, dim3(256), 0, s, g, g.H / 8))))
   return hipGetLastError();
 }
 
 hipError_t launch_route_bwd(const RouteBwdArgs& g, hipStream_t s) {
-  const dim3 grid((unsigned)((g.T + 3) / 4));
+  const dim3 grid(groups((g.T + 3) / 4));
   if (g.renormalize)
     hipLaunchKernelGGL(route_bwd_kernel<true>, grid, dim3(256), 0, s, g);
   else

@@ -237,7 +237,7 @@ struct MatvecArgs {
 hipError_t launch_matvec(const MatvecArgs& a, int num_cus, hipStream_t s);
 
 // ---- MXFP4 blocks and their product (mxfp4.hip, mxgemm.hip) -------------------
-constexpr int64_t kMxMaxElems = (int64_t)1 << 41;  // of one call: 2^30 workgroups of 2048
+constexpr int64_t kMxMaxElems = (int64_t)1 << 41;  // of one call
 hipError_t launch_mx_quantize(const void* x, int x_dtype, int64_t E, int64_t R, int64_t K,
                               bool cols, uint8_t* codes, uint8_t* scales, hipStream_t s);
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, void* out,

@@ -8,6 +8,8 @@
 //
 // Bound by memory: 2.53 bytes an element for bf16 one way, and the same back.
 
+#include <algorithm>
+
 #include "common.h"
 #include "launch.h"
 #include "mfma_common.h"
@@ -26,19 +28,19 @@ __device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
 template <int kT>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* x, int64_t n8,
                                                           uint32_t* codes, uint8_t* scales) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   // n8 is a multiple of 4, so the lanes of a block are in or out together
-  if (i >= n8) return;
-  Eight<kT> v;
-  load_eight<kT>(x, i, v);
-  uint32_t top = eight_top<kT>(v);  // of the four lanes of a block
-  top = max(top, dpp_u<kDppXor1>(top));
-  top = max(top, dpp_u<kDppXor2>(top));
-  if constexpr (kT != kF32) top = wide_bits<kT>(top);
-  const uint32_t byte = scale_byte(top);
-  const uint32_t c = eight_codes<kT>(v, scale_value(byte));
-  codes[i] = byte == 255u ? 0u : c;
-  if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
+    Eight<kT> v;
+    load_eight<kT>(x, i, v);
+    uint32_t top = eight_top<kT>(v);  // of the four lanes of a block
+    top = max(top, dpp_u<kDppXor1>(top));
+    top = max(top, dpp_u<kDppXor2>(top));
+    if constexpr (kT != kF32) top = wide_bits<kT>(top);
+    const uint32_t byte = scale_byte(top);
+    const uint32_t c = eight_codes<kT>(v, scale_value(byte));
+    codes[i] = byte == 255u ? 0u : c;
+    if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+  }
 }
 
 // Blocks along the columns of [R, K]: a lane takes 32 rows of one column, or of two neighbours as
@@ -132,30 +134,33 @@ template <int kOut>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* codes,
                                                             const uint8_t* scales, int64_t n8,
                                                             void* out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n8) return;
-  const uint32_t c = codes[i];
-  const uint32_t byte = scales[i >> 2];
-  const float s = scale_value(byte);
-  float v[8];
-  two_values<0>(c, s, v);
-  two_values<1>(c, s, v + 2);
-  two_values<2>(c, s, v + 4);
-  two_values<3>(c, s, v + 6);
-  if (byte == 255u) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
+    const uint32_t c = codes[i];
+    const uint32_t byte = scales[i >> 2];
+    const float s = scale_value(byte);
+    float v[8];
+    two_values<0>(c, s, v);
+    two_values<1>(c, s, v + 2);
+    two_values<2>(c, s, v + 4);
+    two_values<3>(c, s, v + 6);
+    if (byte == 255u) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(0x7fc00000u);
+      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(0x7fc00000u);
+    }
+    store8<kOut>(out, i * 8, v);
   }
-  store8<kOut>(out, i * 8, v);
 }
 
 }  // namespace
+
+// Workgroups of 256 for n lanes; a grid's threads are counted in 32 bits.
+static unsigned flat_grid(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 22); }
 
 hipError_t launch_mx_quantize(const void* x, int x_dtype, int64_t E, int64_t R, int64_t K,
                               bool cols, uint8_t* codes, uint8_t* scales, hipStream_t s) {
   if (!cols) {
     const int64_t n8 = E * R * K / 8;
-    const dim3 grid((unsigned)((n8 + 255) / 256));
+    const dim3 grid(flat_grid(n8));
     uint32_t* c = reinterpret_cast<uint32_t*>(codes);
     if (x_dtype == kF32)
       hipLaunchKernelGGL(mx_quantize_kernel<kF32>, grid, dim3(256), 0, s, x, n8, c, scales);
@@ -186,7 +191,7 @@ hipError_t launch_mx_quantize(const void* x, int x_dtype, int64_t E, int64_t R, 
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, void* out,
                                 int out_dtype, hipStream_t s) {
   const int64_t n8 = n / 8;
-  const dim3 grid((unsigned)((n8 + 255) / 256));
+  const dim3 grid(flat_grid(n8));
   const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
   if (out_dtype == kF32)
     hipLaunchKernelGGL(mx_dequantize_kernel<kF32>, grid, dim3(256), 0, s, c, scales, n8, out);

@@ -47,8 +47,8 @@ __device__ __forceinline__ void build_tiles(const int32_t* __restrict__ offsets,
     const int ex = tid * kPer + u;
     cnt[u] = 0;
     if (ex < E) {
-      const int from = min(offsets[ex], P), to = min(offsets[ex + 1], P);
-      cnt[u] = max(0, to - from + kBM - 1) / kBM;
+      const int from = max(0, min(offsets[ex], P)), to = max(from, min(offsets[ex + 1], P));
+      cnt[u] = (to - from + kBM - 1) / kBM;
       rows[ex] = from;
       if (ex == E - 1) rows[E] = to;
     }
@@ -139,7 +139,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, i
   int before = 0;
   for (int e0 = 0; e0 < E; e0 += 64) {
     const int ex = e0 + lane;
-    const int from = min(ex < E ? offsets[ex] : P, P);
+    const int from = max(0, min(ex < E ? offsets[ex] : P, P));
     const int to = max(from, min(ex < E ? offsets[ex + 1] : P, P));
     const int n = (to - from + 15) / 16;
     int below = before, all = 0;

@@ -677,7 +677,7 @@ int lora_orthogonalize(const void* u, int u_dtype, int E, int r, int64_t n, int 
  *                 (dy quantised along N).
  * The bytes are the same on every run and device.  Alignment (else EINVAL): x 16 bytes
  * (transposed: its element), codes 16.  No output may be another array of the call.
- * E*R*K at most 2^41; transposed E <= 65535, R <= 2^22, K <= 2^31 (EOVERFLOW). */
+ * E*R*K at most 2^41; transposed E <= 65535, R <= 2^23, K <= 2^28 (EOVERFLOW). */
 int mxfp4_quantize(const void* x, int x_dtype, int64_t E, int64_t R, int64_t K, int transpose,
                    uint8_t* codes, uint8_t* scales, void* stream);
 /* out [R, K] of out_dtype (F32, BF16 or F16) = e2m1 value * 2^(scale - 127), rounded once (fp16:

@@ -95,6 +95,24 @@ def test_rows_of_experts(gpu_lib, name, N, K):
     check(run(gpu_lib, c, out_dtype=torch.float32), ref, mag, K)
 
 
+@pytest.mark.parametrize("E,picks", [(1000, [0, 63, 64, 65, 500, 999]), (1024, [1023]), (65, [64])])
+def test_few_rows_of_many_experts(gpu_lib, E, picks):
+    counts = np.zeros(E, dtype=int)
+    counts[picks] = np.arange(1, len(picks) + 1)
+    c = case(list(counts), 48, 96)
+    assert c["P"] <= 32
+    ref, mag = ref_of(c)
+    check(run(gpu_lib, c, out_dtype=torch.float32), ref, mag, 96)
+
+
+@pytest.mark.parametrize("counts", [[17, 0, 15], [16], [32], [1, 31], [0, 32, 0], [20, 12]])
+def test_several_tiles_of_few_rows(gpu_lib, counts):
+    for K in (96, 4096, 4128, 9216):
+        c = case(counts, 48, K, rows=11, k=3)
+        ref, mag = ref_of(c)
+        check(run(gpu_lib, c, out_dtype=torch.float32), ref, mag, K)
+
+
 @pytest.mark.parametrize("K", [32, 64, 96, 160, 224, 288, 480, 512, 544, 1056, 8192, 8224])
 @pytest.mark.parametrize("counts", [[5], [70, 3], [300]])
 def test_every_tail_of_k(gpu_lib, counts, K):

@@ -30,7 +30,8 @@ QUANT = dict(x=at(0), xd=1, E=2, R=64, K=96, tr=0, codes=at(1), scales=at(2), st
     (-1, dict(R=0)), (-1, dict(K=0)), (-1, dict(K=-32)), (-1, dict(tr=2)), (-1, dict(tr=-1)),
     (-5, dict(xd=3)), (-5, dict(xd=-1)), (-2, dict(K=48)), (-2, dict(tr=1, R=48)),
     (-7, dict(R=1 << 40)), (-7, dict(E=1 << 42)), (-7, dict(R=1 << 20, K=1 << 21)),
-    (-7, dict(tr=1, E=65536)), (-7, dict(tr=1, R=(1 << 22) + 32)),
+    (-7, dict(tr=1, E=65536)), (-7, dict(tr=1, R=(1 << 23) + 32)),
+    (-7, dict(tr=1, K=(1 << 28) + 1)),
     (-1, dict(x=at(0) + 8)), (-1, dict(codes=at(1) + 8)), (-1, dict(tr=1, x=at(0) + 1)),
     (-1, dict(tr=1, xd=0, x=at(0) + 2)), (-1, dict(codes=at(0))), (-1, dict(codes=at(2))),
     (-1, dict(scales=at(0)))])
