@@ -38,6 +38,26 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
   }
 }
 
+// The same in two parts, so that several reads are in flight before the first is used.
+template <int kT>
+struct Raw8 {
+  u32x4 w[kT == kF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const u32x4* q = reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(p) +
+                                                    i * (kT == kF32 ? 4 : 2));
+#pragma unroll
+    for (int j = 0; j < (kT == kF32 ? 2 : 1); ++j) w[j] = q[j];
+  }
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    if constexpr (kT == kF32) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j >> 2][j & 3]);
+    } else {
+      unpack8<kT == kBF16>(w[0], v);
+    }
+  }
+};
+
 __device__ __forceinline__ bool has_row(int32_t at, int64_t R) {
   return at >= 0 && at < R;
 }
@@ -77,61 +97,92 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(DispatchArgs g, int c
     const int32_t* pos = g.pos + t * g.k;
     for (int c = c0; c < c8; c += 256) {
       float y[8] = {};
-      for (int j = 0; j < g.k; ++j) {
-        const int32_t at = pos[j];
-        if (!has_row(at, g.R)) continue;
-        float v[8];
-        load8<kRows>(g.x, (int64_t)at * g.H + c * 8, v);
-        const float w = g.w ? g.w[t * g.k + j] : 1.f;
+      // four pairs' rows are read together; a pair without one reads row 0 and adds nothing
+      for (int j0 = 0; j0 < g.k && g.R > 0; j0 += 4) {
+        Raw8<kRows> v[4];
+        bool has[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] += w * v[i];
+        for (int j = 0; j < 4; ++j) {
+          const int32_t at = j0 + j < g.k ? pos[j0 + j] : -1;
+          has[j] = has_row(at, g.R);
+          v[j].load(g.x, (int64_t)(has[j] ? at : 0) * g.H + c * 8);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float w = g.w && has[j] ? g.w[t * g.k + j0 + j] : 1.f;
+          float f[8];
+          v[j].widen(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = has[j] ? y[i] + w * f[i] : y[i];
+        }
       }
       store8<kY>(g.out, t * g.H + c * 8, y);
     }
   }
 }
 
-// A workgroup takes one token; the pairs' products go eight pairs at a time.
-template <int kDy, int kRows, int kD>
+// kWaves waves of a workgroup take one token (one for rows of 512 columns or less: four tokens a
+// workgroup), eight pairs at a time: their rows are read together, a pair without one reads
+// row 0 and leaves nothing.
+template <int kDy, int kRows, int kD, int kWaves>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(DispatchArgs g, int c8) {
+  constexpr int kToks = 4 / kWaves;
   __shared__ float s_sum[4][8];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
+  for (int64_t t = (int64_t)blockIdx.x * kToks + wave / kWaves; t < g.T;
+       t += (int64_t)gridDim.x * kToks) {
     const int32_t* pos = g.pos + t * g.k;
     for (int j0 = 0; j0 < g.k; j0 += 8) {
       float sum[8] = {};
-      for (int c = threadIdx.x; c < c8; c += 256) {
-        float dy[8];
-        load8<kDy>(g.x, t * g.H + c * 8, dy);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int32_t at = j0 + j < g.k ? pos[j0 + j] : -1;
-          if (!has_row(at, g.R)) continue;
-          const int64_t i0 = (int64_t)at * g.H + c * 8;
-          float v[8];
-          load8<kRows>(g.rows, i0, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sum[j] += dy[i] * v[i];
-          if (g.out) {
-            const float w = g.w ? g.w[t * g.k + j0 + j] : 1.f;
-            float o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = w * dy[i];
-            store8<kD>(g.out, i0, o);
-          }
-        }
-      }
+      int32_t at[8];
+      float w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float s = wave_sum(sum[j]);
-        if (lane == 0) s_sum[wave][j] = s;
+        at[j] = j0 + j < g.k ? pos[j0 + j] : -1;
+        w[j] = g.w && j0 + j < g.k ? g.w[t * g.k + j0 + j] : 1.f;
       }
-      __syncthreads();
-      if (threadIdx.x < 8 && j0 + (int)threadIdx.x < g.k) {
-        const int j = threadIdx.x;
-        g.dw[t * g.k + j0 + j] = (s_sum[0][j] + s_sum[1][j]) + (s_sum[2][j] + s_sum[3][j]);
+      for (int c = threadIdx.x % (64 * kWaves); c < c8 && g.R > 0; c += 64 * kWaves) {
+        Raw8<kDy> d;
+        Raw8<kRows> v[8];
+        d.load(g.x, t * g.H + c * 8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j].load(g.rows, (int64_t)(has_row(at[j], g.R) ? at[j] : 0) * g.H + c * 8);
+        float dy[8];
+        d.widen(dy);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (!has_row(at[j], g.R)) continue;
+          float f[8], o[8];
+          v[j].widen(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            sum[j] += dy[i] * f[i];
+            o[i] = w[j] * dy[i];
+          }
+          if (g.out) store8<kD>(g.out, (int64_t)at[j] * g.H + c * 8, o);
+        }
       }
-      __syncthreads();
+      float* dw = g.dw + t * g.k + j0;
+      if constexpr (kWaves == 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float all = wave_sum(sum[j]);
+          if (lane == j && j0 + j < g.k) dw[j] = all;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float all = wave_sum(sum[j]);
+          if (lane == 0) s_sum[wave][j] = all;
+        }
+        __syncthreads();
+        if (threadIdx.x < 8 && j0 + (int)threadIdx.x < g.k) {
+          const int j = threadIdx.x;
+          dw[j] = (s_sum[0][j] + s_sum[1][j]) + (s_sum[2][j] + s_sum[3][j]);
+        }
+        __syncthreads();
+      }
     }
   }
 }
@@ -216,9 +267,16 @@ hipError_t launch_combine_rows(const DispatchArgs& g, hipStream_t s) {
 }
 
 hipError_t launch_combine_bwd(const DispatchArgs& g, hipStream_t s) {
-  const dim3 grid(groups(g.T));
-  NF4MOE_BY_TYPE(g.x_dtype, kX, NF4MOE_BY_TYPE(g.rows_dtype, kR, NF4MOE_BY_TYPE(g.out_dtype, kO,
-      hipLaunchKernelGGL((combine_bwd_kernel<kX, kR, kO>), grid, dim3(256), 0, s, g, g.H / 8))))
+  const int c8 = g.H / 8;
+  if (c8 <= 64) {
+    const dim3 grid(groups((g.T + 3) / 4));
+    NF4MOE_BY_TYPE(g.x_dtype, kX, NF4MOE_BY_TYPE(g.rows_dtype, kR, NF4MOE_BY_TYPE(g.out_dtype, kO,
+        hipLaunchKernelGGL((combine_bwd_kernel<kX, kR, kO, 1>), grid, dim3(256), 0, s, g, c8))))
+  } else {
+    const dim3 grid(groups(g.T));
+    NF4MOE_BY_TYPE(g.x_dtype, kX, NF4MOE_BY_TYPE(g.rows_dtype, kR, NF4MOE_BY_TYPE(g.out_dtype, kO,
+        hipLaunchKernelGGL((combine_bwd_kernel<kX, kR, kO, 4>), grid, dim3(256), 0, s, g, c8))))
+  }
   return hipGetLastError();
 }
 

@@ -49,7 +49,7 @@ def close(got, want, tol):
 
 
 SHAPES = [(1, 1, 8), (1, 8, 2048), (3, 2, 64), (16, 8, 2048), (33, 4, 2880), (200, 6, 136),
-          (5, 32, 1448), (2, 3, 16384), (7, 1, 24), (1000, 2, 8)]
+          (5, 32, 1448), (2, 3, 16384), (7, 1, 24), (1000, 2, 8), (21, 9, 512), (13, 17, 520), (6, 31, 504)]
 PAIRS = [(a, b) for a in TT for b in TT]
 
 
