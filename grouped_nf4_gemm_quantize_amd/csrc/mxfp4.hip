@@ -6,7 +6,8 @@
 // floor(log2) is the exponent field of the largest magnitude; the division by a
 // power of two is exact and the conversion instructions do it and the rounding.
 //
-// Bound by memory: 2.53 bytes an element for bf16 one way, and the same back.
+// Bound by memory: 2.53 bytes an element for bf16 one way, and the same back.  Measured, 16 x 2048
+// x 2048 bf16: along the rows 29.3 us = 5.8 TB/s, along the columns 31.5-35 us, back 27 us.
 
 #include <algorithm>
 
