@@ -204,6 +204,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs g) {
       if (id < 0 || id >= g.E) id = -1;
       if (id >= 0) dw = g.dw[t * g.k + lane];
     }
+    const bool any = __ballot(id >= 0) != 0;
     const float mine = id >= 0 ? l[id] : -INFINITY;
     float top = mine, all = 0.f;
     if constexpr (!kRenorm) {
@@ -228,7 +229,8 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs g) {
         if (ij == e) v += gj;
       }
       if (e < g.E) {
-        if constexpr (!kRenorm) v = expf(l[e] - top) / all * (v - mean);
+        // without a choice nothing was weighted, whatever the logits are (all -inf: p is NaN)
+        if constexpr (!kRenorm) v = any ? expf(l[e] - top) / all * (v - mean) : 0.f;
         g.dlogits[t * g.E + e] = v;
       }
     }

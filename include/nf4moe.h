@@ -765,7 +765,8 @@ int moe_combine_backward(const void* dy, int dy_dtype, const void* rows, int row
  *                   p[id_j] dw_j), g_e = dw_j where id_j = e, else 0.
  * The choice of the experts has no gradient.  logits and dlogits fp32 [T, E], topk_ids int32
  * [T, k] (one outside [0, E) takes no part: as if dw were 0 and, renormalised, its logit -inf);
- * a chosen expert's logit must be finite, others may be -inf.  dlogits is no input (EINVAL);
+ * a chosen expert's logit must be finite, others may be -inf.  A token without a choice gets 0
+ * whatever its logits are.  dlogits is no input (EINVAL);
  * sizes as for moe_route_permute, everything 4-byte aligned.  One launch, no workspace. */
 int moe_route_backward(const float* logits, const int32_t* topk_ids, const float* dw, int64_t T,
                        int E, int k, int renormalize, float* dlogits, void* stream);

@@ -209,6 +209,25 @@ def test_router_gradient_of_masked_experts(gpu_lib):
         assert np.abs(got[t] - want[0]).max() <= 2.0 ** -19 * np.abs(dw).max()
 
 
+@pytest.mark.parametrize("fill", [-np.inf, np.nan, np.inf, 1.0])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_router_gradient_of_tokens_without_a_choice(gpu_lib, renorm, fill):
+    """Padded tokens (no choice in [0, E)) get 0, whatever their logits and dw hold."""
+    T, E, k = 9, 80, 4
+    rng = np.random.default_rng(2)
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    ids = np.argsort(-logits, 1)[:, :k].astype(np.int32)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    none = [1, 4, 8]
+    ids[none], logits[none], dw[none] = (-1, E, -7, 2 ** 31 - 1), fill, np.nan
+    d = lambda a: torch.from_numpy(a).to(DEV)  # noqa: E731
+    got = host(gpu_lib.moe_route_backward(d(logits), d(ids), d(dw), renormalize=renorm))
+    assert (got[none] == 0).all()
+    rest = np.setdiff1d(np.arange(T), none)
+    want = dispatch.route_backward(logits[rest], ids[rest], dw[rest], renorm)
+    assert np.abs(got[rest] - want).max() <= 2.0 ** -19 * np.abs(dw[rest]).max()
+
+
 def test_captured_and_replayed(gpu_lib):
     c = make(50, 4, 264, drop=0.1)
     out = torch.zeros(c["R"], c["H"], device=DEV)
