@@ -1722,6 +1722,9 @@ int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_
   // tile's rows behind the end
   if (a_rows + kMxTileRows > kMxMaxBytes / (K / 2) || N + kMxTileRows > kMxMaxBytes / (K / 2))
     return fail(NF4MOE_EOVERFLOW, "the activations' codes or one expert's exceed 3.5 GiB");
+  // tiles (64 x 128 at the smallest) are counted in 32 bits
+  if (P / 64 + 1 + E > INT32_MAX / ((N + 127) / 128))
+    return fail(NF4MOE_EOVERFLOW, "P * N is too large (%lld x %lld)", (long long)P, (long long)N);
   if (P == 0) return ok();
   if (a == nullptr || blocks == nullptr || scales == nullptr || expert_offsets == nullptr ||
       out == nullptr || a_rows == 0 || out_rows == 0)

@@ -714,8 +714,8 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t R, int
  * Scale byte 255 on either side makes what it multiplies NaN: its row, or its column for the
  * expert's rows.  The order of the sums depends on the sizes only: results are the same from
  * call to call.  P = 0 does nothing.  Alignment (else EINVAL): a, blocks and out 16 bytes,
- * scales 1, the others 4.  P below 2^30; the codes of a, and of one expert, with 512 rows more
- * at most 3.5 GiB (EOVERFLOW).
+ * scales 1, the others 4.  P below 2^30; (P / 64 + 1 + E) * ceil(N / 128) below 2^31; the codes
+ * of a, and of one expert, with 512 rows more at most 3.5 GiB (EOVERFLOW).
  * The query gives 0 for invalid arguments too. */
 #define NF4MOE_MXFP4 3 /* a_dtype of grouped_mx4_gemm only */
 size_t grouped_mx4_gemm_workspace(int64_t a_rows, int a_dtype, int E, int64_t P, int64_t N,

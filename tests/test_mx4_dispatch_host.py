@@ -73,6 +73,13 @@ def test_product_refuses(lib, status, changes):
     refuse(lib, status, lib.grouped_mx4_gemm, GEMM, changes)
 
 
+@pytest.mark.parametrize("changes", [dict(P=(1 << 30) - 1, N=1 << 22), dict(P=1 << 24, N=1 << 23, K=32, E=1),
+                                     dict(P=1 << 27, N=1 << 17, epi=1)])
+def test_product_tiles_are_counted_in_32_bits(lib, changes):
+    """Many rows scattered into few places: every array is small, the tiles are not."""
+    refuse(lib, -7, lib.grouped_mx4_gemm, GEMM, changes)
+
+
 @pytest.mark.parametrize("other", ["a", "sa", "gather", "blocks", "scales", "off", "rs", "scatter"])
 def test_product_output_is_no_input(lib, other):
     refuse(lib, -1, lib.grouped_mx4_gemm, GEMM, dict(out=GEMM[other]))
