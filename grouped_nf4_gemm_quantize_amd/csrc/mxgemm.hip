@@ -869,15 +869,28 @@ bool mx_gemm_small(int E, int64_t P, int64_t N, bool swiglu) {
   return P <= kSmallRows && small_tiles(E, P, N, swiglu) <= 1536;
 }
 
-// 256-row tiles from 80 rows an expert on.  Measured, 64 against 256 (us, 64 experts of 2048 x 2048):
-// 32 rows each 28.6 and 33.2, 64 rows 32.3 and 40.7, 96 rows 43.8 and 36.6, 128 rows 46.6 and 37.6.
+// 256-row tiles from 80 rows an expert on, where 64-row ones are more than one round of the card's
+// places (an expert's last tile counted half).  Measured, 64 against 256 (us):
+//   64 experts of 2048 x 2048: 32 rows each 28.6 and 33.2, 64 rows 32.3 and 40.7, 96 rows 43.8
+//   and 36.6, 128 rows 46.6 and 37.6;
+//   one round: 1024 rows of one 2048 x 2048 12.7 and 19.1, of one 4096 x 4096 23.7 and 31.5, 512 of
+//   8192 x 8192 37.9 and 55.3, 128 of 28672 x 4096 23.8 and 29.3, 1536 on 8 experts 16.3 and 24.3;
+//   a little more: 1088 rows of one 4096 x 4096 34.9 and 32.2, 576 of 8192 x 8192 67.9 and 53.5,
+//   2048 on 16 experts of 2048 x 2048 25.5 and 22.1; the other way round, 8 experts of 256 rows each
+//   (512 tiles, counted as 576) 14.3 and 23.7.
+static bool mx_gemm_wide(const MxGemmArgs& g, int num_cus) {
+  const int64_t hit = std::min<int64_t>(g.E, g.P);
+  if (g.P / hit < 80) return false;
+  return ((g.P + 63) / 64 + hit / 2) * ((g.N + 127) / 128) > (int64_t)num_cus * Tile64::PER_CU;
+}
+
 hipError_t launch_mx_gemm(const MxGemmArgs& g, int num_cus, hipStream_t s) {
   if (mx_gemm_small(g.E, g.P, g.N, g.swiglu)) {
     const int n_tiles = small_n_tiles(g.N, g.swiglu);
     const dim3 grid((unsigned)small_tiles(g.E, g.P, g.N, g.swiglu));
     if (g.swiglu) launch_small<true>(g, grid, n_tiles, s);
     else launch_small<false>(g, grid, n_tiles, s);
-  } else if (g.P / std::min<int64_t>(g.E, g.P) >= 80) {
+  } else if (mx_gemm_wide(g, num_cus)) {
     launch_tiles<Tile256>(g, num_cus, s);
   } else {
     launch_tiles<Tile64>(g, num_cus, s);
