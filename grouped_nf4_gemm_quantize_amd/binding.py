@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnf4moe.s
 
 F32, BF16, F16 = 0, 1, 2
 MXFP4 = 3  # NF4MOE_MXFP4, activations of grouped_gemm_mx4
+ZERO_REST = 0x100  # NF4MOE_ZERO_REST, added to the type of moe_combine_backward's drows
 NOALLOC_SCRATCH_BYTES = 32 << 20  # NF4MOE_NOALLOC_SCRATCH_BYTES
 EPI_NONE, EPI_SWIGLU, EPI_SWIGLU_BWD = 0, 1, 2
 
@@ -940,25 +941,30 @@ def moe_combine(rows, pair_pos, k: int, w=None, y=None, y_dtype=None):
 def moe_combine_backward(dy, rows, pair_pos, k: int, w=None, drows=None, drows_dtype=None,
                          need_drows: bool = True):
     """Gradients of ``moe_combine`` (see moe_combine_backward in include/nf4moe.h): returns
-    ``(drows, dw)``, dw fp32 [T, k].  ``drows`` may be ``rows``; without ``need_drows`` it is
-    not computed (None)."""
+    ``(drows, dw)``, dw fp32 [T, k].  Without ``need_drows`` drows is not computed (None).
+
+    Rows that no pair names have gradient 0 in the drows that is made here.  In a ``drows`` of
+    the caller's they keep what it held: with ``rows`` itself, which it may be, their values.
+    """
     torch = _torch()
     if dy.dim() != 2 or rows.dim() != 2:
         raise ValueError("dy must be [T, H] and rows [R, H]")
     dev = dy.device
     T, H = dy.shape
     R = rows.shape[0]
+    rest = 0
     if not need_drows:
         drows = None
     elif drows is None:
         drows = torch.empty((R, H), dtype=drows_dtype or rows.dtype, device=dev)
+        rest = ZERO_REST
     dw = torch.empty((T, k), dtype=torch.float32, device=dev)
     _call(dev, load().moe_combine_backward, _ptr(dy), _dtype_code(dy.dtype),
           _need(rows, "rows", dev, (R, H)), _dtype_code(rows.dtype),
           _pairs(pair_pos, "pair_pos", dev, T, k, torch.int32),
           None if w is None else _pairs(w, "w", dev, T, k, torch.float32), T, k, R, H,
           None if drows is None else _need(drows, "drows", dev, (R, H)),
-          F32 if drows is None else _dtype_code(drows.dtype), dw.data_ptr())
+          F32 if drows is None else _dtype_code(drows.dtype) | rest, dw.data_ptr())
     return drows, dw
 
 

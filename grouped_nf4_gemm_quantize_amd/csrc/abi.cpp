@@ -1865,11 +1865,15 @@ int moe_combine_backward(const void* dy, int dy_dtype, const void* rows, int row
   if (st != NF4MOE_OK) return st;
   if (dy == nullptr || (rows == nullptr && R > 0) || pair_pos == nullptr || dw == nullptr)
     return fail(NF4MOE_EINVAL, "dy, rows, pair_pos and dw must be non-null");
+  const bool zero_rest = drows_dtype >= 0 && (drows_dtype & NF4MOE_ZERO_REST) != 0;
+  if (zero_rest) drows_dtype &= ~NF4MOE_ZERO_REST;
   if (!is_float_dtype(dy_dtype) || !is_float_dtype(rows_dtype) || !is_float_dtype(drows_dtype))
     return fail(NF4MOE_EDTYPE, "unknown dtype (dy %d, rows %d, drows %d)", dy_dtype, rows_dtype,
                 drows_dtype);
   if (is_any(drows, {dy, pair_pos, w, dw}) || (is_any(drows, {rows}) && drows_dtype != rows_dtype))
     return fail(NF4MOE_EINVAL, "drows may be rows of the same type, and no other array of the call");
+  if (zero_rest && is_any(drows, {rows}))
+    return fail(NF4MOE_EINVAL, "with NF4MOE_ZERO_REST drows must not be rows");
   if (is_any(dw, {dy, rows, pair_pos, w}))
     return fail(NF4MOE_EINVAL, "dw must not be one of the inputs");
   if (!aligned(dy, 16) || !aligned(rows, 16) || !aligned(drows, 16) || !aligned(pair_pos, 4) ||
@@ -1890,6 +1894,7 @@ int moe_combine_backward(const void* dy, int dy_dtype, const void* rows, int row
   a.x_dtype = dy_dtype;
   a.rows_dtype = rows_dtype;
   a.out_dtype = drows_dtype;
+  a.clear = zero_rest;
   hipError_t err = launch_combine_bwd(a, (hipStream_t)stream);
   if (err != hipSuccess) return hip_fail(err, "combine backward launch");
   return ok();
