@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnf4moe.s
 
 F32, BF16, F16 = 0, 1, 2
 MXFP4 = 3  # NF4MOE_MXFP4, activations of grouped_gemm_mx4
-ZERO_REST = 0x100  # NF4MOE_ZERO_REST, added to the type of moe_combine_backward's drows
+ZERO_REST = 0x100  # NF4MOE_ZERO_REST, added to a type: rows that no pair names become 0
 NOALLOC_SCRATCH_BYTES = 32 << 20  # NF4MOE_NOALLOC_SCRATCH_BYTES
 EPI_NONE, EPI_SWIGLU, EPI_SWIGLU_BWD = 0, 1, 2
 
@@ -902,21 +902,23 @@ def moe_dispatch(x, pair_pos, k: int, w=None, rows: Optional[int] = None, out=No
 
     ``pair_pos`` is int32 [T*k] or [T, k] (``route_permute``'s, or any placement; entries
     outside [0, rows) are dropped), ``w`` fp32 of as many or None.  ``rows`` defaults to
-    T*k.  Rows that no pair names keep what ``out`` held.
+    T*k.  Rows that no pair names are 0, in an ``out`` of the caller's what it held.
     """
     torch = _torch()
     if x.dim() != 2:
         raise ValueError("x must be [T, H]")
     dev = x.device
     T, H = x.shape
+    rest = 0
     if out is None:
+        rest = ZERO_REST
         out = torch.empty((T * k if rows is None else rows, H), dtype=out_dtype or x.dtype,
                           device=dev)
     R = out.shape[0]
     _call(dev, load().moe_dispatch, _ptr(x), _dtype_code(x.dtype),
           _pairs(pair_pos, "pair_pos", dev, T, k, torch.int32),
           None if w is None else _pairs(w, "w", dev, T, k, torch.float32), T, k, R, H,
-          _need(out, "out", dev, (R, H)), _dtype_code(out.dtype))
+          _need(out, "out", dev, (R, H)), _dtype_code(out.dtype) | rest)
     return out
 
 

@@ -1801,12 +1801,20 @@ static int dispatch_shape_check(int64_t T, int k, int64_t R, int64_t H) {
   return NF4MOE_OK;
 }
 
+// Takes NF4MOE_ZERO_REST off a type; whether it was there.
+static bool take_zero_rest(int* dtype) {
+  if (*dtype < 0 || !(*dtype & NF4MOE_ZERO_REST)) return false;
+  *dtype &= ~NF4MOE_ZERO_REST;
+  return true;
+}
+
 int moe_dispatch(const void* x, int x_dtype, const int32_t* pair_pos, const float* w, int64_t T,
                  int k, int64_t R, int64_t H, void* rows, int rows_dtype, void* stream) {
   int st = dispatch_shape_check(T, k, R, H);
   if (st != NF4MOE_OK) return st;
   if (x == nullptr || pair_pos == nullptr || (rows == nullptr && R > 0))
     return fail(NF4MOE_EINVAL, "x, pair_pos and rows must be non-null");
+  const bool zero_rest = take_zero_rest(&rows_dtype);
   if (!is_float_dtype(x_dtype) || !is_float_dtype(rows_dtype))
     return fail(NF4MOE_EDTYPE, "unknown dtype (x %d, rows %d)", x_dtype, rows_dtype);
   if (is_any(rows, {x, pair_pos, w}))
@@ -1825,6 +1833,7 @@ int moe_dispatch(const void* x, int x_dtype, const int32_t* pair_pos, const floa
   a.H = (int)H;
   a.x_dtype = x_dtype;
   a.out_dtype = rows_dtype;
+  a.clear = zero_rest;
   hipError_t err = launch_dispatch(a, (hipStream_t)stream);
   if (err != hipSuccess) return hip_fail(err, "dispatch launch");
   return ok();
@@ -1865,8 +1874,7 @@ int moe_combine_backward(const void* dy, int dy_dtype, const void* rows, int row
   if (st != NF4MOE_OK) return st;
   if (dy == nullptr || (rows == nullptr && R > 0) || pair_pos == nullptr || dw == nullptr)
     return fail(NF4MOE_EINVAL, "dy, rows, pair_pos and dw must be non-null");
-  const bool zero_rest = drows_dtype >= 0 && (drows_dtype & NF4MOE_ZERO_REST) != 0;
-  if (zero_rest) drows_dtype &= ~NF4MOE_ZERO_REST;
+  const bool zero_rest = take_zero_rest(&drows_dtype);
   if (!is_float_dtype(dy_dtype) || !is_float_dtype(rows_dtype) || !is_float_dtype(drows_dtype))
     return fail(NF4MOE_EDTYPE, "unknown dtype (dy %d, rows %d, drows %d)", dy_dtype, rows_dtype,
                 drows_dtype);

@@ -68,9 +68,9 @@ __device__ __forceinline__ bool has_row(int32_t at, int64_t R) {
 
 // Rows that no pair names become 0: the first g.clear workgroups of a launch do that beside the
 // others, each for a run of rows, with a bit a row in LDS set from all positions.  The rows are
-// other ones than the pairs' own, so nothing is waited for.  Combine's gradient of 4096 tokens, k 8,
-// 2048 columns fp16 takes 51.2 us with it and 49.9 without; with a launch that clears all rows before
-// 66.9.
+// other ones than the pairs' own, so nothing is waited for.  4096 tokens, k 8, 2048 columns fp16:
+// dispatch 25.3 us with it and 25.0 without, 42.9 with a launch that clears all rows before; combine's
+// gradient 51.2, 49.9 and 66.9.
 constexpr int kClearGroups = 128;
 constexpr int kClearRows = 1 << 16;  // of a workgroup, at most
 
@@ -121,10 +121,15 @@ __global__ __launch_bounds__(256) void clear_kernel(u32x4* out, int64_t n) {
 // A workgroup takes `toks` tokens (one if a row has 256 chunks of eight or more).
 template <int kX, int kRows>
 __global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs g, int c8, int toks) {
+  if ((int)blockIdx.x < g.clear) {
+    clear_unnamed(g, kRows == kF32 ? 2 * c8 : c8);
+    return;
+  }
+  const int group = blockIdx.x - g.clear, all = gridDim.x - g.clear;
   const int tl = c8 < 256 ? threadIdx.x / c8 : 0;
   const int c0 = threadIdx.x - tl * c8;
   if (tl >= toks) return;
-  for (int64_t t = (int64_t)blockIdx.x * toks + tl; t < g.T; t += (int64_t)gridDim.x * toks) {
+  for (int64_t t = (int64_t)group * toks + tl; t < g.T; t += (int64_t)all * toks) {
     const int32_t* pos = g.pos + t * g.k;
     for (int c = c0; c < c8; c += 256) {
       float v[8];
@@ -310,15 +315,15 @@ unsigned groups(int64_t n) { return (unsigned)std::min<int64_t>(n, 1 << 22); }
 
 // Where g.clear asks for rows without a pair to be cleared: how many workgroups do it, or 0 after a
 // launch that has cleared all rows, if they are so short that this is cheaper, or too many.  By
-// the bytes of the rows for a pair, combine's gradient with workgroups against a launch before (us): 256,
-// of 524288 pairs 147 and 126, of 1048576 345 and 352; 512, 169 and 180, 406 and 435; 1024, 254 and 330.
+// the bytes of the rows for a pair, with workgroups against a launch before, 524288 pairs (us): 512,
+// dispatch 154 and 97, combine's gradient 169 and 180; 1024, 192 and 209, 254 and 330.
 hipError_t clear_groups(DispatchArgs& g, hipStream_t s) {
   const int64_t row_bytes = (int64_t)g.H * (g.out_dtype == kF32 ? 4 : 2);
   if (!g.clear) return hipSuccess;
   g.clear = 0;
   if (g.out == nullptr || g.R == 0) return hipSuccess;
   const int n = (int)std::min<int64_t>(kClearGroups, (g.R + 63) / 64);
-  if (g.R <= (int64_t)n * kClearRows && g.R * row_bytes >= 512 * g.T * g.k) {
+  if (g.R <= (int64_t)n * kClearRows && g.R * row_bytes >= 1024 * g.T * g.k) {
     g.clear = n;
     return hipSuccess;
   }
@@ -330,9 +335,11 @@ hipError_t clear_groups(DispatchArgs& g, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_dispatch(const DispatchArgs& g, hipStream_t s) {
+hipError_t launch_dispatch(DispatchArgs g, hipStream_t s) {
+  const hipError_t err = clear_groups(g, s);
+  if (err != hipSuccess) return err;
   const int c8 = g.H / 8, toks = c8 < 256 ? 256 / c8 : 1;
-  const dim3 grid(groups((g.T + toks - 1) / toks));
+  const dim3 grid(g.clear + groups((g.T + toks - 1) / toks));
   NF4MOE_BY_TYPE(g.x_dtype, kX, NF4MOE_BY_TYPE(g.out_dtype, kO,
       hipLaunchKernelGGL((dispatch_kernel<kX, kO>), grid, dim3(256), 0, s, g, c8, toks)))
   return hipGetLastError();

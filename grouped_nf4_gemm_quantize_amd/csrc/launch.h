@@ -280,9 +280,9 @@ struct DispatchArgs {
   int64_t T, R;         // tokens, expert rows
   int k, H;
   int x_dtype, rows_dtype, out_dtype;
-  int clear;            // backward: whether rows that no pair names become 0
+  int clear;            // dispatch, backward: whether rows that no pair names become 0
 };
-hipError_t launch_dispatch(const DispatchArgs& g, hipStream_t s);
+hipError_t launch_dispatch(DispatchArgs g, hipStream_t s);
 hipError_t launch_combine_rows(const DispatchArgs& g, hipStream_t s);
 hipError_t launch_combine_bwd(DispatchArgs g, hipStream_t s);
 

@@ -732,8 +732,9 @@ int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_
  * pair p = t*k + j of token t has its row at pair_pos[p] (moe_route_permute's pair_pos, or any
  * other placement: rows padded to tiles, pairs dropped over a capacity).  An entry outside
  * [0, R) has no row: it is not dispatched, adds nothing to y and has dw = 0.  Rows that no pair
- * names are left as they were, or set to 0 where drows_dtype has NF4MOE_ZERO_REST: their gradient
- * (rows padded to tiles, or of dropped pairs, then add nothing to a sum over the rows).
+ * names are left as they were, or set to 0 where the type of moe_dispatch's rows or of drows has
+ * NF4MOE_ZERO_REST: what they hold otherwise (no gradient, NaNs of other uses of the memory) gets
+ * into sums over an expert's rows.
  *   moe_dispatch           rows[pair_pos[p]] = w[p] * x[t]
  *   moe_combine            y[t] = sum_j w[p] * rows[pair_pos[p]], j ascending
  *   moe_combine_backward   drows[pair_pos[p]] = w[p] * dy[t];  dw[p] = <dy[t], rows[pair_pos[p]]>
@@ -751,7 +752,7 @@ int grouped_mx4_gemm(const void* a, int a_dtype, const uint8_t* a_scales, int64_
  * launch (two to zero very short or very many rows), the same results from call to call.  Matrices 16-byte aligned, pair_pos, w and dw 4;
  * no output may be another array of the call but drows = rows (EINVAL for equal pointers).
  * T*k and R up to 2^31 - 1 (EOVERFLOW). */
-#define NF4MOE_ZERO_REST 0x100 /* added to drows_dtype: rows that no pair names become 0 */
+#define NF4MOE_ZERO_REST 0x100 /* added to a type: rows that no pair names become 0 */
 int moe_dispatch(const void* x, int x_dtype, const int32_t* pair_pos, const float* w, int64_t T,
                  int k, int64_t R, int64_t H, void* rows, int rows_dtype, void* stream);
 int moe_combine(const void* rows, int rows_dtype, const int32_t* pair_pos, const float* w,
