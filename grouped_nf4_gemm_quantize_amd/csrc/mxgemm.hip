@@ -311,6 +311,7 @@ struct Tile {
   static constexpr int A_DMA = BM / 8 / WAVES, B_DMA = BN / 8 / WAVES;  // copies of 8 rows a wave
   static constexpr int S_GROUPS = (BM + BN) / 64;  // of 64 rows' scales, a copy each
   static constexpr int S_DMA = (S_GROUPS + WAVES - 1) / WAVES;  // a wave (the last group's twice)
+  static_assert(MT <= 2, "a wave has all, one or none of its row tiles");
   static_assert(BM % (8 * WAVES) == 0 && BM % 64 == 0, "whole copies a wave");
   static_assert(32 % (B_DMA * 8) == 0, "a wave copies rows of one group of 32 weight rows");
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;  // 256 codes of a row
@@ -671,7 +672,7 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
   const int G = gridDim.x;  // a multiple of 8
   const int u = (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3);
   if (u >= total) return;
-  // Tiles r .. r + 63 of this workgroup: groups of four row tiles, the row tile changing fastest.
+  // Tiles r .. r + kDescs - 1 of this workgroup: groups of four row tiles, the row tile changing fastest.
   auto look_up = [&](int r) {
     const int64_t t = (int64_t)(r + tid) * G + u;
     if (tid < kDescs && t < total) {
@@ -790,7 +791,6 @@ __global__ __launch_bounds__(T::THREADS, T::PER_CU) void mx_tile_kernel(MxGemmAr
         store_tile<T, M, kSwiglu, kOut>(g, cur, orow[par], rscale[par], wm, wn, n32, g2, acc);
     };
     if (mtv > T::MT / 2) tile(Const<T::MT>{});
-    else if (T::MT > 2 && mtv == 2) tile(Const<T::MT / 2>{});
     else if (mtv == 1) tile(Const<1>{});
     else tile(Const<0>{});
     if (!more) break;
