@@ -849,7 +849,8 @@ def grouped_gemm_mx4(a, a_scales, blocks, scales, offsets, P: int, gather=None,
     ``a``, ``a_scales`` are what ``quantize_mxfp4`` returns for the activation rows, or ``a`` is
     the rows themselves, [rows, K] fp32, bf16 or fp16, with ``a_scales`` None: quantised by the
     call.  ``blocks`` [E, N, K/2] and ``scales`` [E, N, K/32] are the stack.  ``out`` is
-    [out_rows (P), N or N/2], bf16 by default.
+    [out_rows (P), N or N/2], bf16 by default; rows of it that are no expert's, or that
+    ``scatter`` does not name, are not written (in an ``out`` made here they hold anything).
     """
     torch = _torch()
     dev = a.device

@@ -10,9 +10,9 @@
 //
 // All go by token, so that a token's row is read (or written) once for its k pairs; sums over a
 // token's columns stay in one workgroup and have one order.  Bound by memory.  Measured, 4096
-// tokens of 2048 columns, k 8, bf16 tokens and fp16 rows: dispatch 24 us alone = 6.3 TB/s (most of
-// it writes), combine 27 us = 5.6 TB/s, its gradient 50 us = 5.7 TB/s and the router's 4.8 us (a
-// launch and reads in turn).  With one row's read at a time combine took 34 us in a row of calls,
+// tokens of 2048 columns, k 8, bf16 tokens and fp16 rows: dispatch 24-25 us alone = 6.0-6.3 TB/s (most of
+// it writes), combine 27-28 us = 5.4-5.6 TB/s, its gradient 50-52 us = 5.5-5.7 TB/s and the router's
+// 4.1-4.8 us (a launch and reads in turn).  With one row's read at a time combine took 34 us in a row of calls,
 // with several 31.
 
 #include <algorithm>

@@ -7,7 +7,8 @@
 // power of two is exact and the conversion instructions do it and the rounding.
 //
 // Bound by memory: 2.53 bytes an element for bf16 one way, and the same back.  Measured, 16 x 2048
-// x 2048 bf16: along the rows 29.3 us = 5.8 TB/s, along the columns 31.5-35 us, back 27 us.
+// x 2048 bf16, between other calls: along the rows 26-30 us = 5.7-6.5 TB/s, along the columns 35 us
+// (25 on the same input again, part of which is in the cache behind the L2s), back 26-27 us.
 
 #include <algorithm>
 
@@ -47,7 +48,8 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* x, int64_t
 // Blocks along the columns of [R, K]: a lane takes 32 rows of one column, or of two neighbours as
 // they lie in a word (16-bit values, K even).  A workgroup's eight waves have row blocks beside each
 // other: their codes, 128 bytes of a column, and scales go through LDS and leave as whole
-// lines (16 x 2048 x 2048 bf16: 31.5 us; 46.5 us with a lane's 16 bytes and scale byte stored as they are).
+// lines (16 x 2048 x 2048 bf16, both in one run: 31.5 us; 46.5 with a lane's 16 bytes and scale byte stored
+// as they are).
 constexpr int kColWaves = 8;
 
 template <int kT, int kCols>

@@ -13,9 +13,9 @@
 // Three ways, by the rows an expert has (rules and both sides' figures at the launchers): 16-row
 // tiles of one launch that makes the rows' blocks too; 64 x 128 tiles, which stream the weights at
 // the rate of a large copy; 256 x 256 tiles.  Measured (kernels alone, blocks of the rows made before
-// but for the first): one token, 8 of 64 experts, gate and up of H 2048 I 1024 7.4 us; 64 tokens
-// 28.9 us = 4.97 TB/s; 4096 tokens 102-114 us = 2.4-2.7 PFLOP/s; one 8192 x 8192 matrix, 8192
-// rows 262 us = 4.2 PFLOP/s (a 16-bit library product of the size reaches 1.43).
+// but for the first): one token, 8 of 64 experts, gate and up of H 2048 I 1024 7.3-8.0 us; 64 tokens
+// 28.9 us = 4.97 TB/s; 4096 tokens 101-103 us = 2.7 PFLOP/s; one 8192 x 8192 matrix, 8192
+// rows 261-268 us = 4.1-4.2 PFLOP/s (a 16-bit library product of the size reaches 1.43).
 
 #include <algorithm>
 
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(kThreads) void mx_small_kernel(MxGemmArgs g, int n_
 // ---- many rows: tiles through LDS ---------------------------------------------------
 //
 // 256 x 256 (144 KB of LDS) because the copies bound it: a step of 256 of K brings 64 KB of codes
-// from the L2 to a compute unit for 2048 cycles of matrix instructions.  8192^3 takes 265 us; with
+// from the L2 to a compute unit for 2048 cycles of matrix instructions.  8192^3 takes 261-268 us; with
 // copies that hit the first-level cache 205, without any copy 169.  Waiting for the copies is not
 // what they cost (without the waits nothing is gained): the L2s deliver 12 TB/s then, at 1.9 GHz,
 // with the matrix units busy 49 % of the time.  Four waves of 128 x 128 each were slower than eight
